@@ -28,6 +28,9 @@ GEMM_SCRATCH_BYTES = 512 * 1024   # PESTI_GEMM_SCRATCH_BYTES
 
 FORMAT_IDS = {"q8_0": 0, "q4_k": 1, "q6_k": 2, "i8row": 3, "q5_k": 4, "q2_k": 5, "q3_k": 6, "i4row": 7,
               "q4_k_stream": 8}
+# formats of the values of X and Y where a call takes them, and of the expert GEMMs' matrices
+VALUE_FORMAT_IDS = {"f32": 17, "f16": 16}
+EXPERT_FORMAT_IDS = {"f16": 16, "i8row": 3}
 # formats of the small-M GEMM calls that take a format id
 GEMM_FORMAT_IDS = {"f16": 16, "q8_0": 0, "q2_k": 5, "q3_k": 6, "q4_k": 1, "q5_k": 4, "q6_k": 2}
 
@@ -56,6 +59,12 @@ _SIGNATURES = {
     "pesti_gemm_workspace_bytes": (_i64, [_i32, _i64, _i64, _i64]),
     "pesti_gemm_smallm_ws": (_c_int, [_i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
     "pesti_gemm_smallm_noalloc": (_c_int, [_i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "pesti_quant_i8token": (_c_int, [_i32, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "pesti_gemm_i8row_i8token": (_c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp]),
+    "pesti_gemm_experts": (_c_int, [_i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp,
+                                    _vp]),
+    "pesti_gemm_experts_swiglu": (_c_int, [_i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp,
+                                           _i32, _vp, _vp]),
     "pesti_dequant_q8_0": (_c_int, [_i64, _i64, _vp, _vp, _vp]),
     "pesti_dequant_q4_k": (_c_int, [_i64, _i64, _vp, _vp, _vp]),
     "pesti_dequant_q4_k_stream": (_c_int, [_i64, _i64, _vp, _vp, _vp]),
@@ -270,6 +279,90 @@ def pesti_gemm_smallm_noalloc(fmt, m, out_features, in_features, w, x, y, bias=N
     calls that overlap on one GPU race)."""
     return _check("pesti_gemm_smallm_noalloc", load().pesti_gemm_smallm_noalloc(
         _gemm_fid(fmt), m, out_features, in_features, _ptr(w), _ptr(x), _ptr(y), _ptr(bias), _stream(stream)))
+
+
+# --- 8-bit linear layer, expert-grouped products ------------------------------
+def _sized(obj, nbytes, what, dtype=None):
+    """_ptr of an argument, with a tensor's size, element type and device
+    checked too: these calls take several arrays of related sizes."""
+    if not hasattr(obj, "data_ptr"):
+        return _ptr(obj)
+    import torch
+    p = _ptr(obj)
+    if dtype is not None and obj.dtype != getattr(torch, dtype):
+        raise ValueError(f"{what} must be a {dtype} tensor, got {obj.dtype}")
+    if obj.numel() * obj.element_size() < nbytes:
+        raise ValueError(f"{what} holds {obj.numel() * obj.element_size()} bytes, the call needs {nbytes}")
+    if obj.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {obj.device}, not on the current device")
+    return p
+
+
+def _value_format(fmt, obj, what):
+    """(PESTI_FMT_* id, bytes per value) of X or Y: as given, else by the tensor's type."""
+    if fmt is None:
+        kind = str(getattr(obj, "dtype", None))
+        fmt = {"torch.float32": "f32", "torch.float16": "f16"}.get(kind)
+        if fmt is None:
+            raise ValueError(f"{what}: give its format, or a float32 or float16 tensor (got {kind})")
+    fid = VALUE_FORMAT_IDS[fmt] if isinstance(fmt, str) else int(fmt)
+    return fid, 4 if fid == VALUE_FORMAT_IDS["f32"] else 2
+
+
+def pesti_quant_i8token(x_format, m, in_features, x, codes, scales, stream=None):
+    """Rows of X ("f32" or "f16") to int8 codes and a float32 scale per row."""
+    fid, size = _value_format(x_format, x, "x")
+    return _check("pesti_quant_i8token", load().pesti_quant_i8token(
+        fid, m, in_features, _sized(x, m * in_features * size, "x"), _sized(codes, m * in_features, "codes"),
+        _sized(scales, 4 * m, "scales", "float32"), _stream(stream)))
+
+
+def pesti_gemm_i8row_i8token(m, out_features, in_features, codes, row_scales, x_codes, x_scales, y, bias=None,
+                             y_format=None, stream=None):
+    """Y = (x_codes codes^T) * x_scales * row_scales + bias; y_format from y's type if not given."""
+    fid, size = _value_format(y_format, y, "y")
+    return _check("pesti_gemm_i8row_i8token", load().pesti_gemm_i8row_i8token(
+        m, out_features, in_features, _sized(codes, out_features * in_features, "codes"),
+        _sized(row_scales, 4 * out_features, "row_scales", "float32"), _sized(x_codes, m * in_features, "x_codes"),
+        _sized(x_scales, 4 * m, "x_scales", "float32"), fid, _sized(y, m * out_features * size, "y"),
+        _sized(bias, 4 * out_features, "bias", "float32"), _stream(stream)))
+
+
+def _expert_format(fmt):
+    """(PESTI_FMT_* id, bytes per element of W and X)."""
+    fid = EXPERT_FORMAT_IDS[fmt] if isinstance(fmt, str) else int(fmt)
+    return fid, 2 if fid == EXPERT_FORMAT_IDS["f16"] else 1
+
+
+def pesti_gemm_experts(fmt, rows, experts, out_features, in_features, offsets, w, x_tokens, x, y, bias=None,
+                       w_scales=None, x_scales=None, x_rows=None, y_format=None, stream=None):
+    """Y[r] = X[x_rows[r]] W_e^T + b_e for the rows offsets[e]..offsets[e+1]-1 of every expert e;
+    fmt "f16", or "i8row" with w_scales and x_scales."""
+    fid, size = _expert_format(fmt)
+    yid, ysize = _value_format(y_format, y, "y")
+    return _check("pesti_gemm_experts", load().pesti_gemm_experts(
+        fid, rows, experts, out_features, in_features, _sized(offsets, 4 * (experts + 1), "offsets", "int32"),
+        _sized(w, experts * out_features * in_features * size, "w"),
+        _sized(w_scales, 4 * experts * out_features, "w_scales", "float32"), x_tokens,
+        _sized(x, x_tokens * in_features * size, "x"), _sized(x_scales, 4 * x_tokens, "x_scales", "float32"),
+        _sized(x_rows, 4 * rows, "x_rows", "int32"), yid, _sized(y, rows * out_features * ysize, "y"),
+        _sized(bias, 4 * experts * out_features, "bias", "float32"), _stream(stream)))
+
+
+def pesti_gemm_experts_swiglu(fmt, rows, experts, out_features, in_features, offsets, w_gate, w_up, x_tokens, x, h,
+                              gate_scales=None, up_scales=None, x_scales=None, x_rows=None, h_format=None,
+                              stream=None):
+    """h[r] = silu(X[x_rows[r]] W_gate_e^T) * (X[x_rows[r]] W_up_e^T), rows and formats as for pesti_gemm_experts."""
+    fid, size = _expert_format(fmt)
+    hid, hsize = _value_format(h_format, h, "h")
+    w_bytes, s_bytes = experts * out_features * in_features * size, 4 * experts * out_features
+    return _check("pesti_gemm_experts_swiglu", load().pesti_gemm_experts_swiglu(
+        fid, rows, experts, out_features, in_features, _sized(offsets, 4 * (experts + 1), "offsets", "int32"),
+        _sized(w_gate, w_bytes, "w_gate"), _sized(w_up, w_bytes, "w_up"),
+        _sized(gate_scales, s_bytes, "gate_scales", "float32"), _sized(up_scales, s_bytes, "up_scales", "float32"),
+        x_tokens, _sized(x, x_tokens * in_features * size, "x"), _sized(x_scales, 4 * x_tokens, "x_scales", "float32"),
+        _sized(x_rows, 4 * rows, "x_rows", "int32"), hid, _sized(h, rows * out_features * hsize, "h"),
+        _stream(stream)))
 
 
 def gemv_ops(ops):

@@ -1,0 +1,534 @@
+// Products of rows of X with the rows of one weight matrix, or of one matrix
+// per expert: Y = X W^T (+ b) on binary16 or on 8-bit integers with a scale
+// per row of X and per row of W.  Shared by the dense 8-bit linear layer
+// (csrc/gemm_i8.hip) and the expert-grouped products (csrc/gemm_experts.hip).
+//
+// Both element types feed the matrix cores the same way: a lane's operand of
+// v_mfma_i32_16x16x64_i8 and of v_mfma_f32_16x16x32_f16 is 16 consecutive
+// bytes of a row, the four lane groups of a wavefront taking the four
+// 16-byte chunks of a 64-byte k-step.  The kernels here therefore count K in
+// bytes and differ by type only in the instruction and the epilogue.
+//
+// The operands are W first and X second, so a lane ends with four
+// consecutive output columns of one row of X and stores them at once.
+#pragma once
+
+#include "common.h"
+
+namespace pesti {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+struct TileArgs {
+  const uint8_t* w;        // [experts][n][kbytes]
+  const uint8_t* w2;       // gated: the up projection, as w
+  const float* ws;         // 8-bit: [experts][n]
+  const float* ws2;        // gated 8-bit
+  const uint8_t* x;        // [x_tokens][kbytes]
+  const float* xs;         // 8-bit: [x_tokens]
+  const int32_t* x_rows;   // row of X for each row of Y, or null
+  const int32_t* offsets;  // [experts + 1] first rows of Y, or null (one matrix, all rows)
+  void* y;                 // [rows][n]
+  const float* bias;       // [experts][n] or null
+  int64_t rows;
+  int64_t x_tokens;
+  int64_t n;
+  int32_t kbytes;
+  int32_t experts;
+  int32_t tiles_n;         // column tiles of the kernel's width
+  int32_t y_f16;           // Y in binary16, else float32
+};
+
+struct ElemI8 {
+  typedef i32x4 Acc;
+  static constexpr bool kScaled = true;
+  __device__ __forceinline__ static Acc zero() { return i32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ static Acc mma(i32x4 a, i32x4 b, Acc c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+  }
+};
+struct ElemF16 {
+  typedef f32x4 Acc;
+  static constexpr bool kScaled = false;
+  __device__ __forceinline__ static Acc zero() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ static Acc mma(i32x4 a, i32x4 b, Acc c) {
+    typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+  }
+};
+
+// One workgroup's tile: rows row0..row_end-1 of Y (at most the kernel's
+// height of them are its own) times column tile nt of expert `expert`.
+struct TileAt {
+  int64_t row0, row_end;
+  int expert;
+  int nt;
+};
+
+// The t-th of `total` tiles for workgroup b.  Workgroups go to the 8 XCDs in
+// turn, each with its own L2: XCD b % 8 takes a contiguous run of tiles, and
+// the run walks groups of 8 row tiles column by column, so the workgroups
+// that one XCD runs at a time share rows of X and of W.
+__device__ __forceinline__ bool tile_of(int64_t b, int64_t row_tiles, int64_t col_tiles, int64_t* mt, int* nt) {
+  const int64_t total = row_tiles * col_tiles;
+  const int64_t xcd = b % kXcds, slot = b / kXcds;
+  const int64_t per = total / kXcds, rem = total % kXcds;
+  if (slot >= per + (xcd < rem ? 1 : 0)) return false;
+  const uint32_t lin = static_cast<uint32_t>(xcd * per + (xcd < rem ? xcd : rem) + slot);   // below 2^31
+  constexpr uint32_t kGroup = 8;
+  const uint32_t width = kGroup * static_cast<uint32_t>(col_tiles);
+  const uint32_t g = lin / width, in = lin % width;
+  const uint32_t left = static_cast<uint32_t>(row_tiles) - g * kGroup;
+  const uint32_t gm = left < kGroup ? left : kGroup;
+  *mt = g * kGroup + in % gm;
+  *nt = static_cast<int>(in / gm);
+  return true;
+}
+
+// First and last row of expert e, kept inside 0..rows whatever the offsets hold.
+__device__ __forceinline__ void expert_rows(const TileArgs& a, int e, int* first, int* last) {
+  const int rows = static_cast<int>(a.rows);
+  int f = a.offsets[e], l = a.offsets[e + 1];
+  f = f < 0 ? 0 : (f > rows ? rows : f);
+  l = l < f ? f : (l > rows ? rows : l);
+  *first = f;
+  *last = l;
+}
+
+// Inclusive sum over the lanes of a wavefront.
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// The tile of this workgroup: every wavefront finds it by itself, 64 experts
+// at a time.  An expert of c rows has ceil(c / BM) row tiles; their total is
+// known only here, so the grid is launched for the most there can be and the
+// workgroups past the total leave.
+template <int BM>
+__device__ __forceinline__ bool find_tile(const TileArgs& a, TileAt* at) {
+  int64_t mt = 0;
+  if (!a.offsets) {
+    if (!tile_of(blockIdx.x, (a.rows + BM - 1) / BM, a.tiles_n, &mt, &at->nt)) return false;
+    at->expert = 0;
+    at->row0 = mt * BM;
+    at->row_end = a.rows;
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  int f = 0, l = 0, incl = 0, total = 0;
+  for (int e0 = 0; e0 < a.experts; e0 += 64) {
+    f = l = 0;
+    if (e0 + lane < a.experts) expert_rows(a, e0 + lane, &f, &l);
+    incl = wave_scan((l - f + BM - 1) / BM);
+    total += __builtin_amdgcn_readlane(incl, 63);
+  }
+  if (!tile_of(blockIdx.x, total, a.tiles_n, &mt, &at->nt)) return false;
+  int left = static_cast<int>(mt);
+  for (int e0 = 0; e0 < a.experts; e0 += 64) {
+    if (a.experts > 64) {
+      f = l = 0;
+      if (e0 + lane < a.experts) expert_rows(a, e0 + lane, &f, &l);
+      incl = wave_scan((l - f + BM - 1) / BM);
+    }
+    const uint64_t past = __ballot(incl > left);
+    if (past) {
+      const int s = __builtin_ctzll(past);
+      const int first = __builtin_amdgcn_readlane(f, s), last = __builtin_amdgcn_readlane(l, s);
+      const int before = __builtin_amdgcn_readlane(incl, s) - (last - first + BM - 1) / BM;
+      at->expert = e0 + s;
+      at->row0 = first + static_cast<int64_t>(left - before) * BM;
+      at->row_end = last;
+      return true;
+    }
+    left -= __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
+
+// Row of X for row r of Y; *ok says whether there is one (an index outside
+// X stands for a row of zeros: row 0 is loaded in its place and dropped).
+__device__ __forceinline__ int64_t x_row(const TileArgs& a, int64_t r, bool* ok) {
+  int64_t i = a.x_rows ? a.x_rows[r] : r;
+  *ok = i >= 0 && i < a.x_tokens;
+  return *ok ? i : 0;
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
+// Stores the four consecutive columns n..n+3 of row r, rounding once to
+// binary16 where Y is that.  Rows start 4 outputs aligned when n % 4 == 0.
+__device__ __forceinline__ void store4(const TileArgs& a, int64_t r, int64_t n, const float* v) {
+  const int64_t at = r * a.n + n;
+  if (a.y_f16) {
+    _Float16* y = static_cast<_Float16*>(a.y);
+    if ((a.n & 3) == 0) {
+      typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+      if (n < a.n)
+        *reinterpret_cast<h4*>(y + at) = h4{static_cast<_Float16>(v[0]), static_cast<_Float16>(v[1]),
+                                            static_cast<_Float16>(v[2]), static_cast<_Float16>(v[3])};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (n + q < a.n) y[at + q] = static_cast<_Float16>(v[q]);
+    }
+  } else {
+    float* y = static_cast<float*>(a.y);
+    if ((a.n & 3) == 0) {
+      if (n < a.n) *reinterpret_cast<f32x4*>(y + at) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (n + q < a.n) y[at + q] = v[q];
+    }
+  }
+}
+
+// Four per-column values (scales or bias) at columns n..n+3 of an [experts][n]
+// array, 0 past the last.
+__device__ __forceinline__ void load4(const float* p, int64_t n, int64_t count, float* v) {
+  if (n + 3 < count) {
+    typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+    const f32x4u t = *reinterpret_cast<const f32x4u*>(p + n);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = t[q];
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = n + q < count ? p[n + q] : 0.f;
+  }
+}
+
+// The value of four sums for a row of X with scale xs: for 8-bit operands
+// acc * xs * ws, in this order so that small scales do not meet first and
+// underflow; the integer sum is exact and rounded once to float32.
+template <typename E>
+__device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const float* ws, const float* b, float* v) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (E::kScaled)
+      v[q] = __builtin_fmaf(static_cast<float>(c[q]) * xs, ws[q], b[q]);
+    else
+      v[q] = c[q] + b[q];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tiles staged through LDS.  A workgroup of WM * WN wavefronts owns BM rows
+// of Y and BN rows of W (gated: BN / 2 columns, 16 rows of the gate and 16 of
+// the up projection in turn); K advances 128 bytes at a time through NS
+// buffers.  Loads go from memory straight into LDS, 1 KB (8 rows) per
+// wavefront instruction, NS - 1 steps ahead of the matrix cores.
+//
+// LDS holds 128-byte rows with their 16-byte chunks permuted, chunk c of row
+// r at place c ^ (r & 7): a wavefront's operand read (16 rows, one chunk
+// each per lane group) then spreads over all banks.  The permutation is made
+// by the lanes' source addresses, the destination being linear.
+//
+// K past the row's end (kbytes is a multiple of 32, the step 128) reads a
+// zero chunk; rows past the tile's own read the last row in their place and
+// are not stored.
+// ---------------------------------------------------------------------------
+__device__ __align__(16) const uint8_t kZeroChunk[16] = {0};
+
+template <int BM, int BN, int NS>
+constexpr int tile_lds() { return (BM + BN) * 128 * NS; }
+
+template <typename E, int BM, int BN, int WM, int WN, int NS, bool GATED>
+__global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
+  constexpr int kWaves = WM * WN;
+  constexpr int kTM = BM / WM / 16, kTN = BN / WN / 16;
+  constexpr int kInstr = (BM + BN) / 8;
+  constexpr int kPer = (kInstr + kWaves - 1) / kWaves;
+  constexpr int kStage = (BM + BN) * 128;
+  constexpr int kCols = GATED ? BN / 2 : BN;
+  static_assert(!GATED || kTN % 2 == 0, "a wavefront holds gate and up of the same columns");
+  extern __shared__ __align__(16) uint8_t lds[];
+  typedef __attribute__((address_space(3))) uint8_t Lds;
+  typedef __attribute__((address_space(1))) const uint8_t Glb;
+
+  TileAt at;
+  if (!find_tile<BM>(a, &at)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = static_cast<int64_t>(at.nt) * kCols;
+  const int64_t last = at.row_end - 1;
+  const uint8_t* w = a.w + (at.expert * a.n) * static_cast<int64_t>(a.kbytes);
+  const uint8_t* w2 = GATED ? a.w2 + (at.expert * a.n) * static_cast<int64_t>(a.kbytes) : nullptr;
+  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;   // the same place in every row this lane loads
+
+  // Source row of each of the wavefront's load instructions: X rows first,
+  // then W rows; instruction q fills LDS rows 8q..8q+7.
+  const uint8_t* src[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    int q = wave + kWaves * j;
+    q = q < kInstr ? q : kInstr - 1;
+    const int r = 8 * q + (lane >> 3);
+    if (q < BM / 8) {
+      const int64_t row = at.row0 + r;
+      bool ok;
+      const int64_t i = x_row(a, row < last ? row : last, &ok);
+      src[j] = a.x + i * a.kbytes + chunk;
+    } else {
+      const int c = r - BM;
+      const int64_t col = n0 + (GATED ? (c >> 5) * 16 + (c & 15) : c);
+      const uint8_t* m = GATED && (c & 16) ? w2 : w;
+      src[j] = m + (col < a.n ? col : a.n - 1) * a.kbytes + chunk;
+    }
+  }
+  const int steps = (a.kbytes + 127) >> 7;
+  auto issue = [&](int s) {
+    Lds* base = (Lds*)lds + (s % NS) * kStage;
+    const bool in = s * 128 + chunk < a.kbytes;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      int q = wave + kWaves * j;
+      q = q < kInstr ? q : kInstr - 1;
+      const uint8_t* p = in ? src[j] : kZeroChunk;
+      __builtin_amdgcn_global_load_lds((Glb*)p, (__attribute__((address_space(3))) void*)(base + q * 1024), 16, 0, 0);
+      src[j] += 128;
+    }
+  };
+
+  typename E::Acc acc[kTM][kTN];
+#pragma unroll
+  for (int i = 0; i < kTM; ++i)
+#pragma unroll
+    for (int j = 0; j < kTN; ++j) acc[i][j] = E::zero();
+
+#pragma unroll
+  for (int s = 0; s < NS - 1; ++s)
+    if (s < steps) issue(s);
+  const int wm = wave % WM, wn = wave / WM;
+  const int place = ((lane >> 4) ^ (lane & 7)) * 16;
+  const int xrow = (wm * kTM * 16 + (lane & 15)) * 128;
+  const int wrow = (BM + wn * kTN * 16 + (lane & 15)) * 128;
+  for (int s = 0; s < steps; ++s) {
+    // Step s has landed once at most the later steps' loads are in flight;
+    // the barrier extends that to every wavefront's part and says that all
+    // are done reading step s - 1, whose buffer the next load fills.
+    if (s + NS - 2 < steps)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * kPer) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (s + NS - 1 < steps) issue(s + NS - 1);
+    const uint8_t* buf = lds + (s % NS) * kStage;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      i32x4 xf[kTM], wf[kTN];
+#pragma unroll
+      for (int i = 0; i < kTM; ++i)
+        xf[i] = *reinterpret_cast<const i32x4*>(buf + xrow + i * 2048 + (place ^ (64 * ks)));
+#pragma unroll
+      for (int j = 0; j < kTN; ++j)
+        wf[j] = *reinterpret_cast<const i32x4*>(buf + wrow + j * 2048 + (place ^ (64 * ks)));
+#pragma unroll
+      for (int i = 0; i < kTM; ++i)
+#pragma unroll
+        for (int j = 0; j < kTN; ++j) acc[i][j] = E::mma(wf[j], xf[i], acc[i][j]);
+    }
+  }
+
+  const int g = lane >> 4;
+  const float* ws = E::kScaled ? a.ws + at.expert * a.n : nullptr;
+  const float* ws2 = E::kScaled && GATED ? a.ws2 + at.expert * a.n : nullptr;
+  const float* bias = a.bias ? a.bias + at.expert * a.n : nullptr;
+#pragma unroll
+  for (int i = 0; i < kTM; ++i) {
+    const int64_t row = at.row0 + wm * kTM * 16 + 16 * i + (lane & 15);
+    if (row > last) continue;
+    bool ok;
+    const int64_t xi = x_row(a, row, &ok);
+    const float xs = E::kScaled ? (ok ? a.xs[xi] : 0.f) : 1.f;
+#pragma unroll
+    for (int j = 0; j < kTN; j += GATED ? 2 : 1) {
+      const int64_t col = n0 + (wn * kTN * 16 + 16 * j) / (GATED ? 2 : 1) + 4 * g;
+      float s[4] = {1.f, 1.f, 1.f, 1.f}, b[4] = {0.f, 0.f, 0.f, 0.f}, v[4];
+      if (E::kScaled) load4(ws, col, a.n, s);
+      if (!GATED && bias) load4(bias, col, a.n, b);
+      scaled<E>(ok ? acc[i][j] : E::zero(), xs, s, b, v);
+      if constexpr (GATED) {
+        float u[4];
+        if (E::kScaled) load4(ws2, col, a.n, s);
+        scaled<E>(ok ? acc[i][j + 1] : E::zero(), xs, s, b, u);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = silu_mul(v[q], u[q]);
+      }
+      store4(a, row, col, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows of X: a workgroup owns 16 columns and up to 16 * MT rows of Y, and
+// its NW wavefronts split K into contiguous slices, each streaming its part
+// of W from memory straight into operand registers (C k-steps at a time, the
+// next C in flight); the partial sums meet in LDS in wavefront order.
+// ---------------------------------------------------------------------------
+template <typename E, int MT, int NW, int C, bool GATED>
+__global__ __launch_bounds__(NW * 64) void gemm_rows_kernel(TileArgs a) {
+  constexpr int kG = GATED ? 2 : 1;
+  __shared__ typename E::Acc part[NW][MT][kG][kWave];
+  TileAt at;
+  if (!find_tile<16 * MT>(a, &at)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int64_t n0 = static_cast<int64_t>(at.nt) * 16;
+  const int64_t last = at.row_end - 1;
+  const int steps = (a.kbytes + 63) >> 6;
+  const int per = (steps + NW - 1) / NW;
+  const int s0 = wave * per < steps ? wave * per : steps;
+  const int s1 = s0 + per < steps ? s0 + per : steps;
+
+  const int64_t col = n0 + i < a.n ? n0 + i : a.n - 1;
+  const uint8_t* wp[kG];
+  wp[0] = a.w + (at.expert * a.n + col) * static_cast<int64_t>(a.kbytes);
+  if constexpr (GATED) wp[1] = a.w2 + (at.expert * a.n + col) * static_cast<int64_t>(a.kbytes);
+  const uint8_t* xp[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t row = at.row0 + 16 * t + i;
+    bool ok;
+    xp[t] = a.x + x_row(a, row < last ? row : last, &ok) * a.kbytes;
+  }
+
+  struct Buf {
+    i32x4 w[C][kG], x[C][MT];
+  };
+  // k-steps past the slice and the half step past a row's end load the row's
+  // start, and both operands are zeroed before they are used.
+  auto load = [&](int s, Buf& b) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int o = (s + c) * 64 + 16 * g;
+      const int p = s + c < s1 && o < a.kbytes ? o : 0;
+#pragma unroll
+      for (int k = 0; k < kG; ++k) b.w[c][k] = *reinterpret_cast<const i32x4*>(wp[k] + p);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) b.x[c][t] = *reinterpret_cast<const i32x4*>(xp[t] + p);
+    }
+  };
+  typename E::Acc acc[MT][kG];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int k = 0; k < kG; ++k) acc[t][k] = E::zero();
+  auto mma = [&](int s, const Buf& b) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const bool in = s + c < s1 && (s + c) * 64 + 16 * g < a.kbytes;
+      const i32x4 z = {0, 0, 0, 0};
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int k = 0; k < kG; ++k) acc[t][k] = E::mma(in ? b.w[c][k] : z, in ? b.x[c][t] : z, acc[t][k]);
+    }
+  };
+  if (s0 < s1) {
+    Buf ba, bb;
+    load(s0, ba);
+    for (int s = s0; s < s1; s += 2 * C) {
+      load(s + C, bb);
+      mma(s, ba);
+      if (s + C >= s1) break;
+      load(s + 2 * C, ba);
+      mma(s + C, bb);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int k = 0; k < kG; ++k) part[wave][t][k][lane] = acc[t][k];
+  __syncthreads();
+
+  const float* bias = a.bias ? a.bias + at.expert * a.n : nullptr;
+  for (int e = threadIdx.x; e < MT * kWave; e += NW * kWave) {
+    const int t = e / kWave, l = e % kWave;
+    const int64_t row = at.row0 + 16 * t + (l & 15);
+    if (row > last) continue;
+    bool ok;
+    const int64_t xi = x_row(a, row, &ok);
+    const float xs = E::kScaled ? (ok ? a.xs[xi] : 0.f) : 1.f;
+    const int64_t c0 = n0 + 4 * (l >> 4);
+    float v[kG][4];
+#pragma unroll
+    for (int k = 0; k < kG; ++k) {
+      typename E::Acc r = part[0][t][k][l];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) r += part[w][t][k][l];
+      float s[4] = {1.f, 1.f, 1.f, 1.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+      if (E::kScaled) load4((k ? a.ws2 : a.ws) + at.expert * a.n, c0, a.n, s);
+      if (!GATED && bias) load4(bias, c0, a.n, b);
+      scaled<E>(ok ? r : E::zero(), xs, s, b, v[k]);
+    }
+    if constexpr (GATED)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[0][q] = silu_mul(v[0][q], v[1][q]);
+    store4(a, row, c0, v[0]);
+  }
+}
+
+}  // namespace pesti
+
+namespace pesti_host {
+
+// The launch behind the entry points: args with everything but the tile
+// count set, `gated` for the joined gate and up products.
+int gemm_tiles_i8(const pesti::TileArgs& a, bool gated, hipStream_t st);
+int gemm_tiles_f16(const pesti::TileArgs& a, bool gated, hipStream_t st);
+
+// Most row tiles of height bm there can be: each expert with rows ends in at
+// most one partial tile.
+inline int64_t most_row_tiles(const pesti::TileArgs& a, int bm) {
+  if (!a.offsets) return (a.rows + bm - 1) / bm;
+  const int64_t used = a.experts < a.rows ? a.experts : a.rows;
+  return a.rows / bm + used;
+}
+
+inline int launch_tiles(const void* fn, pesti::TileArgs a, int bm, int cols, int threads, size_t lds, hipStream_t st) {
+  const int64_t tn = (a.n + cols - 1) / cols;
+  const int64_t total = most_row_tiles(a, bm) * tn;
+  // Tiles are numbered in 31 bits; the grid is rounded up to whole turns of the XCDs.
+  if (tn > (1 << 27) || total > INT32_MAX - pesti::kXcds) return PESTI_ERR_SHAPE;
+  a.tiles_n = static_cast<int32_t>(tn);
+  void* params[] = {&a};
+  const unsigned grid = static_cast<unsigned>((total + pesti::kXcds - 1) / pesti::kXcds * pesti::kXcds);
+  if (grid == 0) return PESTI_OK;
+  return hipLaunchKernel(fn, dim3(grid), dim3(threads), params, lds, st) == hipSuccess ? PESTI_OK : PESTI_ERR_LAUNCH;
+}
+
+template <typename E, int BM, int BN, int WM, int WN, int NS, bool GATED>
+int launch_tile(const pesti::TileArgs& a, hipStream_t st) {
+  return launch_tiles(reinterpret_cast<const void*>(&pesti::gemm_tile_kernel<E, BM, BN, WM, WN, NS, GATED>), a, BM,
+                      GATED ? BN / 2 : BN, WM * WN * 64, pesti::tile_lds<BM, BN, NS>(), st);
+}
+
+template <typename E, int MT, int NW, int C, bool GATED>
+int launch_rows(const pesti::TileArgs& a, hipStream_t st) {
+  return launch_tiles(reinterpret_cast<const void*>(&pesti::gemm_rows_kernel<E, MT, NW, C, GATED>), a, 16 * MT, 16,
+                      NW * 64, 0, st);
+}
+
+// Rows one matrix is multiplied with, on average over the experts.
+inline int64_t mean_rows(const pesti::TileArgs& a) { return (a.rows + a.experts - 1) / a.experts; }
+
+// Row counts up to 32 stream W once through the K-split kernel; above that
+// operands are shared through LDS.
+template <typename E, bool GATED>
+int launch_any(const pesti::TileArgs& a, hipStream_t st) {
+  const int64_t mean = mean_rows(a);
+  if (mean <= 16) return launch_rows<E, 1, 8, 4, GATED>(a, st);
+  if (mean <= 32) return launch_rows<E, 2, 8, 2, GATED>(a, st);
+  if (mean <= 64) return launch_tile<E, 64, 64, 2, 2, 3, GATED>(a, st);
+  return launch_tile<E, 128, 128, 2, 2, 2, GATED>(a, st);
+}
+
+}  // namespace pesti_host

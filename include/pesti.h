@@ -99,10 +99,14 @@ extern "C" {
 #define PESTI_FMT_Q4_K_STREAM 8
 /* binary16 weights [out][in]: for the small-M GEMM calls that take a format */
 #define PESTI_FMT_F16 16
+/* float32 values: for the calls that take the format of X or Y */
+#define PESTI_FMT_F32 17
 
 #define PESTI_MAX_BATCH 8
 #define PESTI_MAX_IN_FEATURES 32768
 #define PESTI_MAX_GEMM_M 4096
+#define PESTI_MAX_TOKENS (1 << 20)  /* rows of X or Y: 8-bit and expert GEMMs */
+#define PESTI_MAX_EXPERTS 1024
 
 /* --- quantized mat-vec, y = W x + b ------------------------------------ */
 
@@ -335,6 +339,80 @@ int pesti_gemm_smallm_ws(int32_t format, int64_t m, int64_t out_features, int64_
 int pesti_gemm_smallm_noalloc(int32_t format, int64_t m, int64_t out_features, int64_t in_features,
                               const void* w, const uint16_t* x, float* y, const float* bias,
                               void* stream);
+
+/* --- linear layer on 8-bit integers, a scale per token and per channel ----
+ * The prompt-width product of the per-row int8 weights (pesti_gemv_i8row)
+ * with X in 8 bits too: Y[t][o] = x_scales[t] * row_scales[o] *
+ * sum_i x_codes[t][i] * codes[o][i] + bias[o], the sum taken exactly in
+ * 32-bit integers on the matrix cores.  X is quantized once and serves every
+ * layer that reads it (Q, K and V; gate and up).
+ *
+ * pesti_quant_i8token: x [m][in] in x_format (PESTI_FMT_F32 or
+ * PESTI_FMT_F16) to codes int8 [m][in] and scales float32 [m], the rule of
+ * the per-row weights: scale = max|x| / 127 (one float32 rounding), code =
+ * the exact x / scale rounded half away from zero, -127..127.  A row of
+ * zeros (or one whose scale rounds to zero) gets scale 0 and codes 0; a row
+ * that holds an infinity or NaN gets scale NaN and codes 0, so that its
+ * outputs are NaN.  With in_features == 0 the scales are 0.
+ *
+ * pesti_gemm_i8row_i8token: codes int8 [out][in] and row_scales float32
+ * [out] as for pesti_gemv_i8row, x_codes int8 [m][in] and x_scales float32
+ * [m] (any codes -128..127), Y [m][out] in y_format (PESTI_FMT_F32, or
+ * PESTI_FMT_F16 rounded once from float32).  The float32 value is
+ * fma(float(sum) * x_scale, row_scale, bias): three roundings.
+ *
+ * m in [0, PESTI_MAX_TOKENS], else PESTI_ERR_BATCH; codes, x and Y 16-byte
+ * aligned, scales and bias 4; an unknown format is PESTI_ERR_SHAPE. */
+int pesti_quant_i8token(int32_t x_format, int64_t m, int64_t in_features, const void* x,
+                        int8_t* codes, float* scales, void* stream);
+int pesti_gemm_i8row_i8token(int64_t m, int64_t out_features, int64_t in_features,
+                             const int8_t* codes, const float* row_scales,
+                             const int8_t* x_codes, const float* x_scales, int32_t y_format,
+                             void* y, const float* bias, void* stream);
+
+/* --- linear layers grouped by expert ---------------------------------------
+ * Y's rows are sorted by expert: rows offsets[e] .. offsets[e+1]-1 belong to
+ * expert e and are Y[r] = X[x_rows[r]] W_e^T + b_e, any number of them per
+ * expert, none included, in one launch (the grouped mat-vec's case with one
+ * matrix per expert and row counts that only the device knows).
+ *
+ * format: PESTI_FMT_F16 (W and X binary16, the scale arguments ignored) or
+ * PESTI_FMT_I8ROW (W and X int8 with w_scales float32 [experts][out] and
+ * x_scales float32 [x_tokens], as for pesti_gemm_i8row_i8token).
+ *   offsets  int32 [experts + 1] in device memory, non-decreasing within
+ *            0..rows.  Rows of Y outside every expert's range (before
+ *            offsets[0], from offsets[experts] on) are left as they were.
+ *            Values outside 0..rows count as the nearer end, and an expert
+ *            whose end lies before its start has no rows; what rows of Y
+ *            hold after a call with decreasing offsets is not specified.
+ *   w        [experts][out][in]; bias float32 [experts][out] or NULL
+ *   x        [x_tokens][in]
+ *   x_rows   int32 [rows] in device memory, the row of X for each row of Y
+ *            (the same one any number of times), or NULL for row r itself,
+ *            which needs x_tokens >= rows (else PESTI_ERR_BATCH).  An index
+ *            outside 0..x_tokens-1 stands for a row of zeros.
+ *   y        [rows][out] in y_format (PESTI_FMT_F32 or PESTI_FMT_F16)
+ *
+ * pesti_gemm_experts_swiglu joins the gate and up products of the same rows
+ * (h = silu(X W_gate^T) * (X W_up^T), as pesti_gemv_swiglu): w_gate and w_up
+ * [experts][out][in] of one format, gate_scales and up_scales their scales,
+ * h [rows][out] in h_format; no bias.
+ *
+ * rows and x_tokens in [0, PESTI_MAX_TOKENS] (PESTI_ERR_BATCH), experts in
+ * [0, PESTI_MAX_EXPERTS] (PESTI_ERR_SHAPE); sums in float32 (binary16) or
+ * exactly in 32-bit integers.  rows, out_features or experts of 0 return 0
+ * without touching a pointer. */
+int pesti_gemm_experts(int32_t format, int64_t rows, int64_t experts, int64_t out_features,
+                       int64_t in_features, const int32_t* offsets, const void* w,
+                       const float* w_scales, int64_t x_tokens, const void* x,
+                       const float* x_scales, const int32_t* x_rows, int32_t y_format, void* y,
+                       const float* bias, void* stream);
+int pesti_gemm_experts_swiglu(int32_t format, int64_t rows, int64_t experts,
+                              int64_t out_features, int64_t in_features, const int32_t* offsets,
+                              const void* w_gate, const void* w_up, const float* gate_scales,
+                              const float* up_scales, int64_t x_tokens, const void* x,
+                              const float* x_scales, const int32_t* x_rows, int32_t h_format,
+                              void* h, void* stream);
 
 /* --- dequantization to float32 (bit-exact; checks the unpacking) --------
  * w_out float32 [rows][in_features]: each weight rounded once from its

@@ -541,3 +541,76 @@ def quantize_i8row(w):
     q = np.sign(v) * np.floor(np.abs(v) + 0.5)
     codes[nz] = np.clip(q, -127, 127).astype(np.int8)
     return codes, scales
+
+
+# ---------------------------------------------------------------------------
+# 8-bit linear layer with a scale per token and channel, and products grouped
+# by expert
+# ---------------------------------------------------------------------------
+def quantize_i8token(x):
+    """Per-token symmetric int8 quantization of activations: quantize_i8row
+    on the rows of x (float32 or binary16, whose values float32 holds), and
+    scale NaN with codes 0 for a row that holds an infinity or NaN."""
+    x = np.asarray(x, dtype=np.float32)
+    fine = np.isfinite(x).all(axis=1)
+    codes, scales = quantize_i8row(np.where(fine[:, None], x, np.float32(0)))
+    scales[~fine] = np.nan
+    return codes, scales
+
+
+def gemm_i8(x_codes, x_scales, codes, row_scales, bias=None):
+    """Y = x_scale * row_scale * (x_codes codes^T) + bias in float64 (the
+    integer sums are exact: below 2^53), and the magnitude that its rounding
+    errors are relative to: |product| + |bias|."""
+    acc = np.asarray(x_codes, dtype=np.float64) @ np.asarray(codes, dtype=np.float64).T
+    y = acc * np.asarray(x_scales, dtype=np.float64)[:, None] * np.asarray(row_scales, dtype=np.float64)[None, :]
+    size = np.abs(y)
+    if bias is not None:
+        b = np.asarray(bias, dtype=np.float64)
+        y, size = y + b, size + np.abs(b)
+    return y, size
+
+
+def expert_of_rows(offsets, rows: int) -> np.ndarray:
+    """Expert of each of `rows` rows (-1: none), with offsets kept inside
+    0..rows and a range that ends before it starts empty."""
+    e = np.full(rows, -1, dtype=np.int64)
+    for i in range(len(offsets) - 1):
+        f = min(max(int(offsets[i]), 0), rows)
+        e[f:max(f, min(int(offsets[i + 1]), rows))] = i
+    return e
+
+
+def gathered(x, x_rows, rows: int):
+    """Rows of x for each row of Y in float64, rows of zeros where the index
+    is outside x."""
+    x = np.asarray(x, dtype=np.float64)
+    at = np.arange(rows) if x_rows is None else np.asarray(x_rows, dtype=np.int64)
+    ok = (at >= 0) & (at < len(x))
+    out = np.zeros((rows,) + x.shape[1:])
+    out[ok] = x[at[ok]]
+    return out
+
+
+def gemm_experts(offsets, w, x, rows: int, x_rows=None, bias=None, w_scales=None, x_scales=None):
+    """Y[r] = X[x_rows[r]] W_e^T + b_e in float64 for the rows of every
+    expert, NaN elsewhere, and sum |w x| + |b| beside it.  w [experts][out]
+    [in] and x [tokens][in] are values or, with scales, 8-bit codes, whose
+    sums are exact and scaled afterwards (a sum of zero stays zero)."""
+    w = np.asarray(w, dtype=np.float64)
+    xr = gathered(x, x_rows, rows)
+    xs = None if x_scales is None else gathered(x_scales, x_rows, rows)
+    y = np.full((rows, w.shape[1]), np.nan)
+    size = np.full_like(y, np.nan)
+    of = expert_of_rows(offsets, rows)
+    for e in range(len(w)):
+        at = of == e
+        y[at], size[at] = xr[at] @ w[e].T, np.abs(xr[at]) @ np.abs(w[e]).T
+        if w_scales is not None:
+            scale = xs[at][:, None] * np.asarray(w_scales[e], dtype=np.float64)
+            y[at], size[at] = y[at] * scale, size[at] * np.abs(scale)
+        if bias is not None:
+            b = np.asarray(bias[e], dtype=np.float64)
+            y[at] += b
+            size[at] += np.abs(b)
+    return y, size
