@@ -139,10 +139,17 @@ def _ptr(obj):
     raise TypeError(f"cannot pass {type(obj).__name__} as a device pointer")
 
 
+def _raw_stream(torch, dev):
+    """The handle of device dev's current stream.  current_stream() builds a
+    stream object around it, at several times the cost of a launch check."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch, torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -282,20 +289,34 @@ def pesti_gemm_smallm_noalloc(fmt, m, out_features, in_features, w, x, y, bias=N
 
 
 # --- 8-bit linear layer, expert-grouped products ------------------------------
-def _sized(obj, nbytes, what, dtype=None):
+def _sized(dev, obj, nbytes, what, dtype=None):
     """_ptr of an argument, with a tensor's size, element type and device
-    checked too: these calls take several arrays of related sizes."""
+    (the current one, `dev`) checked too: these calls take several arrays of
+    related sizes."""
+    if obj is None or isinstance(obj, int):
+        return obj
     if not hasattr(obj, "data_ptr"):
         return _ptr(obj)
-    import torch
-    p = _ptr(obj)
-    if dtype is not None and obj.dtype != getattr(torch, dtype):
+    if obj.get_device() != dev:
+        raise ValueError(f"{what}: tensor arguments must live in device memory, on the current device {dev}; "
+                         f"got {obj.device}")
+    if not obj.is_contiguous():
+        raise ValueError(f"{what}: tensor arguments must be contiguous")
+    if dtype is not None and obj.dtype != dtype:
         raise ValueError(f"{what} must be a {dtype} tensor, got {obj.dtype}")
-    if obj.numel() * obj.element_size() < nbytes:
-        raise ValueError(f"{what} holds {obj.numel() * obj.element_size()} bytes, the call needs {nbytes}")
-    if obj.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what} is on {obj.device}, not on the current device")
-    return p
+    if obj.nbytes < nbytes:
+        raise ValueError(f"{what} holds {obj.nbytes} bytes, the call needs {nbytes}")
+    return obj.data_ptr()
+
+
+def _place(stream):
+    """(torch, current device, raw stream) of a call: device 0 where no GPU
+    is to be asked (the library then refuses the call itself)."""
+    import torch
+    if stream is None:
+        dev = torch.cuda.current_device()
+        return torch, dev, _raw_stream(torch, dev)
+    return torch, torch.cuda.current_device() if torch.cuda.is_available() else 0, _stream(stream)
 
 
 def _value_format(fmt, obj, what):
@@ -312,20 +333,22 @@ def _value_format(fmt, obj, what):
 def pesti_quant_i8token(x_format, m, in_features, x, codes, scales, stream=None):
     """Rows of X ("f32" or "f16") to int8 codes and a float32 scale per row."""
     fid, size = _value_format(x_format, x, "x")
+    torch, dev, st = _place(stream)
     return _check("pesti_quant_i8token", load().pesti_quant_i8token(
-        fid, m, in_features, _sized(x, m * in_features * size, "x"), _sized(codes, m * in_features, "codes"),
-        _sized(scales, 4 * m, "scales", "float32"), _stream(stream)))
+        fid, m, in_features, _sized(dev, x, m * in_features * size, "x"), _sized(dev, codes, m * in_features, "codes"),
+        _sized(dev, scales, 4 * m, "scales", torch.float32), st))
 
 
 def pesti_gemm_i8row_i8token(m, out_features, in_features, codes, row_scales, x_codes, x_scales, y, bias=None,
                              y_format=None, stream=None):
     """Y = (x_codes codes^T) * x_scales * row_scales + bias; y_format from y's type if not given."""
     fid, size = _value_format(y_format, y, "y")
+    torch, dev, st = _place(stream)
     return _check("pesti_gemm_i8row_i8token", load().pesti_gemm_i8row_i8token(
-        m, out_features, in_features, _sized(codes, out_features * in_features, "codes"),
-        _sized(row_scales, 4 * out_features, "row_scales", "float32"), _sized(x_codes, m * in_features, "x_codes"),
-        _sized(x_scales, 4 * m, "x_scales", "float32"), fid, _sized(y, m * out_features * size, "y"),
-        _sized(bias, 4 * out_features, "bias", "float32"), _stream(stream)))
+        m, out_features, in_features, _sized(dev, codes, out_features * in_features, "codes"),
+        _sized(dev, row_scales, 4 * out_features, "row_scales", torch.float32), _sized(dev, x_codes, m * in_features, "x_codes"),
+        _sized(dev, x_scales, 4 * m, "x_scales", torch.float32), fid, _sized(dev, y, m * out_features * size, "y"),
+        _sized(dev, bias, 4 * out_features, "bias", torch.float32), st))
 
 
 def _expert_format(fmt):
@@ -340,13 +363,14 @@ def pesti_gemm_experts(fmt, rows, experts, out_features, in_features, offsets, w
     fmt "f16", or "i8row" with w_scales and x_scales."""
     fid, size = _expert_format(fmt)
     yid, ysize = _value_format(y_format, y, "y")
+    torch, dev, st = _place(stream)
     return _check("pesti_gemm_experts", load().pesti_gemm_experts(
-        fid, rows, experts, out_features, in_features, _sized(offsets, 4 * (experts + 1), "offsets", "int32"),
-        _sized(w, experts * out_features * in_features * size, "w"),
-        _sized(w_scales, 4 * experts * out_features, "w_scales", "float32"), x_tokens,
-        _sized(x, x_tokens * in_features * size, "x"), _sized(x_scales, 4 * x_tokens, "x_scales", "float32"),
-        _sized(x_rows, 4 * rows, "x_rows", "int32"), yid, _sized(y, rows * out_features * ysize, "y"),
-        _sized(bias, 4 * experts * out_features, "bias", "float32"), _stream(stream)))
+        fid, rows, experts, out_features, in_features, _sized(dev, offsets, 4 * (experts + 1), "offsets", torch.int32),
+        _sized(dev, w, experts * out_features * in_features * size, "w"),
+        _sized(dev, w_scales, 4 * experts * out_features, "w_scales", torch.float32), x_tokens,
+        _sized(dev, x, x_tokens * in_features * size, "x"), _sized(dev, x_scales, 4 * x_tokens, "x_scales", torch.float32),
+        _sized(dev, x_rows, 4 * rows, "x_rows", torch.int32), yid, _sized(dev, y, rows * out_features * ysize, "y"),
+        _sized(dev, bias, 4 * experts * out_features, "bias", torch.float32), st))
 
 
 def pesti_gemm_experts_swiglu(fmt, rows, experts, out_features, in_features, offsets, w_gate, w_up, x_tokens, x, h,
@@ -355,14 +379,15 @@ def pesti_gemm_experts_swiglu(fmt, rows, experts, out_features, in_features, off
     """h[r] = silu(X[x_rows[r]] W_gate_e^T) * (X[x_rows[r]] W_up_e^T), rows and formats as for pesti_gemm_experts."""
     fid, size = _expert_format(fmt)
     hid, hsize = _value_format(h_format, h, "h")
+    torch, dev, st = _place(stream)
     w_bytes, s_bytes = experts * out_features * in_features * size, 4 * experts * out_features
     return _check("pesti_gemm_experts_swiglu", load().pesti_gemm_experts_swiglu(
-        fid, rows, experts, out_features, in_features, _sized(offsets, 4 * (experts + 1), "offsets", "int32"),
-        _sized(w_gate, w_bytes, "w_gate"), _sized(w_up, w_bytes, "w_up"),
-        _sized(gate_scales, s_bytes, "gate_scales", "float32"), _sized(up_scales, s_bytes, "up_scales", "float32"),
-        x_tokens, _sized(x, x_tokens * in_features * size, "x"), _sized(x_scales, 4 * x_tokens, "x_scales", "float32"),
-        _sized(x_rows, 4 * rows, "x_rows", "int32"), hid, _sized(h, rows * out_features * hsize, "h"),
-        _stream(stream)))
+        fid, rows, experts, out_features, in_features, _sized(dev, offsets, 4 * (experts + 1), "offsets", torch.int32),
+        _sized(dev, w_gate, w_bytes, "w_gate"), _sized(dev, w_up, w_bytes, "w_up"),
+        _sized(dev, gate_scales, s_bytes, "gate_scales", torch.float32), _sized(dev, up_scales, s_bytes, "up_scales", torch.float32),
+        x_tokens, _sized(dev, x, x_tokens * in_features * size, "x"), _sized(dev, x_scales, 4 * x_tokens, "x_scales", torch.float32),
+        _sized(dev, x_rows, 4 * rows, "x_rows", torch.int32), hid, _sized(dev, h, rows * out_features * hsize, "h"),
+        st))
 
 
 def gemv_ops(ops):

@@ -13,6 +13,8 @@
 // consecutive output columns of one row of X and stores them at once.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace pesti {
@@ -161,32 +163,40 @@ __device__ __forceinline__ int64_t x_row(const TileArgs& a, int64_t r, bool* ok)
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
-// Stores the four consecutive columns n..n+3 of row r, rounding once to
-// binary16 where Y is that.  Rows start 4 outputs aligned when n % 4 == 0.
-__device__ __forceinline__ void store4(const TileArgs& a, int64_t r, int64_t n, const float* v) {
-  const int64_t at = r * a.n + n;
-  if (a.y_f16) {
-    _Float16* y = static_cast<_Float16*>(a.y);
-    if ((a.n & 3) == 0) {
-      typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-      if (n < a.n)
-        *reinterpret_cast<h4*>(y + at) = h4{static_cast<_Float16>(v[0]), static_cast<_Float16>(v[1]),
-                                            static_cast<_Float16>(v[2]), static_cast<_Float16>(v[3])};
-    } else {
+// Stores N consecutive columns n..n+N-1 of row r, rounding once to binary16
+// where Y is that.  Rows of odd n start anywhere: the vectors ask for no more
+// than their element's alignment, which global memory gives them.
+template <int N>
+__device__ __forceinline__ void store_f16(const TileArgs& a, int64_t r, int64_t n, const float* v) {
+  typedef _Float16 hu __attribute__((ext_vector_type(N), aligned(2)));
+  _Float16* y = static_cast<_Float16*>(a.y) + r * a.n + n;
+  if (n + N <= a.n) {
+    hu h;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (n + q < a.n) y[at + q] = static_cast<_Float16>(v[q]);
-    }
+    for (int q = 0; q < N; ++q) h[q] = static_cast<_Float16>(v[q]);
+    *reinterpret_cast<hu*>(y) = h;
   } else {
-    float* y = static_cast<float*>(a.y);
-    if ((a.n & 3) == 0) {
-      if (n < a.n) *reinterpret_cast<f32x4*>(y + at) = f32x4{v[0], v[1], v[2], v[3]};
-    } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (n + q < a.n) y[at + q] = v[q];
-    }
+    for (int q = 0; q < N - 1; ++q)
+      if (n + q < a.n) y[q] = static_cast<_Float16>(v[q]);
   }
+}
+__device__ __forceinline__ void store_f32(const TileArgs& a, int64_t r, int64_t n, const float* v) {
+  typedef float fu __attribute__((ext_vector_type(4), aligned(4)));
+  float* y = static_cast<float*>(a.y) + r * a.n + n;
+  if (n + 4 <= a.n) {
+    *reinterpret_cast<fu*>(y) = fu{v[0], v[1], v[2], v[3]};
+  } else {
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      if (n + q < a.n) y[q] = v[q];
+  }
+}
+__device__ __forceinline__ void store4(const TileArgs& a, int64_t r, int64_t n, const float* v) {
+  if (a.y_f16)
+    store_f16<4>(a, r, n, v);
+  else
+    store_f32(a, r, n, v);
 }
 
 // Four per-column values (scales or bias) at columns n..n+3 of an [experts][n]
@@ -203,26 +213,44 @@ __device__ __forceinline__ void load4(const float* p, int64_t n, int64_t count, 
   }
 }
 
-// The value of four sums for a row of X with scale xs: for 8-bit operands
-// acc * xs * ws, in this order so that small scales do not meet first and
-// underflow; the integer sum is exact and rounded once to float32.
-template <typename E>
-__device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const float* ws, const float* b, float* v) {
+// The value of four sums for a row of X with scale xs (0: no row of X): for
+// 8-bit operands acc * xs * ws, in this order so that small scales do not
+// meet first and underflow; the integer sum is exact and rounded once to
+// float32.
+template <typename E, typename V>
+__device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const V& ws, const V& b, float* v) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     if constexpr (E::kScaled)
       v[q] = __builtin_fmaf(static_cast<float>(c[q]) * xs, ws[q], b[q]);
     else
-      v[q] = c[q] + b[q];
+      v[q] = (xs == 0.f ? 0.f : c[q]) + b[q];
   }
 }
 
 // ---------------------------------------------------------------------------
 // Tiles staged through LDS.  A workgroup of WM * WN wavefronts owns BM rows
 // of Y and BN rows of W (gated: BN / 2 columns, 16 rows of the gate and 16 of
-// the up projection in turn); K advances 128 bytes at a time through NS
-// buffers.  Loads go from memory straight into LDS, 1 KB (8 rows) per
-// wavefront instruction, NS - 1 steps ahead of the matrix cores.
+// the up projection in turn); K advances 128 bytes a step through two
+// buffers.  Loads go from memory straight into LDS, 1 KB (8 rows of 128
+// bytes, whole cache lines) per wavefront instruction.
+//
+// What bounds it is those loads, not the matrix cores: a step of a 256 x 256
+// tile is 2048 cycles of products per SIMD and 64 KB through the CU's vector
+// memory path.  So they run all the time, one step's worth in flight, and a
+// buffer is refilled in two parts, each as soon as it has been read.  A
+// wavefront takes a step in four phases,
+//
+//   phase  products           reads for the next       refills
+//     0    rows half 0, k 0   half 0, k 1; W k 1
+//     1    half 0, k 1        half 1, k 0              half 0 of X, W
+//     2    half 1, k 0        half 1, k 1              half 0 of X, W
+//     3    half 1, k 1        next step: half 0, W     half 1 of X
+//
+// with a barrier before 1 (half 0 and W are read by all; half 1 has landed)
+// and before 3 (half 1 is read by all; the next step's half 0 and W have
+// landed), and the reads and loads of a phase spread among its products: in
+// a burst they hold up the products of both wavefronts of a SIMD.
 //
 // LDS holds 128-byte rows with their 16-byte chunks permuted, chunk c of row
 // r at place c ^ (r & 7): a wavefront's operand read (16 rows, one chunk
@@ -232,21 +260,27 @@ __device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const
 // K past the row's end (kbytes is a multiple of 32, the step 128) reads a
 // zero chunk; rows past the tile's own read the last row in their place and
 // are not stored.
+//
+// 8192x4096x4096 in 8 bits, binary16 Y: 127 us (2.2 POP/s) in 256 x 256
+// tiles; the products alone (nothing loaded or read) take 78 us.
 // ---------------------------------------------------------------------------
 __device__ __align__(16) const uint8_t kZeroChunk[16] = {0};
 
-template <int BM, int BN, int NS>
-constexpr int tile_lds() { return (BM + BN) * 128 * NS; }
+template <int BM, int BN>
+constexpr int tile_lds() { return (BM + BN) * 128 * 2 + 4 * (BM + 2 * BN); }
 
-template <typename E, int BM, int BN, int WM, int WN, int NS, bool GATED>
+template <typename E, int BM, int BN, int WM, int WN, bool GATED>
 __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   constexpr int kWaves = WM * WN;
   constexpr int kTM = BM / WM / 16, kTN = BN / WN / 16;
-  constexpr int kInstr = (BM + BN) / 8;
-  constexpr int kPer = (kInstr + kWaves - 1) / kWaves;
+  constexpr int kHalf = kTM / 2;
+  static_assert(kTM % 2 == 0, "a wavefront takes its rows of X in two halves");
+  constexpr int kXh = BM / 16 / kWaves, kWn = BN / 8 / kWaves, kPer = 2 * kXh + kWn;
+  static_assert(kXh * kWaves * 16 == BM && kWn * kWaves * 8 == BN, "loads divide evenly among the wavefronts");
+  constexpr int kHalfRows8 = BM / WM / 16;   // 8-row groups in half a wavefront's rows
   constexpr int kStage = (BM + BN) * 128;
   constexpr int kCols = GATED ? BN / 2 : BN;
-  static_assert(!GATED || kTN % 2 == 0, "a wavefront holds gate and up of the same columns");
+  static_assert(kTN % (GATED ? 4 : 2) == 0, "a wavefront holds pairs of sub-tiles, gate and up of the same columns");
   extern __shared__ __align__(16) uint8_t lds[];
   typedef __attribute__((address_space(3))) uint8_t Lds;
   typedef __attribute__((address_space(1))) const uint8_t Glb;
@@ -261,36 +295,65 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   const uint8_t* w2 = GATED ? a.w2 + (at.expert * a.n) * static_cast<int64_t>(a.kbytes) : nullptr;
   const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;   // the same place in every row this lane loads
 
-  // Source row of each of the wavefront's load instructions: X rows first,
-  // then W rows; instruction q fills LDS rows 8q..8q+7.
+  // Columns of a pair of 16-row operands: sub-tile jj's four of lane group g.
+  // In float32 a lane stores four columns at a time and four lanes 64 bytes
+  // in a row; in binary16 the pair's rows of W are taken in an order that
+  // gives a lane eight columns in a row, so that its store is as wide.
+  auto pair_col = [&](int jj, int g) { return a.y_f16 ? 8 * g + 4 * jj : 16 * jj + 4 * g; };
+
+  // Scales and bias of the tile for the epilogue, into LDS: read before the
+  // products so that their latency (the scale of a gathered row is two loads
+  // deep) is not paid after them.  A row without a row of X has scale 0.
+  float* xs_l = reinterpret_cast<float*>(lds + 2 * kStage);
+  float* ws_l = xs_l + BM;
+  float* b_l = ws_l + (GATED ? 2 : 1) * kCols;   // not gated
+  for (int r = threadIdx.x; r < BM; r += kWaves * 64) {
+    const int64_t row = at.row0 + r;
+    bool ok;
+    const int64_t i = x_row(a, row < last ? row : last, &ok);
+    xs_l[r] = ok ? (E::kScaled ? a.xs[i] : 1.f) : 0.f;
+  }
+  for (int c = threadIdx.x; c < kCols; c += kWaves * 64) {
+    const int64_t at_c = at.expert * a.n + (n0 + c < a.n ? n0 + c : a.n - 1);
+    if constexpr (E::kScaled) ws_l[c] = a.ws[at_c];
+    if constexpr (E::kScaled && GATED) ws_l[kCols + c] = a.ws2[at_c];
+    if constexpr (!GATED) b_l[c] = a.bias ? a.bias[at_c] : 0.f;
+  }
+
+  // The wavefront's load instructions of a step and their source rows, 8 LDS
+  // rows each: first those of the first half of every wavefront's rows of X
+  // (kXh) and of W (kWn), then those of the second half of X.
   const uint8_t* src[kPer];
+  int dst[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    int q = wave + kWaves * j;
-    q = q < kInstr ? q : kInstr - 1;
-    const int r = 8 * q + (lane >> 3);
-    if (q < BM / 8) {
-      const int64_t row = at.row0 + r;
+    if (j < kXh || j >= kXh + kWn) {
+      const int h = wave * kXh + (j < kXh ? j : j - kXh - kWn);   // 8 rows among BM / 2
+      const int r8 = h / kHalfRows8 * (2 * kHalfRows8) + h % kHalfRows8 + (j < kXh ? 0 : kHalfRows8);
+      const int64_t row = at.row0 + 8 * r8 + (lane >> 3);
       bool ok;
       const int64_t i = x_row(a, row < last ? row : last, &ok);
       src[j] = a.x + i * a.kbytes + chunk;
+      dst[j] = r8 * 1024;
     } else {
-      const int c = r - BM;
-      const int64_t col = n0 + (GATED ? (c >> 5) * 16 + (c & 15) : c);
+      const int c8 = wave * kWn + j - kXh, c = 8 * c8 + (lane >> 3), sub = GATED ? c >> 5 : c >> 4;
+      const int64_t col = n0 + (sub >> 1) * 32 + pair_col(sub & 1, (c & 15) >> 2) + (c & 3);
       const uint8_t* m = GATED && (c & 16) ? w2 : w;
       src[j] = m + (col < a.n ? col : a.n - 1) * a.kbytes + chunk;
+      dst[j] = (BM / 8 + c8) * 1024;
     }
   }
   const int steps = (a.kbytes + 127) >> 7;
-  auto issue = [&](int s) {
-    Lds* base = (Lds*)lds + (s % NS) * kStage;
+  // Loads j0..j1-1 of step s; past the last step (and past the row's end
+  // within it) they read zeros, so that no phase of the loop has a branch.
+  auto issue = [&](int s, int j0, int j1) {
+    Lds* base = (Lds*)lds + (s & 1) * kStage;
     const bool in = s * 128 + chunk < a.kbytes;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      int q = wave + kWaves * j;
-      q = q < kInstr ? q : kInstr - 1;
+      if (j < j0 || j >= j1) continue;
       const uint8_t* p = in ? src[j] : kZeroChunk;
-      __builtin_amdgcn_global_load_lds((Glb*)p, (__attribute__((address_space(3))) void*)(base + q * 1024), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((Glb*)p, (__attribute__((address_space(3))) void*)(base + dst[j]), 16, 0, 0);
       src[j] += 128;
     }
   };
@@ -301,67 +364,118 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
 #pragma unroll
     for (int j = 0; j < kTN; ++j) acc[i][j] = E::zero();
 
-#pragma unroll
-  for (int s = 0; s < NS - 1; ++s)
-    if (s < steps) issue(s);
   const int wm = wave % WM, wn = wave / WM;
   const int place = ((lane >> 4) ^ (lane & 7)) * 16;
   const int xrow = (wm * kTM * 16 + (lane & 15)) * 128;
   const int wrow = (BM + wn * kTN * 16 + (lane & 15)) * 128;
-  for (int s = 0; s < steps; ++s) {
-    // Step s has landed once at most the later steps' loads are in flight;
-    // the barrier extends that to every wavefront's part and says that all
-    // are done reading step s - 1, whose buffer the next load fills.
-    if (s + NS - 2 < steps)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * kPer) : "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  i32x4 xa[kHalf], xb[kHalf], wa[kTN], wb[kTN];
+  auto read_x = [&](const uint8_t* buf, int half, int ks, i32x4* f) {
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i)
+      f[i] = *reinterpret_cast<const i32x4*>(buf + xrow + (half * kHalf + i) * 2048 + (place ^ (64 * ks)));
+  };
+  auto read_w = [&](const uint8_t* buf, int ks, i32x4* f) {
+#pragma unroll
+    for (int j = 0; j < kTN; ++j) f[j] = *reinterpret_cast<const i32x4*>(buf + wrow + j * 2048 + (place ^ (64 * ks)));
+  };
+  // One phase: the products of half the rows and half a step, among them the
+  // READS of the next phase and LOADS of a later step.
+  auto mma = [&](int half, const i32x4* x, const i32x4* w, auto reads, auto loads) {
+    constexpr int kReads = decltype(reads)::value, kLoads = decltype(loads)::value;
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i)
+#pragma unroll
+      for (int j = 0; j < kTN; ++j) acc[half * kHalf + i][j] = E::mma(w[j], x[i], acc[half * kHalf + i][j]);
+    constexpr int kRun = kHalf * kTN / (kReads + kLoads) < 1 ? 1 : kHalf * kTN / (kReads + kLoads);
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kRun, 0);
+    }
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kRun, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr int kFirst = kXh + kWn, kMid = (kFirst + 1) / 2;
+  constexpr std::integral_constant<int, 0> kNone{};
+  constexpr std::integral_constant<int, kHalf> kX{};
+  constexpr std::integral_constant<int, kHalf + kTN> kXW{};
+  constexpr std::integral_constant<int, kMid> kL1{};
+  constexpr std::integral_constant<int, kFirst - kMid> kL2{};
+  constexpr std::integral_constant<int, kXh> kL3{};
+  // Waits for all but the newest kPer loads and for the reads, then for the
+  // other wavefronts.
+  auto sync = [&]() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kPer) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (s + NS - 1 < steps) issue(s + NS - 1);
-    const uint8_t* buf = lds + (s % NS) * kStage;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      i32x4 xf[kTM], wf[kTN];
-#pragma unroll
-      for (int i = 0; i < kTM; ++i)
-        xf[i] = *reinterpret_cast<const i32x4*>(buf + xrow + i * 2048 + (place ^ (64 * ks)));
-#pragma unroll
-      for (int j = 0; j < kTN; ++j)
-        wf[j] = *reinterpret_cast<const i32x4*>(buf + wrow + j * 2048 + (place ^ (64 * ks)));
-#pragma unroll
-      for (int i = 0; i < kTM; ++i)
-#pragma unroll
-        for (int j = 0; j < kTN; ++j) acc[i][j] = E::mma(wf[j], xf[i], acc[i][j]);
-    }
-  }
+  };
 
+  issue(0, 0, kPer);
+  issue(1, 0, kPer);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kPer + kXh) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  read_x(lds, 0, 0, xa);
+  read_w(lds, 0, wa);
+  __builtin_amdgcn_sched_barrier(0);
+  for (int s = 0; s < steps; ++s) {
+    const uint8_t* buf = lds + (s & 1) * kStage;
+    const uint8_t* next = lds + (~s & 1) * kStage;
+    read_x(buf, 0, 1, xb);
+    read_w(buf, 1, wb);
+    mma(0, xa, wa, kXW, kNone);
+    sync();
+    read_x(buf, 1, 0, xa);
+    issue(s + 2, 0, kMid);
+    mma(0, xb, wb, kX, kL1);
+    read_x(buf, 1, 1, xb);
+    issue(s + 2, kMid, kFirst);
+    mma(1, xa, wa, kX, kL2);
+    sync();
+    read_x(next, 0, 0, xa);   // past the last step: zeros, not used
+    read_w(next, 0, wa);
+    issue(s + 2, kFirst, kPer);
+    mma(1, xb, wb, kXW, kL3);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the last zeros are in before LDS is given up
+
+  // Columns in pairs of sub-tiles (gated: two gates and their two ups).
   const int g = lane >> 4;
-  const float* ws = E::kScaled ? a.ws + at.expert * a.n : nullptr;
-  const float* ws2 = E::kScaled && GATED ? a.ws2 + at.expert * a.n : nullptr;
-  const float* bias = a.bias ? a.bias + at.expert * a.n : nullptr;
+  constexpr int kG = GATED ? 2 : 1;
 #pragma unroll
   for (int i = 0; i < kTM; ++i) {
-    const int64_t row = at.row0 + wm * kTM * 16 + 16 * i + (lane & 15);
-    if (row > last) continue;
-    bool ok;
-    const int64_t xi = x_row(a, row, &ok);
-    const float xs = E::kScaled ? (ok ? a.xs[xi] : 0.f) : 1.f;
+    const int r = (wm * kTM + i) * 16 + (lane & 15);
+    const int64_t row = at.row0 + r;
+    const float xs = xs_l[r];
 #pragma unroll
-    for (int j = 0; j < kTN; j += GATED ? 2 : 1) {
-      const int64_t col = n0 + (wn * kTN * 16 + 16 * j) / (GATED ? 2 : 1) + 4 * g;
-      float s[4] = {1.f, 1.f, 1.f, 1.f}, b[4] = {0.f, 0.f, 0.f, 0.f}, v[4];
-      if (E::kScaled) load4(ws, col, a.n, s);
-      if (!GATED && bias) load4(bias, col, a.n, b);
-      scaled<E>(ok ? acc[i][j] : E::zero(), xs, s, b, v);
-      if constexpr (GATED) {
-        float u[4];
-        if (E::kScaled) load4(ws2, col, a.n, s);
-        scaled<E>(ok ? acc[i][j + 1] : E::zero(), xs, s, b, u);
+    for (int p = 0; p < kTN / (2 * kG); ++p) {
+      const int c0 = (wn * kTN / (2 * kG) + p) * 32;
+      float v[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = silu_mul(v[q], u[q]);
+      for (int jj = 0; jj < 2; ++jj) {
+        const int c = c0 + pair_col(jj, g);
+        const f32x4 s = E::kScaled ? *reinterpret_cast<const f32x4*>(ws_l + c) : f32x4{};
+        const f32x4 b = GATED ? f32x4{0.f, 0.f, 0.f, 0.f} : *reinterpret_cast<const f32x4*>(b_l + c);
+        scaled<E>(acc[i][kG * (2 * p + jj)], xs, s, b, v + 4 * jj);
+        if constexpr (GATED) {
+          const f32x4 s2 = E::kScaled ? *reinterpret_cast<const f32x4*>(ws_l + kCols + c) : f32x4{};
+          float u[4];
+          scaled<E>(acc[i][kG * (2 * p + jj) + 1], xs, s2, b, u);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[4 * jj + q] = silu_mul(v[4 * jj + q], u[q]);
+        }
       }
-      store4(a, row, col, v);
+      if (row > last) continue;
+      if (a.y_f16) {
+        store_f16<8>(a, row, n0 + c0 + 8 * g, v);
+      } else {
+        store_f32(a, row, n0 + c0 + 4 * g, v);
+        store_f32(a, row, n0 + c0 + 16 + 4 * g, v + 4);
+      }
     }
   }
 }
@@ -456,7 +570,7 @@ __global__ __launch_bounds__(NW * 64) void gemm_rows_kernel(TileArgs a) {
     if (row > last) continue;
     bool ok;
     const int64_t xi = x_row(a, row, &ok);
-    const float xs = E::kScaled ? (ok ? a.xs[xi] : 0.f) : 1.f;
+    const float xs = ok ? (E::kScaled ? a.xs[xi] : 1.f) : 0.f;
     const int64_t c0 = n0 + 4 * (l >> 4);
     float v[kG][4];
 #pragma unroll
@@ -467,7 +581,7 @@ __global__ __launch_bounds__(NW * 64) void gemm_rows_kernel(TileArgs a) {
       float s[4] = {1.f, 1.f, 1.f, 1.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
       if (E::kScaled) load4((k ? a.ws2 : a.ws) + at.expert * a.n, c0, a.n, s);
       if (!GATED && bias) load4(bias, c0, a.n, b);
-      scaled<E>(ok ? r : E::zero(), xs, s, b, v[k]);
+      scaled<E>(r, xs, s, b, v[k]);
     }
     if constexpr (GATED)
 #pragma unroll
@@ -505,10 +619,10 @@ inline int launch_tiles(const void* fn, pesti::TileArgs a, int bm, int cols, int
   return hipLaunchKernel(fn, dim3(grid), dim3(threads), params, lds, st) == hipSuccess ? PESTI_OK : PESTI_ERR_LAUNCH;
 }
 
-template <typename E, int BM, int BN, int WM, int WN, int NS, bool GATED>
+template <typename E, int BM, int BN, int WM, int WN, bool GATED>
 int launch_tile(const pesti::TileArgs& a, hipStream_t st) {
-  return launch_tiles(reinterpret_cast<const void*>(&pesti::gemm_tile_kernel<E, BM, BN, WM, WN, NS, GATED>), a, BM,
-                      GATED ? BN / 2 : BN, WM * WN * 64, pesti::tile_lds<BM, BN, NS>(), st);
+  return launch_tiles(reinterpret_cast<const void*>(&pesti::gemm_tile_kernel<E, BM, BN, WM, WN, GATED>), a, BM,
+                      GATED ? BN / 2 : BN, WM * WN * 64, pesti::tile_lds<BM, BN>(), st);
 }
 
 template <typename E, int MT, int NW, int C, bool GATED>
@@ -520,15 +634,33 @@ int launch_rows(const pesti::TileArgs& a, hipStream_t st) {
 // Rows one matrix is multiplied with, on average over the experts.
 inline int64_t mean_rows(const pesti::TileArgs& a) { return (a.rows + a.experts - 1) / a.experts; }
 
+// Tiles of bm rows and bn columns that a launch comes to: experts' rows end
+// on average half a tile early.
+inline int64_t tiles_about(const pesti::TileArgs& a, int bm, int cols) {
+  const int64_t row_tiles = a.offsets ? a.rows / bm + (a.experts + 1) / 2 : (a.rows + bm - 1) / bm;
+  return row_tiles * ((a.n + cols - 1) / cols);
+}
+
 // Row counts up to 32 stream W once through the K-split kernel; above that
-// operands are shared through LDS.
+// operands are shared through LDS, in the largest tile that there are enough
+// of to fill the chip and that the rows of an expert fill: bytes into LDS
+// bound these kernels, and a tile of BM x BN moves (BM + BN) / (BM BN) per
+// product.  Measured (us at 64x128 / 128x128 / 128x256 / 256x256): 8-bit
+// 8192x4096x4096 182 / 162 / 146 / 127; 64 experts, 512 rows each,
+// 2048x1024 163 / 147 / 135 / 127; binary16 SwiGLU of 32 experts, 256 rows
+// each, 1408x2048 189 / 178 / 165 / 183; 8 experts, 255 rows, 2429x1056
+// 28 / 30 / 26 / 37; 8-bit 4096x896x4864 30 / 29 / 35 / 59; 513x2304x768
+// 7.9 / 9.1 / 10.5 / 16.4.
 template <typename E, bool GATED>
 int launch_any(const pesti::TileArgs& a, hipStream_t st) {
+  constexpr int kG = GATED ? 2 : 1;
   const int64_t mean = mean_rows(a);
   if (mean <= 16) return launch_rows<E, 1, 8, 4, GATED>(a, st);
   if (mean <= 32) return launch_rows<E, 2, 8, 2, GATED>(a, st);
-  if (mean <= 64) return launch_tile<E, 64, 64, 2, 2, 3, GATED>(a, st);
-  return launch_tile<E, 128, 128, 2, 2, 2, GATED>(a, st);
+  if (mean > 256 && tiles_about(a, 256, 256 / kG) >= 448) return launch_tile<E, 256, 256, 2, 4, GATED>(a, st);
+  if (mean > 128 && tiles_about(a, 128, 256 / kG) >= 192) return launch_tile<E, 128, 256, 2, 4, GATED>(a, st);
+  if (mean > 64 && tiles_about(a, 128, 128 / kG) >= 192) return launch_tile<E, 128, 128, 2, 2, GATED>(a, st);
+  return launch_tile<E, 64, 128, 2, 2, GATED>(a, st);
 }
 
 }  // namespace pesti_host
