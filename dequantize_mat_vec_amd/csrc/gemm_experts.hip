@@ -25,6 +25,7 @@ int run(int32_t format, pesti::TileArgs a, int64_t experts, int64_t in_features,
   if (a.rows < 0 || a.rows > PESTI_MAX_TOKENS || a.x_tokens < 0 || a.x_tokens > PESTI_MAX_TOKENS)
     return PESTI_ERR_BATCH;
   if (!a.x_rows && a.x_tokens < a.rows) return PESTI_ERR_BATCH;
+  if (a.x_rows && a.x_tokens * in_features * (i8 ? 1 : 2) > UINT32_MAX - 15) return PESTI_ERR_SHAPE;
   if (a.rows == 0 || a.n == 0 || experts == 0) return PESTI_OK;
   const bool data = in_features > 0 && a.x_tokens > 0;
   if (!a.y || !a.offsets) return PESTI_ERR_NULL;

@@ -257,20 +257,28 @@ __device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const
 // each per lane group) then spreads over all banks.  The permutation is made
 // by the lanes' source addresses, the destination being linear.
 //
-// K past the row's end (kbytes is a multiple of 32, the step 128) reads a
-// zero chunk; rows past the tile's own read the last row in their place and
+// K past the row's end (kbytes is a multiple of 32, the step 128) reads
+// zeros; rows past the tile's own read the last row in their place and
 // are not stored.
 //
 // 8192x4096x4096 in 8 bits, binary16 Y: 127 us (2.2 POP/s) in 256 x 256
 // tiles; the products alone (nothing loaded or read) take 78 us.
 // ---------------------------------------------------------------------------
-__device__ __align__(16) const uint8_t kZeroChunk[16] = {0};
+#ifdef __HIP_DEVICE_COMPILE__   // the host compiler has no buffer descriptors, and needs only the kernel's name
+typedef __amdgpu_buffer_rsrc_t BufferRsrc;
+constexpr uint32_t kNoOffset = 0xFFFFFFF0u;   // past the end of every buffer
+__device__ __forceinline__ BufferRsrc buffer_of(const uint8_t* p, int64_t bytes) {
+  // raw 32-bit data, no stride or swizzle; at most 2^32 - 16 bytes
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, static_cast<int>(bytes), 0x00020000);
+}
+#endif
 
 template <int BM, int BN>
 constexpr int tile_lds() { return (BM + BN) * 128 * 2 + 4 * (BM + 2 * BN); }
 
 template <typename E, int BM, int BN, int WM, int WN, bool GATED>
 __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__
   constexpr int kWaves = WM * WN;
   constexpr int kTM = BM / WM / 16, kTN = BN / WN / 16;
   constexpr int kHalf = kTM / 2;
@@ -283,7 +291,6 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   static_assert(kTN % (GATED ? 4 : 2) == 0, "a wavefront holds pairs of sub-tiles, gate and up of the same columns");
   extern __shared__ __align__(16) uint8_t lds[];
   typedef __attribute__((address_space(3))) uint8_t Lds;
-  typedef __attribute__((address_space(1))) const uint8_t Glb;
 
   TileAt at;
   if (!find_tile<BM>(a, &at)) return;
@@ -293,6 +300,7 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   const int64_t last = at.row_end - 1;
   const uint8_t* w = a.w + (at.expert * a.n) * static_cast<int64_t>(a.kbytes);
   const uint8_t* w2 = GATED ? a.w2 + (at.expert * a.n) * static_cast<int64_t>(a.kbytes) : nullptr;
+  const int w_rows = a.n - n0 < kCols ? static_cast<int>(a.n - n0) : kCols;
   const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;   // the same place in every row this lane loads
 
   // Columns of a pair of 16-row operands: sub-tile jj's four of lane group g.
@@ -323,7 +331,15 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   // The wavefront's load instructions of a step and their source rows, 8 LDS
   // rows each: first those of the first half of every wavefront's rows of X
   // (kXh) and of W (kWn), then those of the second half of X.
-  const uint8_t* src[kPer];
+  // Addresses are 32-bit offsets from bases that do not change, the step in
+  // a scalar register: with 64-bit addresses advanced per step the vector
+  // ALU work of the loads cost 5-8% (8192x4096x4096 124 against 116 us).  An
+  // offset past the end loads zeros.
+  const int64_t x0 = a.x_rows ? 0 : at.row0;
+  const BufferRsrc rx = buffer_of(a.x + x0 * a.kbytes, (a.x_rows ? a.x_tokens : a.x_tokens - x0 < BM ? a.x_tokens - x0 : BM) * a.kbytes);
+  const BufferRsrc rw = buffer_of(w + n0 * a.kbytes, w_rows * a.kbytes);
+  const BufferRsrc rw2 = GATED ? buffer_of(w2 + n0 * a.kbytes, w_rows * a.kbytes) : rw;
+  uint32_t src[kPer];
   int dst[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -332,14 +348,13 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
       const int r8 = h / kHalfRows8 * (2 * kHalfRows8) + h % kHalfRows8 + (j < kXh ? 0 : kHalfRows8);
       const int64_t row = at.row0 + 8 * r8 + (lane >> 3);
       bool ok;
-      const int64_t i = x_row(a, row < last ? row : last, &ok);
-      src[j] = a.x + i * a.kbytes + chunk;
+      const int64_t i = x_row(a, row < last ? row : last, &ok) - x0;
+      src[j] = static_cast<uint32_t>((ok ? i : 0) * a.kbytes + chunk);
       dst[j] = r8 * 1024;
     } else {
       const int c8 = wave * kWn + j - kXh, c = 8 * c8 + (lane >> 3), sub = GATED ? c >> 5 : c >> 4;
-      const int64_t col = n0 + (sub >> 1) * 32 + pair_col(sub & 1, (c & 15) >> 2) + (c & 3);
-      const uint8_t* m = GATED && (c & 16) ? w2 : w;
-      src[j] = m + (col < a.n ? col : a.n - 1) * a.kbytes + chunk;
+      const int col = (sub >> 1) * 32 + pair_col(sub & 1, (c & 15) >> 2) + (c & 3);
+      src[j] = static_cast<uint32_t>(col < w_rows ? col : w_rows - 1) * a.kbytes + chunk;
       dst[j] = (BM / 8 + c8) * 1024;
     }
   }
@@ -352,9 +367,11 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       if (j < j0 || j >= j1) continue;
-      const uint8_t* p = in ? src[j] : kZeroChunk;
-      __builtin_amdgcn_global_load_lds((Glb*)p, (__attribute__((address_space(3))) void*)(base + dst[j]), 16, 0, 0);
-      src[j] += 128;
+      const bool is_x = j < kXh || j >= kXh + kWn;
+      const bool up = GATED && ((wave * kWn + j - kXh) & 2);   // 16 rows of the gate, 16 of the up projection
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? rx : (up ? rw2 : rw),
+                                               (__attribute__((address_space(3))) void*)(base + dst[j]), 16,
+                                               in ? src[j] : kNoOffset, s * 128, 0, 0);
     }
   };
 
@@ -478,6 +495,7 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
       }
     }
   }
+#endif
 }
 
 // ---------------------------------------------------------------------------

@@ -390,7 +390,9 @@ int pesti_gemm_i8row_i8token(int64_t m, int64_t out_features, int64_t in_feature
  *   x_rows   int32 [rows] in device memory, the row of X for each row of Y
  *            (the same one any number of times), or NULL for row r itself,
  *            which needs x_tokens >= rows (else PESTI_ERR_BATCH).  An index
- *            outside 0..x_tokens-1 stands for a row of zeros.
+ *            outside 0..x_tokens-1 stands for a row of zeros.  Rows that are
+ *            picked are addressed in 32 bits: X of 4 GiB or more with x_rows
+ *            is PESTI_ERR_SHAPE.
  *   y        [rows][out] in y_format (PESTI_FMT_F32 or PESTI_FMT_F16)
  *
  * pesti_gemm_experts_swiglu joins the gate and up products of the same rows

@@ -89,6 +89,9 @@ def test_experts_refusals(gated):
     for kw in (dict(rows=-1), dict(rows=MOST + 1, t=MOST), dict(t=-1), dict(t=MOST + 1)):
         assert call(**kw) == _lib.PESTI_ERR_BATCH
     assert call(rows=5, t=4) == _lib.PESTI_ERR_BATCH        # no x_rows: row r of X itself
+    # picked rows are addressed in 32 bits
+    for fmt, t in ((F16, 1 << 16), (I8, 1 << 17)):
+        assert call(fmt=fmt, k=32768, t=t, at=FAKE) == _lib.PESTI_ERR_SHAPE
     names = ["off", "w", "ws", "x", "xs", "y"] + (["w2", "ws2"] if gated else [])
     for name in names:
         assert call(**{name: None}) == _lib.PESTI_ERR_NULL, name
