@@ -67,26 +67,6 @@ struct TileAt {
   int nt;
 };
 
-// The t-th of `total` tiles for workgroup b.  Workgroups go to the 8 XCDs in
-// turn, each with its own L2: XCD b % 8 takes a contiguous run of tiles, and
-// the run walks groups of 8 row tiles column by column, so the workgroups
-// that one XCD runs at a time share rows of X and of W.
-__device__ __forceinline__ bool tile_of(int64_t b, int64_t row_tiles, int64_t col_tiles, int64_t* mt, int* nt) {
-  const int64_t total = row_tiles * col_tiles;
-  const int64_t xcd = b % kXcds, slot = b / kXcds;
-  const int64_t per = total / kXcds, rem = total % kXcds;
-  if (slot >= per + (xcd < rem ? 1 : 0)) return false;
-  const uint32_t lin = static_cast<uint32_t>(xcd * per + (xcd < rem ? xcd : rem) + slot);   // below 2^31
-  constexpr uint32_t kGroup = 8;
-  const uint32_t width = kGroup * static_cast<uint32_t>(col_tiles);
-  const uint32_t g = lin / width, in = lin % width;
-  const uint32_t left = static_cast<uint32_t>(row_tiles) - g * kGroup;
-  const uint32_t gm = left < kGroup ? left : kGroup;
-  *mt = g * kGroup + in % gm;
-  *nt = static_cast<int>(in / gm);
-  return true;
-}
-
 // First and last row of expert e, kept inside 0..rows whatever the offsets hold.
 __device__ __forceinline__ void expert_rows(const TileArgs& a, int e, int* first, int* last) {
   const int rows = static_cast<int>(a.rows);
@@ -97,61 +77,105 @@ __device__ __forceinline__ void expert_rows(const TileArgs& a, int e, int* first
   *last = l;
 }
 
-// Inclusive sum over the lanes of a wavefront.
+// Inclusive sum over the lanes of a wavefront: within rows of 16 lanes, then
+// each row's last lane into the rows after it.
 __device__ __forceinline__ int wave_scan(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d, 64);
-    if (lane >= d) v += o;
-  }
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31 into rows 2 and 3
   return v;
 }
 
-// The tile of this workgroup: every wavefront finds it by itself, 64 experts
-// at a time.  An expert of c rows has ceil(c / BM) row tiles; their total is
-// known only here, so the grid is launched for the most there can be and the
-// workgroups past the total leave.
-template <int BM>
-__device__ __forceinline__ bool find_tile(const TileArgs& a, TileAt* at) {
-  int64_t mt = 0;
-  if (!a.offsets) {
-    if (!tile_of(blockIdx.x, (a.rows + BM - 1) / BM, a.tiles_n, &mt, &at->nt)) return false;
-    at->expert = 0;
-    at->row0 = mt * BM;
-    at->row_end = a.rows;
+// Where the tiles are.  An expert of c rows has ceil(c / BM) row tiles; their
+// total is known only here, so the grid is launched for the most there can be
+// and workgroups without a tile leave.  Every wavefront looks tiles up by
+// itself, in LDS: per expert the row tiles up to its end and its first and
+// last row.  A kernel that looks up one tile (ONE) keeps up to 64 experts in
+// a register of its lanes instead, without a barrier; in the others these
+// registers were spilled.
+template <int BM, bool ONE>
+struct TileMap {
+  int f, l, incl;   // ONE: of expert `lane`
+  int row_tiles;
+  int* table;       // [3][experts]
+
+  // Called by all threads of the workgroup.
+  __device__ __forceinline__ void init(const TileArgs& a, int* table_lds) {
+    table = table_lds;
+    if (!a.offsets) {
+      row_tiles = static_cast<int>((a.rows + BM - 1) / BM);
+      return;
+    }
+    const int lane = threadIdx.x & 63;
+    if (ONE && a.experts <= 64) {
+      f = l = 0;
+      if (lane < a.experts) expert_rows(a, lane, &f, &l);
+      incl = wave_scan((l - f + BM - 1) / BM);
+      row_tiles = __builtin_amdgcn_readlane(incl, 63);
+      return;
+    }
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+      int first, last;
+      expert_rows(a, e, &first, &last);
+      table[e] = (last - first + BM - 1) / BM;
+      table[a.experts + e] = first;
+      table[2 * a.experts + e] = last;
+    }
+    __syncthreads();
+    row_tiles = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 64) {
+      const int sum = row_tiles + wave_scan(e0 + lane < a.experts ? table[e0 + lane] : 0);
+      row_tiles = __builtin_amdgcn_readlane(sum, 63);
+      __syncthreads();   // all wavefronts have read these 64; the first replaces them
+      if (e0 + lane < a.experts && threadIdx.x < 64) table[e0 + lane] = sum;
+    }
+    __syncthreads();
+  }
+
+  // Rows and expert of row tile mt (below row_tiles).
+  __device__ __forceinline__ void rows_of(const TileArgs& a, int mt, TileAt* at) const {
+    int e = 0, first = 0, last = static_cast<int>(a.rows), before = 0;
+    if (ONE && a.offsets && a.experts <= 64) {
+      e = __builtin_ctzll(__ballot(incl > mt));
+      first = __builtin_amdgcn_readlane(f, e);
+      last = __builtin_amdgcn_readlane(l, e);
+      before = __builtin_amdgcn_readlane(incl, e) - (last - first + BM - 1) / BM;
+    } else if (a.offsets) {
+      const int lane = threadIdx.x & 63;
+      for (int e0 = 0; e0 < a.experts; e0 += 64)   // experts whose tiles all come before mt
+        e += __builtin_popcountll(__ballot(e0 + lane < a.experts && table[e0 + lane] <= mt));
+      first = __builtin_amdgcn_readfirstlane(table[a.experts + e]);
+      last = __builtin_amdgcn_readfirstlane(table[2 * a.experts + e]);
+      before = e ? __builtin_amdgcn_readfirstlane(table[e - 1]) : 0;
+    }
+    at->expert = e;
+    at->row0 = first + static_cast<int64_t>(mt - before) * BM;
+    at->row_end = last;
+  }
+
+  // The i-th tile of XCD `xcd`; false past its last.  Workgroups go to the 8
+  // XCDs in turn, each with its own L2: an XCD takes a contiguous run of
+  // tiles, and the run walks groups of 8 row tiles column by column, so the
+  // workgroups that one XCD runs at a time share rows of X and of W.
+  __device__ __forceinline__ bool find(const TileArgs& a, uint32_t xcd, int64_t i, TileAt* at) const {
+    const int64_t total = static_cast<int64_t>(row_tiles) * a.tiles_n;
+    const int64_t per = total / kXcds;
+    const uint32_t rem = static_cast<uint32_t>(total % kXcds);
+    if (i >= per + (xcd < rem ? 1 : 0)) return false;
+    const uint32_t lin = static_cast<uint32_t>(xcd * per + (xcd < rem ? xcd : rem) + i);   // below 2^31
+    constexpr uint32_t kGroup = 8;
+    const uint32_t width = kGroup * static_cast<uint32_t>(a.tiles_n);
+    const uint32_t g = lin / width, in = lin % width;
+    const uint32_t left = static_cast<uint32_t>(row_tiles) - g * kGroup;
+    const uint32_t gm = left < kGroup ? left : kGroup;
+    at->nt = static_cast<int>(in / gm);
+    rows_of(a, static_cast<int>(g * kGroup + in % gm), at);
     return true;
   }
-  const int lane = threadIdx.x & 63;
-  int f = 0, l = 0, incl = 0, total = 0;
-  for (int e0 = 0; e0 < a.experts; e0 += 64) {
-    f = l = 0;
-    if (e0 + lane < a.experts) expert_rows(a, e0 + lane, &f, &l);
-    incl = wave_scan((l - f + BM - 1) / BM);
-    total += __builtin_amdgcn_readlane(incl, 63);
-  }
-  if (!tile_of(blockIdx.x, total, a.tiles_n, &mt, &at->nt)) return false;
-  int left = static_cast<int>(mt);
-  for (int e0 = 0; e0 < a.experts; e0 += 64) {
-    if (a.experts > 64) {
-      f = l = 0;
-      if (e0 + lane < a.experts) expert_rows(a, e0 + lane, &f, &l);
-      incl = wave_scan((l - f + BM - 1) / BM);
-    }
-    const uint64_t past = __ballot(incl > left);
-    if (past) {
-      const int s = __builtin_ctzll(past);
-      const int first = __builtin_amdgcn_readlane(f, s), last = __builtin_amdgcn_readlane(l, s);
-      const int before = __builtin_amdgcn_readlane(incl, s) - (last - first + BM - 1) / BM;
-      at->expert = e0 + s;
-      at->row0 = first + static_cast<int64_t>(left - before) * BM;
-      at->row_end = last;
-      return true;
-    }
-    left -= __builtin_amdgcn_readlane(incl, 63);
-  }
-  return false;
-}
+};
 
 // Row of X for row r of Y; *ok says whether there is one (an index outside
 // X stands for a row of zeros: row 0 is loaded in its place and dropped).
@@ -261,10 +285,25 @@ __device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const
 // zeros; rows past the tile's own read the last row in their place and
 // are not stored.
 //
-// 8192x4096x4096 in 8 bits, binary16 Y: 127 us (2.2 POP/s) in 256 x 256
+// The grid fills the chip once and a workgroup takes tiles in turn, the loads
+// of the next tile's first two steps running under the last steps and the
+// epilogue of the one before: with a workgroup per tile, finding it, filling
+// the buffers and storing took 59 of 127 us for 64 experts of 512 rows,
+// 2048 x 1024 (now 114; the K loop alone about 70).
+//
+// 8192x4096x4096 in 8 bits, binary16 Y: 114 us (2.4 POP/s) in 256 x 256
 // tiles; the products alone (nothing loaded or read) take 78 us.
 // ---------------------------------------------------------------------------
 #ifdef __HIP_DEVICE_COMPILE__   // the host compiler has no buffer descriptors, and needs only the kernel's name
+// A value that what is computed from it is computed from again: the compiler
+// would take such sums of lane numbers out of the loop over tiles, at the
+// price of registers that its 256 x 256 instance does not have (it reloaded
+// them one by one, each time waiting for all loads in flight).
+__device__ __forceinline__ int again(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 typedef __amdgpu_buffer_rsrc_t BufferRsrc;
 constexpr uint32_t kNoOffset = 0xFFFFFFF0u;   // past the end of every buffer
 __device__ __forceinline__ BufferRsrc buffer_of(const uint8_t* p, int64_t bytes) {
@@ -274,7 +313,11 @@ __device__ __forceinline__ BufferRsrc buffer_of(const uint8_t* p, int64_t bytes)
 #endif
 
 template <int BM, int BN>
-constexpr int tile_lds() { return (BM + BN) * 128 * 2 + 4 * (BM + 2 * BN); }
+constexpr int tile_lds() { return (BM + BN) * 128 * 2 + 2 * 4 * (BM + 2 * BN) + 4 * BM; }
+// Steps of a tile at least: what is loaded for the next tile's turn (rows of
+// X at a tile's start, scales two steps before its end) has then been waited
+// for by the steps' own waits when it is read.
+constexpr int kMinSteps = 4;
 
 template <typename E, int BM, int BN, int WM, int WN, bool GATED>
 __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
@@ -291,17 +334,27 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   static_assert(kTN % (GATED ? 4 : 2) == 0, "a wavefront holds pairs of sub-tiles, gate and up of the same columns");
   extern __shared__ __align__(16) uint8_t lds[];
   typedef __attribute__((address_space(3))) uint8_t Lds;
-
-  TileAt at;
-  if (!find_tile<BM>(a, &at)) return;
+  typedef __attribute__((address_space(3))) void LdsAny;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t n0 = static_cast<int64_t>(at.nt) * kCols;
-  const int64_t last = at.row_end - 1;
-  const uint8_t* w = a.w + (at.expert * a.n) * static_cast<int64_t>(a.kbytes);
-  const uint8_t* w2 = GATED ? a.w2 + (at.expert * a.n) * static_cast<int64_t>(a.kbytes) : nullptr;
-  const int w_rows = a.n - n0 < kCols ? static_cast<int>(a.n - n0) : kCols;
+  const int tid = threadIdx.x;
+
+  // LDS: two steps of X and W; two sets of the scales and bias that epilogues
+  // read; rows of X of the next tile; the tile table.
+  constexpr int kSet = 4 * (BM + 2 * BN);
+  const int sets = 2 * kStage, index = sets + 2 * kSet;
+  int* const index_l = reinterpret_cast<int*>(lds + index);
+  TileMap<BM, false> map;
+  map.init(a, index_l + BM);
+  const uint32_t xcd = blockIdx.x % kXcds;
+  const int64_t slots = gridDim.x / kXcds;
+  int64_t ith = blockIdx.x / kXcds;
+  TileAt at, to;
+  if (!map.find(a, xcd, ith, &at)) return;
+
   const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;   // the same place in every row this lane loads
+  const int last_step = (a.kbytes + 127) >> 7;
+  const int steps = last_step < kMinSteps ? kMinSteps : last_step;
 
   // Columns of a pair of 16-row operands: sub-tile jj's four of lane group g.
   // In float32 a lane stores four columns at a time and four lanes 64 bytes
@@ -309,78 +362,102 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   // gives a lane eight columns in a row, so that its store is as wide.
   auto pair_col = [&](int jj, int g) { return a.y_f16 ? 8 * g + 4 * jj : 16 * jj + 4 * g; };
 
-  // Scales and bias of the tile for the epilogue, into LDS: read before the
-  // products so that their latency (the scale of a gathered row is two loads
-  // deep) is not paid after them.  A row without a row of X has scale 0.
-  float* xs_l = reinterpret_cast<float*>(lds + 2 * kStage);
-  float* ws_l = xs_l + BM;
-  float* b_l = ws_l + (GATED ? 2 : 1) * kCols;   // not gated
-  for (int r = threadIdx.x; r < BM; r += kWaves * 64) {
-    const int64_t row = at.row0 + r;
-    bool ok;
-    const int64_t i = x_row(a, row < last ? row : last, &ok);
-    xs_l[r] = ok ? (E::kScaled ? a.xs[i] : 1.f) : 0.f;
-  }
-  for (int c = threadIdx.x; c < kCols; c += kWaves * 64) {
-    const int64_t at_c = at.expert * a.n + (n0 + c < a.n ? n0 + c : a.n - 1);
-    if constexpr (E::kScaled) ws_l[c] = a.ws[at_c];
-    if constexpr (E::kScaled && GATED) ws_l[kCols + c] = a.ws2[at_c];
-    if constexpr (!GATED) b_l[c] = a.bias ? a.bias[at_c] : 0.f;
-  }
-
-  // The wavefront's load instructions of a step and their source rows, 8 LDS
-  // rows each: first those of the first half of every wavefront's rows of X
-  // (kXh) and of W (kWn), then those of the second half of X.
-  // Addresses are 32-bit offsets from bases that do not change, the step in
-  // a scalar register: with 64-bit addresses advanced per step the vector
-  // ALU work of the loads cost 5-8% (8192x4096x4096 124 against 116 us).  An
-  // offset past the end loads zeros.
-  const int64_t x0 = a.x_rows ? 0 : at.row0;
-  const BufferRsrc rx = buffer_of(a.x + x0 * a.kbytes, (a.x_rows ? a.x_tokens : a.x_tokens - x0 < BM ? a.x_tokens - x0 : BM) * a.kbytes);
-  const BufferRsrc rw = buffer_of(w + n0 * a.kbytes, w_rows * a.kbytes);
-  const BufferRsrc rw2 = GATED ? buffer_of(w2 + n0 * a.kbytes, w_rows * a.kbytes) : rw;
+  // The wavefront's load instructions of a step, 8 LDS rows each: first those
+  // of the first half of every wavefront's rows of X (kXh) and of W (kWn),
+  // then those of the second half of X.  Addresses are 32-bit offsets from
+  // bases that stay for a tile, the step in a scalar register: with 64-bit
+  // addresses advanced per step the vector ALU work of the loads cost 5-8%
+  // (8192x4096x4096 124 against 116 us).  An offset past the end loads zeros.
   uint32_t src[kPer];
   int dst[kPer];
+  BufferRsrc rx, rw, rw2;
+  uint32_t limit;   // bytes of a row that loads may reach: 0 where there is no tile
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     if (j < kXh || j >= kXh + kWn) {
       const int h = wave * kXh + (j < kXh ? j : j - kXh - kWn);   // 8 rows among BM / 2
-      const int r8 = h / kHalfRows8 * (2 * kHalfRows8) + h % kHalfRows8 + (j < kXh ? 0 : kHalfRows8);
-      const int64_t row = at.row0 + 8 * r8 + (lane >> 3);
-      bool ok;
-      const int64_t i = x_row(a, row < last ? row : last, &ok) - x0;
-      src[j] = static_cast<uint32_t>((ok ? i : 0) * a.kbytes + chunk);
-      dst[j] = r8 * 1024;
+      dst[j] = (h / kHalfRows8 * (2 * kHalfRows8) + h % kHalfRows8 + (j < kXh ? 0 : kHalfRows8)) * 1024;
     } else {
-      const int c8 = wave * kWn + j - kXh, c = 8 * c8 + (lane >> 3), sub = GATED ? c >> 5 : c >> 4;
-      const int col = (sub >> 1) * 32 + pair_col(sub & 1, (c & 15) >> 2) + (c & 3);
-      src[j] = static_cast<uint32_t>(col < w_rows ? col : w_rows - 1) * a.kbytes + chunk;
-      dst[j] = (BM / 8 + c8) * 1024;
+      dst[j] = (BM / 8 + wave * kWn + j - kXh) * 1024;
     }
   }
-  const int steps = (a.kbytes + 127) >> 7;
-  // Loads j0..j1-1 of step s; past the last step (and past the row's end
-  // within it) they read zeros, so that no phase of the loop has a branch.
-  auto issue = [&](int s, int j0, int j1) {
-    Lds* base = (Lds*)lds + (s & 1) * kStage;
-    const bool in = s * 128 + chunk < a.kbytes;
+  // Rows of X that tile t picks, into LDS (a load, to be waited for).
+  auto load_index = [&](const TileAt& t) {
+    if (a.x_rows && wave < BM / 64) {
+      const int64_t rows = t.row_end - t.row0 < BM ? t.row_end - t.row0 : BM;   // past them: row 0, not stored
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          buffer_of(reinterpret_cast<const uint8_t*>(a.x_rows + t.row0), rows * 4),
+          (LdsAny*)((Lds*)lds + index + wave * 256), 4, tid * 4, 0, 0, 0);
+    }
+  };
+  // Turns the loads to tile t (its rows of X in LDS), and starts the loads of
+  // its scales and bias into set `set`: they are read by an epilogue at the
+  // earliest kMinSteps steps later.  A row without a row of X has scale 0.
+  auto turn_to = [&](const TileAt& t, int set) {
+    const int tid = again(threadIdx.x), lane = tid & 63;
+    const int64_t n0 = static_cast<int64_t>(t.nt) * kCols, first = t.expert * a.n + n0;
+    const int cols = a.n - n0 < kCols ? static_cast<int>(a.n - n0) : kCols;
+    const int rows = t.row_end - t.row0 < BM ? static_cast<int>(t.row_end - t.row0) : BM;
+    const int64_t x0 = a.x_rows ? 0 : t.row0, x_left = a.x_tokens - x0;
+    rx = buffer_of(a.x + x0 * a.kbytes, (a.x_rows ? a.x_tokens : x_left < BM ? (x_left < 0 ? 0 : x_left) : BM) * a.kbytes);
+    rw = buffer_of(a.w + first * a.kbytes, static_cast<int64_t>(cols) * a.kbytes);
+    if constexpr (GATED) rw2 = buffer_of(a.w2 + first * a.kbytes, static_cast<int64_t>(cols) * a.kbytes);
+    limit = a.kbytes;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (j < kXh || j >= kXh + kWn) {
+        int r = dst[j] / 128 + (lane >> 3);
+        r = r < rows ? r : rows - 1;
+        const int i = a.x_rows ? index_l[r] : r;
+        // a row that there is not loads zeros; its products are dropped below
+        src[j] = i >= 0 && i < (a.x_rows ? a.x_tokens : x_left) ? static_cast<uint32_t>(i) * a.kbytes + chunk : kNoOffset;
+      } else {
+        const int c = dst[j] / 128 - BM + (lane >> 3), sub = GATED ? c >> 5 : c >> 4;
+        const int col = (sub >> 1) * 32 + pair_col(sub & 1, (c & 15) >> 2) + (c & 3);
+        src[j] = static_cast<uint32_t>(col < cols ? col : cols - 1) * a.kbytes + chunk;
+      }
+    }
+    Lds* to_l = (Lds*)lds + sets + set * kSet + wave * 256;
+    if (wave < BM / 64) {
+      const int i = a.x_rows ? index_l[tid < rows ? tid : 0] : tid;
+      const bool ok = i >= 0 && i < (a.x_rows ? a.x_tokens : x_left);
+      if constexpr (E::kScaled)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            buffer_of(reinterpret_cast<const uint8_t*>(a.xs + x0), (a.x_tokens - x0) * 4), (LdsAny*)to_l, 4,
+            ok ? static_cast<uint32_t>(i) * 4 : kNoOffset, 0, 0, 0);
+      else
+        *reinterpret_cast<float*>(lds + sets + set * kSet + tid * 4) = ok ? 1.f : 0.f;
+    }
+    if (wave < kCols / 64) {
+      const uint32_t o = tid * 4;
+      if constexpr (E::kScaled)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(reinterpret_cast<const uint8_t*>(a.ws + first), cols * 4),
+                                                 (LdsAny*)(to_l + 4 * BM), 4, o, 0, 0, 0);
+      if constexpr (E::kScaled && GATED)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(reinterpret_cast<const uint8_t*>(a.ws2 + first), cols * 4),
+                                                 (LdsAny*)(to_l + 4 * (BM + kCols)), 4, o, 0, 0, 0);
+      if constexpr (!GATED)   // without a bias every offset is past the end: zeros
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            buffer_of(reinterpret_cast<const uint8_t*>(a.bias ? a.bias + first : nullptr), a.bias ? cols * 4 : 0),
+            (LdsAny*)(to_l + 4 * (BM + kCols)), 4, o, 0, 0, 0);
+    }
+  };
+  // Loads j0..j1-1 of step s of the tile turned to, into buffer `buf`; past
+  // the row's end they read zeros, so that no phase of the loop has a branch.
+  auto issue = [&](int s, int buf, int j0, int j1) {
+    Lds* base = (Lds*)lds + buf * kStage;
+    const bool in = static_cast<uint32_t>(s * 128 + chunk) < limit;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       if (j < j0 || j >= j1) continue;
       const bool is_x = j < kXh || j >= kXh + kWn;
       const bool up = GATED && ((wave * kWn + j - kXh) & 2);   // 16 rows of the gate, 16 of the up projection
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? rx : (up ? rw2 : rw),
-                                               (__attribute__((address_space(3))) void*)(base + dst[j]), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? rx : (up ? rw2 : rw), (LdsAny*)(base + dst[j]), 16,
                                                in ? src[j] : kNoOffset, s * 128, 0, 0);
     }
   };
 
   typename E::Acc acc[kTM][kTN];
-#pragma unroll
-  for (int i = 0; i < kTM; ++i)
-#pragma unroll
-    for (int j = 0; j < kTN; ++j) acc[i][j] = E::zero();
-
   const int wm = wave % WM, wn = wave / WM;
   const int place = ((lane >> 4) ^ (lane & 7)) * 16;
   const int xrow = (wm * kTM * 16 + (lane & 15)) * 128;
@@ -423,78 +500,111 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   constexpr std::integral_constant<int, kMid> kL1{};
   constexpr std::integral_constant<int, kFirst - kMid> kL2{};
   constexpr std::integral_constant<int, kXh> kL3{};
-  // Waits for all but the newest kPer loads and for the reads, then for the
+  // Waits for all but the newest kPer loads and for the reads; then for the
   // other wavefronts.
-  auto sync = [&]() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kPer) : "memory");
+  auto sync = [&](bool loads) {
+    if (loads) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPer) : "memory");
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
 
-  issue(0, 0, kPer);
-  issue(1, 0, kPer);
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kPer + kXh) : "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+  if (a.x_rows) {
+    load_index(at);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    sync(false);
+  }
+  turn_to(at, 0);
+  issue(0, 0, 0, kPer);
+  issue(1, 1, 0, kPer);
+  sync(true);
   read_x(lds, 0, 0, xa);
   read_w(lds, 0, wa);
-  __builtin_amdgcn_sched_barrier(0);
-  for (int s = 0; s < steps; ++s) {
-    const uint8_t* buf = lds + (s & 1) * kStage;
-    const uint8_t* next = lds + (~s & 1) * kStage;
-    read_x(buf, 0, 1, xb);
-    read_w(buf, 1, wb);
-    mma(0, xa, wa, kXW, kNone);
-    sync();
-    read_x(buf, 1, 0, xa);
-    issue(s + 2, 0, kMid);
-    mma(0, xb, wb, kX, kL1);
-    read_x(buf, 1, 1, xb);
-    issue(s + 2, kMid, kFirst);
-    mma(1, xa, wa, kX, kL2);
-    sync();
-    read_x(next, 0, 0, xa);   // past the last step: zeros, not used
-    read_w(next, 0, wa);
-    issue(s + 2, kFirst, kPer);
-    mma(1, xb, wb, kXW, kL3);
-  }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the last zeros are in before LDS is given up
-
-  // Columns in pairs of sub-tiles (gated: two gates and their two ups).
-  const int g = lane >> 4;
-  constexpr int kG = GATED ? 2 : 1;
+  int buf = 0, set = 0;
+  for (;;) {
+    ith += slots;
+    const bool more = map.find(a, xcd, ith, &to);
+    if (more) load_index(to);
 #pragma unroll
-  for (int i = 0; i < kTM; ++i) {
-    const int r = (wm * kTM + i) * 16 + (lane & 15);
-    const int64_t row = at.row0 + r;
-    const float xs = xs_l[r];
+    for (int i = 0; i < kTM; ++i)
 #pragma unroll
-    for (int p = 0; p < kTN / (2 * kG); ++p) {
-      const int c0 = (wn * kTN / (2 * kG) + p) * 32;
-      float v[8];
+      for (int j = 0; j < kTN; ++j) acc[i][j] = E::zero();
+    __builtin_amdgcn_sched_barrier(0);
+    // The loads run two steps ahead: in the last two steps of a tile they
+    // are the first two of the next.
+    for (int s = 0; s < steps; ++s) {
+      const uint8_t* here = lds + buf * kStage;
+      const uint8_t* next = lds + (buf ^ 1) * kStage;
+      read_x(here, 0, 1, xb);
+      read_w(here, 1, wb);
+      mma(0, xa, wa, kXW, kNone);
+      sync(s > 0);   // a tile's first step has been waited for before the epilogue
+      if (s == steps - 2) {
+        if (more)
+          turn_to(to, set ^ 1);
+        else
+          limit = 0;
+      }
+      const int ahead = s + 2 < steps ? s + 2 : s + 2 - steps;
+      read_x(here, 1, 0, xa);
+      issue(ahead, buf, 0, kMid);
+      mma(0, xb, wb, kX, kL1);
+      read_x(here, 1, 1, xb);
+      issue(ahead, buf, kMid, kFirst);
+      mma(1, xa, wa, kX, kL2);
+      sync(true);
+      read_x(next, 0, 0, xa);
+      read_w(next, 0, wa);
+      issue(ahead, buf, kFirst, kPer);
+      mma(1, xb, wb, kXW, kL3);
+      buf ^= 1;
+    }
+    // the next tile's first step, before this tile's stores count as the newest
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPer) : "memory");
+    const int64_t n0 = static_cast<int64_t>(at.nt) * kCols;
+    const float* xs_l = reinterpret_cast<const float*>(lds + sets + set * kSet);
+    const float* ws_l = xs_l + BM;
+    const float* b_l = ws_l + kCols;   // gated: the up projection's scales
+    // Columns in pairs of sub-tiles (gated: two gates and their two ups).
+    const int lane = again(threadIdx.x & 63), g = lane >> 4;
+    constexpr int kG = GATED ? 2 : 1;
 #pragma unroll
-      for (int jj = 0; jj < 2; ++jj) {
-        const int c = c0 + pair_col(jj, g);
-        const f32x4 s = E::kScaled ? *reinterpret_cast<const f32x4*>(ws_l + c) : f32x4{};
-        const f32x4 b = GATED ? f32x4{0.f, 0.f, 0.f, 0.f} : *reinterpret_cast<const f32x4*>(b_l + c);
-        scaled<E>(acc[i][kG * (2 * p + jj)], xs, s, b, v + 4 * jj);
-        if constexpr (GATED) {
-          const f32x4 s2 = E::kScaled ? *reinterpret_cast<const f32x4*>(ws_l + kCols + c) : f32x4{};
-          float u[4];
-          scaled<E>(acc[i][kG * (2 * p + jj) + 1], xs, s2, b, u);
+    for (int i = 0; i < kTM; ++i) {
+      const int r = (wm * kTM + i) * 16 + (lane & 15);
+      const int64_t row = at.row0 + r;
+      const float xs = xs_l[r];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[4 * jj + q] = silu_mul(v[4 * jj + q], u[q]);
+      for (int p = 0; p < kTN / (2 * kG); ++p) {
+        const int c0 = (wn * kTN / (2 * kG) + p) * 32;
+        float v[8];
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const int c = c0 + pair_col(jj, g);
+          const f32x4 s = E::kScaled ? *reinterpret_cast<const f32x4*>(ws_l + c) : f32x4{};
+          const f32x4 b = GATED ? f32x4{0.f, 0.f, 0.f, 0.f} : *reinterpret_cast<const f32x4*>(b_l + c);
+          scaled<E>(acc[i][kG * (2 * p + jj)], xs, s, b, v + 4 * jj);
+          if constexpr (GATED) {
+            const f32x4 s2 = E::kScaled ? *reinterpret_cast<const f32x4*>(b_l + c) : f32x4{};
+            float u[4];
+            scaled<E>(acc[i][kG * (2 * p + jj) + 1], xs, s2, b, u);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[4 * jj + q] = silu_mul(v[4 * jj + q], u[q]);
+          }
+        }
+        if (row >= at.row_end) continue;
+        if (a.y_f16) {
+          store_f16<8>(a, row, n0 + c0 + 8 * g, v);
+        } else {
+          store_f32(a, row, n0 + c0 + 4 * g, v);
+          store_f32(a, row, n0 + c0 + 16 + 4 * g, v + 4);
         }
       }
-      if (row > last) continue;
-      if (a.y_f16) {
-        store_f16<8>(a, row, n0 + c0 + 8 * g, v);
-      } else {
-        store_f32(a, row, n0 + c0 + 4 * g, v);
-        store_f32(a, row, n0 + c0 + 16 + 4 * g, v + 4);
-      }
     }
+    if (!more) break;
+    at = to;
+    set ^= 1;
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the last zeros are in before LDS is given up
 #endif
 }
 
@@ -508,8 +618,11 @@ template <typename E, int MT, int NW, int C, bool GATED>
 __global__ __launch_bounds__(NW * 64) void gemm_rows_kernel(TileArgs a) {
   constexpr int kG = GATED ? 2 : 1;
   __shared__ typename E::Acc part[NW][MT][kG][kWave];
+  extern __shared__ __align__(16) uint8_t lds[];   // the tile table of more than 64 experts
+  TileMap<16 * MT, true> map;
+  map.init(a, reinterpret_cast<int*>(lds));
   TileAt at;
-  if (!find_tile<16 * MT>(a, &at)) return;
+  if (!map.find(a, blockIdx.x % kXcds, blockIdx.x / kXcds, &at)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
@@ -617,6 +730,8 @@ namespace pesti_host {
 int gemm_tiles_i8(const pesti::TileArgs& a, bool gated, hipStream_t st);
 int gemm_tiles_f16(const pesti::TileArgs& a, bool gated, hipStream_t st);
 
+constexpr int64_t kCus = 256, kCuLds = 160 * 1024;   // compute units, bytes of LDS on each
+
 // Most row tiles of height bm there can be: each expert with rows ends in at
 // most one partial tile.
 inline int64_t most_row_tiles(const pesti::TileArgs& a, int bm) {
@@ -625,28 +740,32 @@ inline int64_t most_row_tiles(const pesti::TileArgs& a, int bm) {
   return a.rows / bm + used;
 }
 
-inline int launch_tiles(const void* fn, pesti::TileArgs a, int bm, int cols, int threads, size_t lds, hipStream_t st) {
+// most: workgroups to launch at most (each then takes several tiles in turn), 0 for one tile each.
+inline int launch_tiles(const void* fn, pesti::TileArgs a, int bm, int cols, int threads, size_t lds, int64_t most,
+                        hipStream_t st) {
   const int64_t tn = (a.n + cols - 1) / cols;
   const int64_t total = most_row_tiles(a, bm) * tn;
   // Tiles are numbered in 31 bits; the grid is rounded up to whole turns of the XCDs.
   if (tn > (1 << 27) || total > INT32_MAX - pesti::kXcds) return PESTI_ERR_SHAPE;
   a.tiles_n = static_cast<int32_t>(tn);
   void* params[] = {&a};
-  const unsigned grid = static_cast<unsigned>((total + pesti::kXcds - 1) / pesti::kXcds * pesti::kXcds);
+  unsigned grid = static_cast<unsigned>((total + pesti::kXcds - 1) / pesti::kXcds * pesti::kXcds);
+  if (most > 0 && grid > most) grid = static_cast<unsigned>(most);
   if (grid == 0) return PESTI_OK;
   return hipLaunchKernel(fn, dim3(grid), dim3(threads), params, lds, st) == hipSuccess ? PESTI_OK : PESTI_ERR_LAUNCH;
 }
 
 template <typename E, int BM, int BN, int WM, int WN, bool GATED>
 int launch_tile(const pesti::TileArgs& a, hipStream_t st) {
+  const int64_t lds = pesti::tile_lds<BM, BN>() + (a.offsets ? 12 * a.experts : 0);
   return launch_tiles(reinterpret_cast<const void*>(&pesti::gemm_tile_kernel<E, BM, BN, WM, WN, GATED>), a, BM,
-                      GATED ? BN / 2 : BN, WM * WN * 64, pesti::tile_lds<BM, BN>(), st);
+                      GATED ? BN / 2 : BN, WM * WN * 64, lds, kCus * (kCuLds / lds), st);
 }
 
 template <typename E, int MT, int NW, int C, bool GATED>
 int launch_rows(const pesti::TileArgs& a, hipStream_t st) {
   return launch_tiles(reinterpret_cast<const void*>(&pesti::gemm_rows_kernel<E, MT, NW, C, GATED>), a, 16 * MT, 16,
-                      NW * 64, 0, st);
+                      NW * 64, a.offsets && a.experts > 64 ? 12 * a.experts : 0, 0, st);
 }
 
 // Rows one matrix is multiplied with, on average over the experts.

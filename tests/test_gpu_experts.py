@@ -317,6 +317,46 @@ def test_swiglu(which, n, k, form):
     check_swiglu(got, offsets, rows, form, x, xs, gate, up, kind, at)
 
 
+@pytest.mark.parametrize("mean", [1, 20, 40, 70, 150, 300])
+@pytest.mark.parametrize("e", [64, 65, 700, 1024])
+def test_experts_by_the_hundred(e, mean):
+    """Many experts of every mean row count (each kernel's look-up of tiles), columns of several tiles; rows of
+    X repeat.  Few columns of K: the oracle's work stays small."""
+    rng = np.random.default_rng([16, e, mean])
+    counts = rng.integers(0, 2 * mean + 1, size=e)
+    counts[rng.integers(0, e, size=e // 5)] = 0
+    n, k = 40, 32
+    x, xs, ((w, ws),) = experts_inputs(rng, "i8", e, n, k, 50)
+    offsets, at, rows = routed(rng, counts, 50, lead=1, behind=2)
+    announce(f"experts by the hundred {e} {mean} rows {rows}")
+    got = run_experts("i8", offsets, rows, x, xs, w, ws, "f32", at)
+    check_experts(got, offsets, rows, "i8", x, xs, w, ws, "f32", at)
+
+
+@pytest.mark.parametrize("form", ["f16", "i8"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_several_tiles_for_a_workgroup(form, gated):
+    """More tiles than workgroups run at a time, in the kernels of every tile size: each workgroup takes several,
+    of different experts and widths, with K from one step to many."""
+    for case, (counts, n, k) in enumerate([([700, 300, 1, 513, 400], 2600, 32), ([300, 140, 260, 3, 129], 3999, 288),
+                                           ([90, 70, 65, 128, 0, 127], 9000, 96), ([40, 64, 33, 50], 20001, 64),
+                                           ([600, 520, 770], 2800, 576)]):
+        rng = np.random.default_rng([17, case])
+        e = len(counts)
+        if gated:
+            n //= 2
+        x, xs, mats = experts_inputs(rng, form, e, n, k, 61, mats=2 if gated else 1)
+        offsets, at, rows = routed(rng, counts, 61, lead=case % 2, behind=1, wild=case % 2 == 0)
+        announce(f"several tiles {form} {gated} {case}")
+        if gated:
+            got = run_swiglu(form, offsets, rows, x, xs, mats[0], mats[1], "f16", at)
+            check_swiglu(got, offsets, rows, form, x, xs, mats[0], mats[1], "f16", at)
+        else:
+            bias = rng.standard_normal((e, n)).astype(np.float32)
+            got = run_experts(form, offsets, rows, x, xs, mats[0][0], mats[0][1], "f32", at, bias)
+            check_experts(got, offsets, rows, form, x, xs, mats[0][0], mats[0][1], "f32", at, bias)
+
+
 @pytest.mark.parametrize("form", ["f16", "i8"])
 def test_experts_without_gather_or_columns_or_tokens(form):
     """x_rows left out (row r of X is row r of Y); k = 0 and an empty X give the bias."""
