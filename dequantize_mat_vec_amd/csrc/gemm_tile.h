@@ -13,6 +13,7 @@
 // consecutive output columns of one row of X and stores them at once.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -609,14 +610,20 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows of X: a workgroup owns 16 columns and up to 16 * MT rows of Y, and
-// its NW wavefronts split K into contiguous slices, each streaming its part
-// of W from memory straight into operand registers (C k-steps at a time, the
-// next C in flight); the partial sums meet in LDS in wavefront order.
+// Few tiles: where 64 x 128 tiles would leave most compute units idle, a
+// workgroup owns 16 columns and up to 16 * MT rows of Y, and its NW
+// wavefronts split K into contiguous slices, each streaming its part of W and
+// X from memory straight into operand registers, D lines of 128 bytes (two
+// k-steps) per row in flight; the partial sums meet in LDS in wavefront order.
+// What bounds it is latency: finding the expert, the picked rows, one trip
+// for W, the sum.  So NW and D are the fewest that have a whole row of common
+// lengths in flight at once; loads past the row's end cost their issue.
 // ---------------------------------------------------------------------------
-template <typename E, int MT, int NW, int C, bool GATED>
+template <typename E, int MT, int NW, int D, bool GATED>
 __global__ __launch_bounds__(NW * 64) void gemm_rows_kernel(TileArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__
   constexpr int kG = GATED ? 2 : 1;
+  constexpr int C = 2;
   __shared__ typename E::Acc part[NW][MT][kG][kWave];
   extern __shared__ __align__(16) uint8_t lds[];   // the tile table of more than 64 experts
   TileMap<16 * MT, true> map;
@@ -626,99 +633,110 @@ __global__ __launch_bounds__(NW * 64) void gemm_rows_kernel(TileArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int64_t n0 = static_cast<int64_t>(at.nt) * 16;
-  const int64_t last = at.row_end - 1;
-  const int steps = (a.kbytes + 63) >> 6;
-  const int per = (steps + NW - 1) / NW;
-  const int s0 = wave * per < steps ? wave * per : steps;
-  const int s1 = s0 + per < steps ? s0 + per : steps;
+  const int64_t n0 = static_cast<int64_t>(at.nt) * 16, first = at.expert * a.n + n0;
+  const int cols = a.n - n0 < 16 ? static_cast<int>(a.n - n0) : 16;
+  const int steps = (a.kbytes + 63) >> 6, per = (steps + NW - 1) / NW;
+  const uint32_t begin = wave * per * 64;
+  const uint32_t end = begin + per * 64 < static_cast<uint32_t>(a.kbytes) ? begin + per * 64 : a.kbytes;
 
-  const int64_t col = n0 + i < a.n ? n0 + i : a.n - 1;
-  const uint8_t* wp[kG];
-  wp[0] = a.w + (at.expert * a.n + col) * static_cast<int64_t>(a.kbytes);
-  if constexpr (GATED) wp[1] = a.w2 + (at.expert * a.n + col) * static_cast<int64_t>(a.kbytes);
-  const uint8_t* xp[MT];
+  const int64_t x0 = a.x_rows ? 0 : at.row0, x_left = a.x_tokens - x0;
+  int xi[MT];
+  bool ok[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
-    const int64_t row = at.row0 + 16 * t + i;
-    bool ok;
-    xp[t] = a.x + x_row(a, row < last ? row : last, &ok) * a.kbytes;
+    const int64_t row = at.row0 + 16 * t + i < at.row_end ? at.row0 + 16 * t + i : at.row_end - 1;
+    xi[t] = a.x_rows ? a.x_rows[row] : static_cast<int>(row - x0);
+    ok[t] = xi[t] >= 0 && xi[t] < (a.x_rows ? a.x_tokens : x_left);
   }
-
+  const BufferRsrc rw = buffer_of(a.w + first * a.kbytes, static_cast<int64_t>(cols) * a.kbytes);
+  const BufferRsrc rw2 = GATED ? buffer_of(a.w2 + first * a.kbytes, static_cast<int64_t>(cols) * a.kbytes) : rw;
+  const BufferRsrc rx = buffer_of(
+      a.x + x0 * a.kbytes, (a.x_rows ? a.x_tokens : x_left < 16 * MT ? (x_left < 0 ? 0 : x_left) : 16 * MT) * a.kbytes);
+  const uint32_t wrow = static_cast<uint32_t>(i < cols ? i : cols - 1) * a.kbytes;
   struct Buf {
     i32x4 w[C][kG], x[C][MT];
   };
-  // k-steps past the slice and the half step past a row's end load the row's
-  // start, and both operands are zeroed before they are used.
-  auto load = [&](int s, Buf& b) {
+  // Past the slice, and in the half step past a row's end, both are zeros.
+  auto load_w = [&](uint32_t o, Buf& b) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int o = (s + c) * 64 + 16 * g;
-      const int p = s + c < s1 && o < a.kbytes ? o : 0;
-#pragma unroll
-      for (int k = 0; k < kG; ++k) b.w[c][k] = *reinterpret_cast<const i32x4*>(wp[k] + p);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) b.x[c][t] = *reinterpret_cast<const i32x4*>(xp[t] + p);
+      const uint32_t p = o + 64 * c + 16 * g, q = p < end ? wrow + p : kNoOffset;
+      b.w[c][0] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, q, 0, 0));
+      if constexpr (GATED) b.w[c][1] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw2, q, 0, 0));
     }
+  };
+  auto load_x = [&](uint32_t o, Buf& b) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint32_t p = o + 64 * c + 16 * g;
+        const uint32_t q = ok[t] && p < end ? static_cast<uint32_t>(xi[t]) * a.kbytes + p : kNoOffset;
+        b.x[c][t] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, q, 0, 0));
+      }
   };
   typename E::Acc acc[MT][kG];
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
     for (int k = 0; k < kG; ++k) acc[t][k] = E::zero();
-  auto mma = [&](int s, const Buf& b) {
+  auto mma = [&](const Buf& b) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const bool in = s + c < s1 && (s + c) * 64 + 16 * g < a.kbytes;
-      const i32x4 z = {0, 0, 0, 0};
+    for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int k = 0; k < kG; ++k) acc[t][k] = E::mma(in ? b.w[c][k] : z, in ? b.x[c][t] : z, acc[t][k]);
-    }
+        for (int k = 0; k < kG; ++k) acc[t][k] = E::mma(b.w[c][k], b.x[c][t], acc[t][k]);
   };
-  if (s0 < s1) {
-    Buf ba, bb;
-    load(s0, ba);
-    for (int s = s0; s < s1; s += 2 * C) {
-      load(s + C, bb);
-      mma(s, ba);
-      if (s + C >= s1) break;
-      load(s + 2 * C, ba);
-      mma(s + C, bb);
-    }
+  // W first: it does not wait for the rows of X to be known.
+  Buf ring[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) load_w(begin + 128 * d, ring[d]);
+#pragma unroll
+  for (int d = 0; d < D; ++d) load_x(begin + 128 * d, ring[d]);
+  // What the epilogue needs, before the products: lane l of the wavefront
+  // that stores a row tile has its row l % 16 and four columns.
+  float xs[MT], ws[kG][4], b4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < MT; ++t) xs[t] = ok[t] ? (E::kScaled ? a.xs[x0 + xi[t]] : 1.f) : 0.f;
+  if constexpr (E::kScaled) {
+    load4(a.ws + at.expert * a.n, n0 + 4 * g, a.n, ws[0]);
+    if constexpr (GATED) load4(a.ws2 + at.expert * a.n, n0 + 4 * g, a.n, ws[kG - 1]);
   }
+  if (!GATED && a.bias) load4(a.bias + at.expert * a.n, n0 + 4 * g, a.n, b4);
+  uint32_t o = begin;
+  for (; o + 128 * D < end; o += 128 * D)
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      mma(ring[d]);
+      load_w(o + 128 * (D + d), ring[d]);
+      load_x(o + 128 * (D + d), ring[d]);
+    }
+#pragma unroll
+  for (int d = 0; d < D; ++d) mma(ring[d]);   // the last: zeros past the slice
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
     for (int k = 0; k < kG; ++k) part[wave][t][k][lane] = acc[t][k];
   __syncthreads();
-
-  const float* bias = a.bias ? a.bias + at.expert * a.n : nullptr;
-  for (int e = threadIdx.x; e < MT * kWave; e += NW * kWave) {
-    const int t = e / kWave, l = e % kWave;
-    const int64_t row = at.row0 + 16 * t + (l & 15);
-    if (row > last) continue;
-    bool ok;
-    const int64_t xi = x_row(a, row, &ok);
-    const float xs = ok ? (E::kScaled ? a.xs[xi] : 1.f) : 0.f;
-    const int64_t c0 = n0 + 4 * (l >> 4);
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    if (wave != t % NW) continue;
     float v[kG][4];
 #pragma unroll
     for (int k = 0; k < kG; ++k) {
-      typename E::Acc r = part[0][t][k][l];
+      typename E::Acc r = part[0][t][k][lane];
 #pragma unroll
-      for (int w = 1; w < NW; ++w) r += part[w][t][k][l];
-      float s[4] = {1.f, 1.f, 1.f, 1.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
-      if (E::kScaled) load4((k ? a.ws2 : a.ws) + at.expert * a.n, c0, a.n, s);
-      if (!GATED && bias) load4(bias, c0, a.n, b);
-      scaled<E>(r, xs, s, b, v[k]);
+      for (int w = 1; w < NW; ++w) r += part[w][t][k][lane];
+      scaled<E>(r, xs[t], ws[k], b4, v[k]);
     }
     if constexpr (GATED)
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[0][q] = silu_mul(v[0][q], v[1][q]);
-    store4(a, row, c0, v[0]);
+    const int64_t row = at.row0 + 16 * t + i;
+    if (row < at.row_end) store4(a, row, n0 + 4 * g, v[0]);
   }
+#endif
 }
 
 }  // namespace pesti
@@ -762,41 +780,63 @@ int launch_tile(const pesti::TileArgs& a, hipStream_t st) {
                       GATED ? BN / 2 : BN, WM * WN * 64, lds, kCus * (kCuLds / lds), st);
 }
 
-template <typename E, int MT, int NW, int C, bool GATED>
-int launch_rows(const pesti::TileArgs& a, hipStream_t st) {
-  return launch_tiles(reinterpret_cast<const void*>(&pesti::gemm_rows_kernel<E, MT, NW, C, GATED>), a, 16 * MT, 16,
+template <typename E, int MT, int NW, int D, bool GATED>
+int launch_rows_w(const pesti::TileArgs& a, hipStream_t st) {
+  return launch_tiles(reinterpret_cast<const void*>(&pesti::gemm_rows_kernel<E, MT, NW, D, GATED>), a, 16 * MT, 16,
                       NW * 64, a.offsets && a.experts > 64 ? 12 * a.experts : 0, 0, st);
 }
+template <typename E, int MT, bool GATED>
+int launch_rows(const pesti::TileArgs& a, hipStream_t st) {
+  return a.kbytes <= 2048 ? launch_rows_w<E, MT, 2, 4, GATED>(a, st) : launch_rows_w<E, MT, 4, 5, GATED>(a, st);
+}
 
-// Rows one matrix is multiplied with, on average over the experts.
-inline int64_t mean_rows(const pesti::TileArgs& a) { return (a.rows + a.experts - 1) / a.experts; }
-
-// Tiles of bm rows and bn columns that a launch comes to: experts' rows end
+// Tiles of bm rows and cols columns that a launch comes to: experts' rows end
 // on average half a tile early.
 inline int64_t tiles_about(const pesti::TileArgs& a, int bm, int cols) {
-  const int64_t row_tiles = a.offsets ? a.rows / bm + (a.experts + 1) / 2 : (a.rows + bm - 1) / bm;
+  const int64_t half = a.experts < a.rows ? (a.experts + 1) / 2 : 0;
+  const int64_t row_tiles = a.offsets && half ? a.rows / bm + half : most_row_tiles(a, bm);
   return row_tiles * ((a.n + cols - 1) / cols);
 }
 
-// Row counts up to 32 stream W once through the K-split kernel; above that
-// operands are shared through LDS, in the largest tile that there are enough
-// of to fill the chip and that the rows of an expert fill: bytes into LDS
-// bound these kernels, and a tile of BM x BN moves (BM + BN) / (BM BN) per
-// product.  Measured (us at 64x128 / 128x128 / 128x256 / 256x256): 8-bit
-// 8192x4096x4096 182 / 162 / 146 / 127; 64 experts, 512 rows each,
-// 2048x1024 163 / 147 / 135 / 127; binary16 SwiGLU of 32 experts, 256 rows
-// each, 1408x2048 189 / 178 / 165 / 183; 8 experts, 255 rows, 2429x1056
-// 28 / 30 / 26 / 37; 8-bit 4096x896x4864 30 / 29 / 35 / 59; 513x2304x768
-// 7.9 / 9.1 / 10.5 / 16.4.
+// The kernel for a shape.
+//
+// Fewer 64 x 128 tiles than compute units leave them idle: the rows kernel
+// takes over as long as its workgroups fit the chip about once, with the
+// fewest rows each that do it (us for 16, 32 and 64 rows and the 64 x 128
+// tile: 8-bit 64x896x4864 7.8 / 10 / 14 / 16, 128x896x4864 12 / 10 / 15 / 17,
+// 256x896x4864 21 / 18 / 15 / 18, 40x4864x896 6.8 / 7.6 / 7.1 / 7.4, 100x4864x896
+// 11 / 10 / 10 / 7.8; 8 experts of one row, gated 1024x2048, 9.9 against 13).
+// With more tiles, tiles win for one row as for many (8-bit 1x151936x896: 28
+// against 34 us; 50 experts of five rows, 1408x2048: 36 both).
+//
+// Among the tiles, time goes by how many each compute unit gets (a 128 x 128
+// tile takes 1.6 times a 64 x 128 one, 128 x 256 3 times, 256 x 256 5.3
+// times: bytes into LDS bound them, (BM + BN) / (BM BN) per product), so the
+// least of tiles per unit times that is taken.  Measured (us at 64x128 /
+// 128x128 / 128x256 / 256x256): 8-bit 8192x4096x4096 175 / 153 / 135 / 114,
+// 4096x4096x4096 91 / 70 / 67 / 60, 2048x4864x896 19 / 19 / 22 / 20,
+// 4096x896x4864 28 / 24 / 32 / 49, 513x2304x768 7.6 / 8.9 / 11 / 16; 64
+// experts, 512 rows each, 2048x1024 147 / 129 / 118 / 114; 60 experts, 173
+// rows, 1408x2048 78 / 66 / 68 / 69; binary16, 8 experts, 255 rows,
+// 2429x1056 28 / 28 / 26 / 36, gated, 32 experts, 256 rows, 1408x2048 196 /
+// 159 / 158 / 172.
 template <typename E, bool GATED>
 int launch_any(const pesti::TileArgs& a, hipStream_t st) {
   constexpr int kG = GATED ? 2 : 1;
-  const int64_t mean = mean_rows(a);
-  if (mean <= 16) return launch_rows<E, 1, 8, 4, GATED>(a, st);
-  if (mean <= 32) return launch_rows<E, 2, 8, 2, GATED>(a, st);
-  if (mean > 256 && tiles_about(a, 256, 256 / kG) >= 448) return launch_tile<E, 256, 256, 2, 4, GATED>(a, st);
-  if (mean > 128 && tiles_about(a, 128, 256 / kG) >= 192) return launch_tile<E, 128, 256, 2, 4, GATED>(a, st);
-  if (mean > 64 && tiles_about(a, 128, 128 / kG) >= 192) return launch_tile<E, 128, 128, 2, 2, GATED>(a, st);
+  if (most_row_tiles(a, 64) * ((a.n + 128 / kG - 1) / (128 / kG)) < kCus) {
+    const int64_t cols = (a.n + 15) / 16, limit = kCus * 3 / 2;
+    const int64_t r1 = most_row_tiles(a, 16), r2 = most_row_tiles(a, 32), r4 = most_row_tiles(a, 64);
+    if (r1 * cols <= limit || r1 == r4) return launch_rows<E, 1, GATED>(a, st);
+    if (r2 * cols <= limit || (GATED && r2 == r4)) return launch_rows<E, 2, GATED>(a, st);
+    if constexpr (!GATED)
+      if (r4 * cols <= kCus) return launch_rows<E, 4, GATED>(a, st);
+  }
+  auto cost = [&](int bm, int bn, int64_t unit) { return (tiles_about(a, bm, bn / kG) + kCus - 1) / kCus * unit; };
+  const int64_t c0 = cost(64, 128, 10), c1 = cost(128, 128, 16), c2 = cost(128, 256, 30), c3 = cost(256, 256, 53);
+  const int64_t low = std::min(std::min(c0, c1), std::min(c2, c3));
+  if (c3 == low) return launch_tile<E, 256, 256, 2, 4, GATED>(a, st);
+  if (c2 == low) return launch_tile<E, 128, 256, 2, 4, GATED>(a, st);
+  if (c1 == low) return launch_tile<E, 128, 128, 2, 2, GATED>(a, st);
   return launch_tile<E, 64, 128, 2, 2, GATED>(a, st);
 }
 
