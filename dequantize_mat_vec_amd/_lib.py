@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().with_name("libpesti.so")
@@ -293,7 +294,7 @@ def _sized(dev, obj, nbytes, what, dtype=None):
     """_ptr of an argument, with a tensor's size, element type and device
     (the current one, `dev`) checked too: these calls take several arrays of
     related sizes."""
-    if obj is None or isinstance(obj, int):
+    if obj is None or type(obj) is int:
         return obj
     if not hasattr(obj, "data_ptr"):
         return _ptr(obj)
@@ -312,22 +313,28 @@ def _sized(dev, obj, nbytes, what, dtype=None):
 def _place(stream):
     """(torch, current device, raw stream) of a call: device 0 where no GPU
     is to be asked (the library then refuses the call itself)."""
-    import torch
+    torch = sys.modules.get("torch")   # cheaper than an import statement per call
+    if torch is None:
+        import torch
     if stream is None:
         dev = torch.cuda.current_device()
         return torch, dev, _raw_stream(torch, dev)
     return torch, torch.cuda.current_device() if torch.cuda.is_available() else 0, _stream(stream)
 
 
+_TYPE_FORMATS = {"torch.float32": 17, "torch.float16": 16}   # by str(dtype)
+
+
 def _value_format(fmt, obj, what):
     """(PESTI_FMT_* id, bytes per value) of X or Y: as given, else by the tensor's type."""
     if fmt is None:
         kind = str(getattr(obj, "dtype", None))
-        fmt = {"torch.float32": "f32", "torch.float16": "f16"}.get(kind)
-        if fmt is None:
+        fid = _TYPE_FORMATS.get(kind)
+        if fid is None:
             raise ValueError(f"{what}: give its format, or a float32 or float16 tensor (got {kind})")
-    fid = VALUE_FORMAT_IDS[fmt] if isinstance(fmt, str) else int(fmt)
-    return fid, 4 if fid == VALUE_FORMAT_IDS["f32"] else 2
+    else:
+        fid = VALUE_FORMAT_IDS[fmt] if isinstance(fmt, str) else int(fmt)
+    return fid, 4 if fid == 17 else 2
 
 
 def pesti_quant_i8token(x_format, m, in_features, x, codes, scales, stream=None):

@@ -78,6 +78,17 @@ __device__ __forceinline__ uint32_t align_bytes(uint32_t hi, uint32_t lo, uint32
   return __builtin_amdgcn_alignbyte(hi, lo, shift);
 }
 
+#ifdef __HIP_DEVICE_COMPILE__   // the host compiler has no buffer descriptors: bodies that use them are guarded too
+// Loads through a buffer descriptor take 32-bit offsets and give zeros past
+// the buffer's end, with no branch or stand-in address.
+typedef __amdgpu_buffer_rsrc_t BufferRsrc;
+constexpr uint32_t kNoOffset = 0xFFFFFFF0u;   // past the end of every buffer
+__device__ __forceinline__ BufferRsrc buffer_of(const uint8_t* p, int64_t bytes) {
+  // raw 32-bit data, no stride or swizzle; at most 2^32 - 16 bytes
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, static_cast<int>(bytes), 0x00020000);
+}
+#endif
+
 // ---------------------------------------------------------------------------
 // Cross-lane sums within groups of L lanes; every lane of the group ends with
 // the group's total.

@@ -295,7 +295,7 @@ __device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const
 // 8192x4096x4096 in 8 bits, binary16 Y: 114 us (2.4 POP/s) in 256 x 256
 // tiles; the products alone (nothing loaded or read) take 78 us.
 // ---------------------------------------------------------------------------
-#ifdef __HIP_DEVICE_COMPILE__   // the host compiler has no buffer descriptors, and needs only the kernel's name
+#ifdef __HIP_DEVICE_COMPILE__   // the host compiler needs only the kernels' names
 // A value that what is computed from it is computed from again: the compiler
 // would take such sums of lane numbers out of the loop over tiles, at the
 // price of registers that its 256 x 256 instance does not have (it reloaded
@@ -303,13 +303,6 @@ __device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const
 __device__ __forceinline__ int again(int v) {
   asm volatile("" : "+v"(v));
   return v;
-}
-
-typedef __amdgpu_buffer_rsrc_t BufferRsrc;
-constexpr uint32_t kNoOffset = 0xFFFFFFF0u;   // past the end of every buffer
-__device__ __forceinline__ BufferRsrc buffer_of(const uint8_t* p, int64_t bytes) {
-  // raw 32-bit data, no stride or swizzle; at most 2^32 - 16 bytes
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, static_cast<int>(bytes), 0x00020000);
 }
 #endif
 

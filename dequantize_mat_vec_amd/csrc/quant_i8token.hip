@@ -7,14 +7,23 @@
 //   c[t][i] = x[t][i] / s[t]                rounded half away from zero
 //
 // One pass: a row stays in the registers of the 64, 256 or 1024 lanes that
-// serve it between its maximum and its codes, so X is read once.
+// serve it between its maximum and its codes, so X is read once.  What bounds
+// long batches is memory and, close behind, vector ALU work: 4096 x 4864
+// binary16 (60 MB) took 24 us with a division-free exact rounding of every
+// element (17 operations), 16 us with the one below (6; 8192 x 8192 41 us, 4.9 TB/s).
 //
-// The codes are those of the exact quotient.  t = x * (1 / s) is within a
-// few ulps of x / s, so q = rint(t) is off by one at most; the residual
-// r = x - q s is exact in one fma (both terms are multiples of ulp(s) or
-// finer with |r| below 2 s, so r needs no more than 24 bits), and comparing
-// 2 |r| with s moves q by one exactly where the quotient lies on the other
-// side of a border, ties away from zero.
+// The codes are those of the exact quotient.  t = x * (1 / s) + 1.5 * 2^23 in
+// one fma is the nearest integer of x * (1 / s), its low byte the code, and
+// d = x * (1 / s) - q, the distance from it, shows where that may not be the
+// nearest to x / s: 1 / s is within 2^-24 of its value, so the two lie within
+// 127 * 2^-24 of each other.  Where some |d| of a wavefront's elements comes
+// within 10^-5 of 1/2 (a few wavefronts in a hundred), all are done again
+// exactly: the residual r = x - q s is exact in one fma (both terms are
+// multiples of ulp(s) or finer with |r| below 2 s, so r needs no more than 24
+// bits), and comparing 2 |r| with s moves q by one exactly where the quotient
+// lies on the other side of a border, ties away from zero.
+#include <type_traits>
+
 #include "common.h"
 
 namespace pesti {
@@ -27,26 +36,50 @@ struct QuantArgs {
   int64_t k;
 };
 
-// Elements of one 16-byte load as float32.
+// A 16-byte load: its elements as float32, and the largest magnitude's bits
+// (as float32) so far.  Magnitudes compare as their bit patterns, with
+// infinities and then NaN above every finite value, so one integer maximum
+// finds them all.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<_Float16> {
   static constexpr int kN = 8;
-  typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-  __device__ __forceinline__ static void load(const void* p, int64_t i, float* v) {
-    const h8 h = reinterpret_cast<const h8*>(p)[i];
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  typedef u16x2 Max;
+  __device__ __forceinline__ static Max zero() { return u16x2{0, 0}; }
+  __device__ __forceinline__ static Max max(Max m, u32x4a v) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(h[e]);
+    for (int w = 0; w < 4; ++w) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[w] & 0x7FFF7FFFu));
+    return m;
+  }
+  __device__ __forceinline__ static uint32_t bits(Max m) {
+    const uint16_t h = m.x > m.y ? m.x : m.y;
+    return __builtin_bit_cast(uint32_t, static_cast<float>(__builtin_bit_cast(_Float16, h)));
+  }
+  __device__ __forceinline__ static float at(u32x4a v, int e) {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    const uint32_t w = v[e / 2];   // a copy: bit_cast of the element itself reads the vector's first
+    return static_cast<float>(__builtin_bit_cast(h2, w)[e & 1]);
   }
 };
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
-  __device__ __forceinline__ static void load(const void* p, int64_t i, float* v) {
-    const f32x4 f = reinterpret_cast<const f32x4*>(p)[i];
+  typedef uint32_t Max;
+  __device__ __forceinline__ static Max zero() { return 0; }
+  __device__ __forceinline__ static Max max(Max m, u32x4a v) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = f[e];
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t u = v[w] & 0x7FFFFFFFu;
+      m = m > u ? m : u;
+    }
+    return m;
+  }
+  __device__ __forceinline__ static uint32_t bits(Max m) { return m; }
+  __device__ __forceinline__ static float at(u32x4a v, int e) {
+    const uint32_t w = v[e];
+    return __builtin_bit_cast(float, w);
   }
 };
 
@@ -62,39 +95,30 @@ __device__ __forceinline__ int code_of(float x, float inv, float s) {
   return static_cast<int>(q);
 }
 
-// LANES lanes per row (64: four rows per workgroup), NV 16-byte vectors per
-// lane at most.
-template <typename T, int LANES, int NV>
-__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void quant_i8token_kernel(QuantArgs a) {
-  constexpr int kN = Vec<T>::kN;
-  constexpr int kRows = LANES < 256 ? 256 / LANES : 1;
-  __shared__ uint32_t wave_max[LANES / 64 < 1 ? 1 : LANES / 64];
-  const int lane = threadIdx.x % LANES;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / LANES;
-  if (LANES == 64 && row >= a.m) return;
-  const int nv = static_cast<int>(a.k / kN);
-  const uint8_t* xr = static_cast<const uint8_t*>(a.x) + row * a.k * static_cast<int64_t>(sizeof(T));
+// Largest value of a wavefront, in a scalar register.
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  auto dpp = [](uint32_t x, auto ctrl) {
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(x), decltype(ctrl)::value, 0xF, 0xF, false));
+  };
+  v = umax(v, dpp(v, std::integral_constant<int, 0xB1>{}));    // lane ^ 1
+  v = umax(v, dpp(v, std::integral_constant<int, 0x4E>{}));    // lane ^ 2
+  v = umax(v, dpp(v, std::integral_constant<int, 0x141>{}));   // mirror within 8
+  v = umax(v, dpp(v, std::integral_constant<int, 0x140>{}));   // mirror within 16
+  auto lane = [&](int l) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l)); };
+  return umax(umax(lane(0), lane(16)), umax(lane(32), lane(48)));
+}
 
-  float v[NV][kN];
+// Scale and codes of a row held by LANES lanes, NV vectors each.
+template <typename T, int LANES, int NV>
+__device__ __forceinline__ void one_row(const QuantArgs& a, int64_t row, int lane, int nv, const u32x4a (&v)[NV],
+                                        uint32_t* wave_max) {
+  typedef Vec<T> V;
+  constexpr int kN = V::kN;
+  typename V::Max m = V::zero();
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = lane + LANES * j;
-    if (i < nv) {
-      Vec<T>::load(xr, i, v[j]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kN; ++e) v[j][e] = 0.f;
-    }
-  }
-  // Magnitudes compare as their bit patterns, with infinities and then NaN
-  // above every finite value, so one integer maximum finds both.
-  uint32_t mx = 0;
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < kN; ++e) mx = umax(mx, __builtin_bit_cast(uint32_t, v[j][e]) & 0x7FFFFFFFu);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) mx = umax(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), d, 64)));
+  for (int j = 0; j < NV; ++j) m = V::max(m, v[j]);
+  uint32_t mx = wave_umax(V::bits(m));
   if constexpr (LANES > 64) {
     if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = mx;
     __syncthreads();
@@ -102,38 +126,89 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void quant_i8token_kerne
     for (int w = 0; w < LANES / 64; ++w) mx = umax(mx, wave_max[w]);
   }
 
-  const float amax = __builtin_bit_cast(float, mx);
   const bool finite = mx < 0x7F800000u;
-  float s = finite ? amax / 127.f : __builtin_nanf("");
+  float s = finite ? __builtin_bit_cast(float, mx) / 127.f : __builtin_nanf("");
   if (lane == 0) a.scales[row] = s;
+  int8_t* cr = a.codes + row * a.k;
+  auto store = [&](int j, const uint32_t* p) {
+    const int i = lane + LANES * j;
+    if (i >= nv) return;
+    if constexpr (kN == 8)
+      reinterpret_cast<uint2*>(cr)[i] = make_uint2(p[0], p[1]);
+    else
+      reinterpret_cast<uint32_t*>(cr)[i] = p[0];
+  };
+  uint32_t p[NV][kN / 4];
+  float far = 0.f;
   const bool live = finite && s > 0.f;
-  // 1 / s overflows below 2^-128 and s has few bits among the subnormals:
-  // there both sides of the quotient are scaled by an exact power of two.
+  if (live && s >= 0x1p-100f) {
+    const float inv = 1.f / s;
+    constexpr float kRound = 12582912.f;   // 1.5 * 2^23: sums with it are integers, low byte first
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int w = 0; w < kN / 4; ++w) {
+        uint32_t t[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = V::at(v[j], 4 * w + e);
+          const float q = __builtin_fmaf(x, inv, kRound);
+          far = __builtin_fmaxf(far, __builtin_fabsf(__builtin_fmaf(x, inv, kRound - q)));
+          t[e] = __builtin_bit_cast(uint32_t, q);
+        }
+        // low bytes of t[0..3]
+        const uint32_t lo = __builtin_amdgcn_perm(t[1], t[0], 0x0C0C0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(t[3], t[2], 0x04000C0Cu);
+        p[j][w] = lo | hi;
+      }
+    if (!__any(far > 0.5f - 1e-5f)) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) store(j, p[j]);
+      return;
+    }
+  }
+  // Every element exactly.  1 / s overflows below 2^-128 and s has few bits
+  // among the subnormals: there both sides of the quotient are scaled by an
+  // exact power of two.
   const float up = s < 0x1p-100f ? 0x1p100f : 1.f;
   s = live ? s * up : 1.f;
   const float inv = live ? 1.f / s : 0.f;
-  int8_t* cr = a.codes + row * a.k;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int i = lane + LANES * j;
-    uint32_t packed[kN / 4];
 #pragma unroll
     for (int w = 0; w < kN / 4; ++w) {
-      uint32_t p = 0;
+      p[j][w] = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float x = live ? v[j][4 * w + e] * up : 0.f;
-        p |= static_cast<uint32_t>(code_of(x, inv, s) & 0xFF) << (8 * e);
+        const float x = live ? V::at(v[j], 4 * w + e) * up : 0.f;
+        p[j][w] |= static_cast<uint32_t>(code_of(x, inv, s) & 0xFF) << (8 * e);
       }
-      packed[w] = p;
     }
-    if (i < nv) {
-      if constexpr (kN == 8)
-        reinterpret_cast<uint2*>(cr)[i] = make_uint2(packed[0], packed[1]);
-      else
-        reinterpret_cast<uint32_t*>(cr)[i] = packed[0];
-    }
+    store(j, p[j]);
   }
+}
+
+// LANES lanes per row (64: four rows per workgroup), NV 16-byte vectors per
+// lane at most.  One row each: workgroups that take several, the next one's
+// loads under the work on this one, measured slower (8192 x 8192 52 us
+// against 40).
+template <typename T, int LANES, int NV>
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void quant_i8token_kernel(QuantArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int kRows = LANES < 256 ? 256 / LANES : 1;
+  __shared__ uint32_t wave_max[LANES / 64];
+  const int lane = threadIdx.x % LANES;
+  const int64_t row =
+      static_cast<int64_t>(blockIdx.x) * kRows + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
+  if (LANES == 64 && row >= a.m) return;
+  const int64_t bytes = a.k * static_cast<int64_t>(sizeof(T));
+  const BufferRsrc x = buffer_of(static_cast<const uint8_t*>(a.x) + row * bytes, bytes);
+  u32x4a v[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)   // zeros past the row's end
+    v[j] = __builtin_bit_cast(u32x4a, __builtin_amdgcn_raw_buffer_load_b128(x, 16 * (lane + LANES * j), 0, 0));
+  one_row<T, LANES, NV>(a, row, lane, static_cast<int>(a.k / Vec<T>::kN), v, wave_max);
+#endif
 }
 
 }  // namespace pesti
@@ -151,13 +226,21 @@ int launch(const pesti::QuantArgs& a, hipStream_t st) {
   return e == hipSuccess ? PESTI_OK : PESTI_ERR_LAUNCH;
 }
 
+// 1024 lanes serve rows of more than 2048 vectors: at least 3 per lane, at
+// most 4 in binary16.
 template <typename T, int LANES>
 int launch_nv(const pesti::QuantArgs& a, hipStream_t st) {
   const int64_t per = (a.k / pesti::Vec<T>::kN + LANES - 1) / LANES;
-  if (per <= 1) return launch<T, LANES, 1>(a, st);
-  if (per <= 2) return launch<T, LANES, 2>(a, st);
-  if (per <= 4) return launch<T, LANES, 4>(a, st);
-  return launch<T, LANES, 8>(a, st);
+  if constexpr (LANES < 1024) {
+    if (per <= 1) return launch<T, LANES, 1>(a, st);
+    if (per <= 2) return launch<T, LANES, 2>(a, st);
+  }
+  if (per <= 3) return launch<T, LANES, 3>(a, st);
+  if constexpr (LANES < 1024 || sizeof(T) == 4) {
+    if (per > 6) return launch<T, LANES, 8>(a, st);
+    if (per > 4) return launch<T, LANES, 6>(a, st);
+  }
+  return launch<T, LANES, 4>(a, st);
 }
 
 // Lanes per row: a wavefront per row once the rows fill the chip and a row
