@@ -296,7 +296,11 @@ def _sized(dev, obj, nbytes, what, dtype=None):
     related sizes."""
     if obj is None or type(obj) is int:
         return obj
-    if not hasattr(obj, "data_ptr"):
+    try:
+        if (obj.get_device() == dev and obj.nbytes >= nbytes and (dtype is None or obj.dtype == dtype)
+                and obj.is_contiguous()):
+            return obj.data_ptr()
+    except AttributeError:
         return _ptr(obj)
     if obj.get_device() != dev:
         raise ValueError(f"{what}: tensor arguments must live in device memory, on the current device {dev}; "
@@ -305,9 +309,7 @@ def _sized(dev, obj, nbytes, what, dtype=None):
         raise ValueError(f"{what}: tensor arguments must be contiguous")
     if dtype is not None and obj.dtype != dtype:
         raise ValueError(f"{what} must be a {dtype} tensor, got {obj.dtype}")
-    if obj.nbytes < nbytes:
-        raise ValueError(f"{what} holds {obj.nbytes} bytes, the call needs {nbytes}")
-    return obj.data_ptr()
+    raise ValueError(f"{what} holds {obj.nbytes} bytes, the call needs {nbytes}")
 
 
 def _place(stream):

@@ -66,6 +66,7 @@ struct TileAt {
   int64_t row0, row_end;
   int expert;
   int nt;
+  bool whole;   // more than half the kernel's height
 };
 
 // First and last row of expert e, kept inside 0..rows whatever the offsets hold.
@@ -90,91 +91,122 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// Where the tiles are.  An expert of c rows has ceil(c / BM) row tiles; their
-// total is known only here, so the grid is launched for the most there can be
-// and workgroups without a tile leave.  Every wavefront looks tiles up by
-// itself, in LDS: per expert the row tiles up to its end and its first and
-// last row.  A kernel that looks up one tile (ONE) keeps up to 64 experts in
-// a register of its lanes instead, without a barrier; in the others these
-// registers were spilled.
+// Row tiles of `rows` rows: those of more than BM / 2 rows, and the one of
+// fewer that may be left (with HALVES; else that counts as whole).
+template <int BM, bool HALVES>
+__device__ __forceinline__ int whole_tiles(int rows) {
+  return HALVES ? rows / BM + (rows % BM > BM / 2) : (rows + BM - 1) / BM;
+}
+template <int BM, bool HALVES>
+__device__ __forceinline__ int half_tiles(int rows) {
+  return HALVES && rows % BM > 0 && rows % BM <= BM / 2;
+}
+
+// Where the tiles are.  Their total is known only here, so the grid is
+// launched for the most there can be and workgroups without a tile leave.
+// Every wavefront looks tiles up by itself, in LDS: per expert the whole and
+// the half row tiles up to its end and its first and last row.  A kernel that
+// looks up one tile (ONE) keeps up to 64 experts in a register of its lanes
+// instead, without a barrier; in the others these registers were spilled.
 template <int BM, bool ONE>
 struct TileMap {
-  int f, l, incl;   // ONE: of expert `lane`
-  int row_tiles;
-  int* table;       // [3][experts]
+  int f, l, incl;     // ONE: of expert `lane`
+  int whole, halves;  // row tiles
+  int* table;         // [4][experts]
 
   // Called by all threads of the workgroup.
   __device__ __forceinline__ void init(const TileArgs& a, int* table_lds) {
     table = table_lds;
+    halves = 0;
     if (!a.offsets) {
-      row_tiles = static_cast<int>((a.rows + BM - 1) / BM);
+      whole = whole_tiles<BM, !ONE>(static_cast<int>(a.rows));
+      halves = half_tiles<BM, !ONE>(static_cast<int>(a.rows));
       return;
     }
     const int lane = threadIdx.x & 63;
     if (ONE && a.experts <= 64) {
       f = l = 0;
       if (lane < a.experts) expert_rows(a, lane, &f, &l);
-      incl = wave_scan((l - f + BM - 1) / BM);
-      row_tiles = __builtin_amdgcn_readlane(incl, 63);
+      incl = wave_scan(whole_tiles<BM, !ONE>(l - f));
+      whole = __builtin_amdgcn_readlane(incl, 63);
       return;
     }
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
       int first, last;
       expert_rows(a, e, &first, &last);
-      table[e] = (last - first + BM - 1) / BM;
-      table[a.experts + e] = first;
-      table[2 * a.experts + e] = last;
+      table[e] = whole_tiles<BM, !ONE>(last - first);
+      table[a.experts + e] = half_tiles<BM, !ONE>(last - first);
+      table[2 * a.experts + e] = first;
+      table[3 * a.experts + e] = last;
     }
     __syncthreads();
-    row_tiles = 0;
+    whole = 0;
     for (int e0 = 0; e0 < a.experts; e0 += 64) {
-      const int sum = row_tiles + wave_scan(e0 + lane < a.experts ? table[e0 + lane] : 0);
-      row_tiles = __builtin_amdgcn_readlane(sum, 63);
+      const int e = e0 + lane < a.experts ? e0 + lane : a.experts - 1;
+      const bool in = e0 + lane < a.experts;
+      const int w = whole + wave_scan(in ? table[e] : 0);
+      const int h = halves + (ONE ? 0 : wave_scan(in ? table[a.experts + e] : 0));
+      whole = __builtin_amdgcn_readlane(w, 63);
+      halves = __builtin_amdgcn_readlane(h, 63);
       __syncthreads();   // all wavefronts have read these 64; the first replaces them
-      if (e0 + lane < a.experts && threadIdx.x < 64) table[e0 + lane] = sum;
+      if (in && threadIdx.x < 64) {
+        table[e] = w;
+        table[a.experts + e] = h;
+      }
     }
     __syncthreads();
   }
 
-  // Rows and expert of row tile mt (below row_tiles).
-  __device__ __forceinline__ void rows_of(const TileArgs& a, int mt, TileAt* at) const {
+  // Rows and expert of whole row tile mt, or of half tile mt.
+  __device__ __forceinline__ void rows_of(const TileArgs& a, int mt, bool is_whole, TileAt* at) const {
     int e = 0, first = 0, last = static_cast<int>(a.rows), before = 0;
     if (ONE && a.offsets && a.experts <= 64) {
       e = __builtin_ctzll(__ballot(incl > mt));
       first = __builtin_amdgcn_readlane(f, e);
       last = __builtin_amdgcn_readlane(l, e);
-      before = __builtin_amdgcn_readlane(incl, e) - (last - first + BM - 1) / BM;
+      before = __builtin_amdgcn_readlane(incl, e) - whole_tiles<BM, !ONE>(last - first);
     } else if (a.offsets) {
       const int lane = threadIdx.x & 63;
+      const int* t = is_whole ? table : table + a.experts;
       for (int e0 = 0; e0 < a.experts; e0 += 64)   // experts whose tiles all come before mt
-        e += __builtin_popcountll(__ballot(e0 + lane < a.experts && table[e0 + lane] <= mt));
-      first = __builtin_amdgcn_readfirstlane(table[a.experts + e]);
-      last = __builtin_amdgcn_readfirstlane(table[2 * a.experts + e]);
-      before = e ? __builtin_amdgcn_readfirstlane(table[e - 1]) : 0;
+        e += __builtin_popcountll(__ballot(e0 + lane < a.experts && t[e0 + lane] <= mt));
+      first = __builtin_amdgcn_readfirstlane(table[2 * a.experts + e]);
+      last = __builtin_amdgcn_readfirstlane(table[3 * a.experts + e]);
+      before = e ? __builtin_amdgcn_readfirstlane(t[e - 1]) : 0;
     }
     at->expert = e;
-    at->row0 = first + static_cast<int64_t>(mt - before) * BM;
+    at->row0 = first + static_cast<int64_t>(is_whole ? mt - before : (last - first) / BM) * BM;
     at->row_end = last;
+    at->whole = is_whole;
   }
 
   // The i-th tile of XCD `xcd`; false past its last.  Workgroups go to the 8
-  // XCDs in turn, each with its own L2: an XCD takes a contiguous run of
-  // tiles, and the run walks groups of 8 row tiles column by column, so the
-  // workgroups that one XCD runs at a time share rows of X and of W.
+  // XCDs in turn, each with its own L2: an XCD takes a contiguous run of the
+  // whole tiles, then one of the half tiles, and a run walks groups of 8 row
+  // tiles column by column, so the workgroups that one XCD runs at a time
+  // share rows of X and of W.
   __device__ __forceinline__ bool find(const TileArgs& a, uint32_t xcd, int64_t i, TileAt* at) const {
-    const int64_t total = static_cast<int64_t>(row_tiles) * a.tiles_n;
-    const int64_t per = total / kXcds;
-    const uint32_t rem = static_cast<uint32_t>(total % kXcds);
-    if (i >= per + (xcd < rem ? 1 : 0)) return false;
-    const uint32_t lin = static_cast<uint32_t>(xcd * per + (xcd < rem ? xcd : rem) + i);   // below 2^31
-    constexpr uint32_t kGroup = 8;
-    const uint32_t width = kGroup * static_cast<uint32_t>(a.tiles_n);
-    const uint32_t g = lin / width, in = lin % width;
-    const uint32_t left = static_cast<uint32_t>(row_tiles) - g * kGroup;
-    const uint32_t gm = left < kGroup ? left : kGroup;
-    at->nt = static_cast<int>(in / gm);
-    rows_of(a, static_cast<int>(g * kGroup + in % gm), at);
-    return true;
+    for (int part = 0; part < 2; ++part) {
+      const int row_tiles = part ? halves : whole;
+      const int64_t total = static_cast<int64_t>(row_tiles) * a.tiles_n;
+      const int64_t per = total / kXcds;
+      const uint32_t rem = static_cast<uint32_t>(total % kXcds);
+      const int64_t count = per + (xcd < rem ? 1 : 0);
+      if (i >= count) {
+        i -= count;
+        continue;
+      }
+      const uint32_t lin = static_cast<uint32_t>(xcd * per + (xcd < rem ? xcd : rem) + i);   // below 2^31
+      constexpr uint32_t kGroup = 8;
+      const uint32_t width = kGroup * static_cast<uint32_t>(a.tiles_n);
+      const uint32_t g = lin / width, in = lin % width;
+      const uint32_t left = static_cast<uint32_t>(row_tiles) - g * kGroup;
+      const uint32_t gm = left < kGroup ? left : kGroup;
+      at->nt = static_cast<int>(in / gm);
+      rows_of(a, static_cast<int>(g * kGroup + in % gm), part == 0, at);
+      return true;
+    }
+    return false;
   }
 };
 
@@ -322,7 +354,6 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   static_assert(kTM % 2 == 0, "a wavefront takes its rows of X in two halves");
   constexpr int kXh = BM / 16 / kWaves, kWn = BN / 8 / kWaves, kPer = 2 * kXh + kWn;
   static_assert(kXh * kWaves * 16 == BM && kWn * kWaves * 8 == BN, "loads divide evenly among the wavefronts");
-  constexpr int kHalfRows8 = BM / WM / 16;   // 8-row groups in half a wavefront's rows
   constexpr int kStage = (BM + BN) * 128;
   constexpr int kCols = GATED ? BN / 2 : BN;
   static_assert(kTN % (GATED ? 4 : 2) == 0, "a wavefront holds pairs of sub-tiles, gate and up of the same columns");
@@ -342,9 +373,12 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   map.init(a, index_l + BM);
   const uint32_t xcd = blockIdx.x % kXcds;
   const int64_t slots = gridDim.x / kXcds;
-  int64_t ith = blockIdx.x / kXcds;
+  // The XCD's tiles, whole ones first, are dealt to its workgroups back and
+  // forth, so that those with fewer whole tiles get more of the halves.
+  const int64_t slot = blockIdx.x / kXcds;
+  int64_t turn = 0;
   TileAt at, to;
-  if (!map.find(a, xcd, ith, &at)) return;
+  if (!map.find(a, xcd, slot, &at)) return;
 
   const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;   // the same place in every row this lane loads
   const int last_step = (a.kbytes + 127) >> 7;
@@ -357,8 +391,8 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   auto pair_col = [&](int jj, int g) { return a.y_f16 ? 8 * g + 4 * jj : 16 * jj + 4 * g; };
 
   // The wavefront's load instructions of a step, 8 LDS rows each: first those
-  // of the first half of every wavefront's rows of X (kXh) and of W (kWn),
-  // then those of the second half of X.  Addresses are 32-bit offsets from
+  // of the first half of the rows of X (kXh) and of W (kWn), then those of
+  // the second half of X.  Addresses are 32-bit offsets from
   // bases that stay for a tile, the step in a scalar register: with 64-bit
   // addresses advanced per step the vector ALU work of the loads cost 5-8%
   // (8192x4096x4096 124 against 116 us).  An offset past the end loads zeros.
@@ -369,8 +403,7 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     if (j < kXh || j >= kXh + kWn) {
-      const int h = wave * kXh + (j < kXh ? j : j - kXh - kWn);   // 8 rows among BM / 2
-      dst[j] = (h / kHalfRows8 * (2 * kHalfRows8) + h % kHalfRows8 + (j < kXh ? 0 : kHalfRows8)) * 1024;
+      dst[j] = (j < kXh ? wave * kXh + j : BM / 16 + wave * kXh + j - kXh - kWn) * 1024;
     } else {
       dst[j] = (BM / 8 + wave * kWn + j - kXh) * 1024;
     }
@@ -404,7 +437,8 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
         r = r < rows ? r : rows - 1;
         const int i = a.x_rows ? index_l[r] : r;
         // a row that there is not loads zeros; its products are dropped below
-        src[j] = i >= 0 && i < (a.x_rows ? a.x_tokens : x_left) ? static_cast<uint32_t>(i) * a.kbytes + chunk : kNoOffset;
+        const bool ok = i >= 0 && i < (a.x_rows ? a.x_tokens : x_left) && (t.whole || j < kXh);
+        src[j] = ok ? static_cast<uint32_t>(i) * a.kbytes + chunk : kNoOffset;
       } else {
         const int c = dst[j] / 128 - BM + (lane >> 3), sub = GATED ? c >> 5 : c >> 4;
         const int col = (sub >> 1) * 32 + pair_col(sub & 1, (c & 15) >> 2) + (c & 3);
@@ -454,27 +488,28 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   typename E::Acc acc[kTM][kTN];
   const int wm = wave % WM, wn = wave / WM;
   const int place = ((lane >> 4) ^ (lane & 7)) * 16;
-  const int xrow = (wm * kTM * 16 + (lane & 15)) * 128;
+  const int xrow = (wm * kHalf * 16 + (lane & 15)) * 128;
   const int wrow = (BM + wn * kTN * 16 + (lane & 15)) * 128;
   i32x4 xa[kHalf], xb[kHalf], wa[kTN], wb[kTN];
   auto read_x = [&](const uint8_t* buf, int half, int ks, i32x4* f) {
 #pragma unroll
     for (int i = 0; i < kHalf; ++i)
-      f[i] = *reinterpret_cast<const i32x4*>(buf + xrow + (half * kHalf + i) * 2048 + (place ^ (64 * ks)));
+      f[i] = *reinterpret_cast<const i32x4*>(buf + xrow + half * (BM * 64) + i * 2048 + (place ^ (64 * ks)));
   };
   auto read_w = [&](const uint8_t* buf, int ks, i32x4* f) {
 #pragma unroll
     for (int j = 0; j < kTN; ++j) f[j] = *reinterpret_cast<const i32x4*>(buf + wrow + j * 2048 + (place ^ (64 * ks)));
   };
-  // One phase: the products of half the rows and half a step, among them the
-  // READS of the next phase and LOADS of a later step.
-  auto mma = [&](int half, const i32x4* x, const i32x4* w, auto reads, auto loads) {
+  // One phase: the products of rows i0..i1-1 of a half and of half a step,
+  // among them the READS of the next phase and LOADS of a later step.
+  auto mma = [&](int half, auto i0, auto i1, const i32x4* x, const i32x4* w, auto reads, auto loads) {
+    constexpr int kI0 = decltype(i0)::value, kI1 = decltype(i1)::value;
     constexpr int kReads = decltype(reads)::value, kLoads = decltype(loads)::value;
 #pragma unroll
-    for (int i = 0; i < kHalf; ++i)
+    for (int i = kI0; i < kI1; ++i)
 #pragma unroll
       for (int j = 0; j < kTN; ++j) acc[half * kHalf + i][j] = E::mma(w[j], x[i], acc[half * kHalf + i][j]);
-    constexpr int kRun = kHalf * kTN / (kReads + kLoads) < 1 ? 1 : kHalf * kTN / (kReads + kLoads);
+    constexpr int kEach = (kI1 - kI0) * kTN / (kReads + kLoads ? kReads + kLoads : 1), kRun = kEach < 1 ? 1 : kEach;
 #pragma unroll
     for (int r = 0; r < kReads; ++r) {
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
@@ -494,10 +529,12 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   constexpr std::integral_constant<int, kMid> kL1{};
   constexpr std::integral_constant<int, kFirst - kMid> kL2{};
   constexpr std::integral_constant<int, kXh> kL3{};
-  // Waits for all but the newest kPer loads and for the reads; then for the
+  constexpr std::integral_constant<int, kPer> kAll{};
+  constexpr std::integral_constant<int, (kHalf + 1) / 2> kMidRow{};   // of a half's sub-tiles
+  // Waits for all but the newest N loads and for the reads; then for the
   // other wavefronts.
-  auto sync = [&](bool loads) {
-    if (loads) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPer) : "memory");
+  auto sync = [&](bool loads, auto newest) {
+    if (loads) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(decltype(newest)::value) : "memory");
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -506,18 +543,18 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
   if (a.x_rows) {
     load_index(at);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    sync(false);
+    sync(false, kAll);
   }
   turn_to(at, 0);
   issue(0, 0, 0, kPer);
   issue(1, 1, 0, kPer);
-  sync(true);
+  sync(true, kAll);
   read_x(lds, 0, 0, xa);
   read_w(lds, 0, wa);
   int buf = 0, set = 0;
   for (;;) {
-    ith += slots;
-    const bool more = map.find(a, xcd, ith, &to);
+    ++turn;
+    const bool more = map.find(a, xcd, turn * slots + (turn & 1 ? slots - 1 - slot : slot), &to);
     if (more) load_index(to);
 #pragma unroll
     for (int i = 0; i < kTM; ++i)
@@ -525,34 +562,52 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
       for (int j = 0; j < kTN; ++j) acc[i][j] = E::zero();
     __builtin_amdgcn_sched_barrier(0);
     // The loads run two steps ahead: in the last two steps of a tile they
-    // are the first two of the next.
-    for (int s = 0; s < steps; ++s) {
+    // are the first two of the next.  A tile's first step has been waited for
+    // before the epilogue.
+    auto turn_at = [&](int s) {
+      if (s != steps - 2) return;
+      if (more)
+        turn_to(to, set ^ 1);
+      else
+        limit = 0;
+    };
+    auto step = [&](int s, auto whole) {
       const uint8_t* here = lds + buf * kStage;
       const uint8_t* next = lds + (buf ^ 1) * kStage;
+      const int ahead = s + 2 < steps ? s + 2 : s + 2 - steps;
       read_x(here, 0, 1, xb);
       read_w(here, 1, wb);
-      mma(0, xa, wa, kXW, kNone);
-      sync(s > 0);   // a tile's first step has been waited for before the epilogue
-      if (s == steps - 2) {
-        if (more)
-          turn_to(to, set ^ 1);
-        else
-          limit = 0;
+      mma(0, kNone, kX, xa, wa, kXW, kNone);
+      sync(s > 0, kAll);
+      turn_at(s);
+      if constexpr (decltype(whole)::value) {
+        read_x(here, 1, 0, xa);
+        issue(ahead, buf, 0, kMid);
+        mma(0, kNone, kX, xb, wb, kX, kL1);
+        read_x(here, 1, 1, xb);
+        issue(ahead, buf, kMid, kFirst);
+        mma(1, kNone, kX, xa, wa, kX, kL2);
+        sync(true, kAll);
+        read_x(next, 0, 0, xa);
+        read_w(next, 0, wa);
+        issue(ahead, buf, kFirst, kPer);
+        mma(1, kNone, kX, xb, wb, kXW, kL3);
+      } else {
+        // half a tile: phases 0 and 1 alone, the barrier before the next
+        // step's operands in the middle of phase 1
+        issue(ahead, buf, 0, kPer);
+        mma(0, kNone, kMidRow, xb, wb, kNone, kAll);
+        sync(true, kAll);
+        read_x(next, 0, 0, xa);
+        read_w(next, 0, wa);
+        mma(0, kMidRow, kX, xb, wb, kXW, kNone);
       }
-      const int ahead = s + 2 < steps ? s + 2 : s + 2 - steps;
-      read_x(here, 1, 0, xa);
-      issue(ahead, buf, 0, kMid);
-      mma(0, xb, wb, kX, kL1);
-      read_x(here, 1, 1, xb);
-      issue(ahead, buf, kMid, kFirst);
-      mma(1, xa, wa, kX, kL2);
-      sync(true);
-      read_x(next, 0, 0, xa);
-      read_w(next, 0, wa);
-      issue(ahead, buf, kFirst, kPer);
-      mma(1, xb, wb, kXW, kL3);
       buf ^= 1;
-    }
+    };
+    if (at.whole)
+      for (int s = 0; s < steps; ++s) step(s, std::true_type{});
+    else
+      for (int s = 0; s < steps; ++s) step(s, std::false_type{});
     // the next tile's first step, before this tile's stores count as the newest
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPer) : "memory");
     const int64_t n0 = static_cast<int64_t>(at.nt) * kCols;
@@ -564,7 +619,8 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
     constexpr int kG = GATED ? 2 : 1;
 #pragma unroll
     for (int i = 0; i < kTM; ++i) {
-      const int r = (wm * kTM + i) * 16 + (lane & 15);
+      if (i >= kHalf && !at.whole) break;
+      const int r = i / kHalf * (BM / 2) + (wm * kHalf + i % kHalf) * 16 + (lane & 15);
       const int64_t row = at.row0 + r;
       const float xs = xs_l[r];
 #pragma unroll
@@ -768,7 +824,7 @@ inline int launch_tiles(const void* fn, pesti::TileArgs a, int bm, int cols, int
 
 template <typename E, int BM, int BN, int WM, int WN, bool GATED>
 int launch_tile(const pesti::TileArgs& a, hipStream_t st) {
-  const int64_t lds = pesti::tile_lds<BM, BN>() + (a.offsets ? 12 * a.experts : 0);
+  const int64_t lds = pesti::tile_lds<BM, BN>() + (a.offsets ? 16 * a.experts : 0);
   return launch_tiles(reinterpret_cast<const void*>(&pesti::gemm_tile_kernel<E, BM, BN, WM, WN, GATED>), a, BM,
                       GATED ? BN / 2 : BN, WM * WN * 64, lds, kCus * (kCuLds / lds), st);
 }
@@ -776,18 +832,24 @@ int launch_tile(const pesti::TileArgs& a, hipStream_t st) {
 template <typename E, int MT, int NW, int D, bool GATED>
 int launch_rows_w(const pesti::TileArgs& a, hipStream_t st) {
   return launch_tiles(reinterpret_cast<const void*>(&pesti::gemm_rows_kernel<E, MT, NW, D, GATED>), a, 16 * MT, 16,
-                      NW * 64, a.offsets && a.experts > 64 ? 12 * a.experts : 0, 0, st);
+                      NW * 64, a.offsets && a.experts > 64 ? 16 * a.experts : 0, 0, st);
 }
 template <typename E, int MT, bool GATED>
 int launch_rows(const pesti::TileArgs& a, hipStream_t st) {
   return a.kbytes <= 2048 ? launch_rows_w<E, MT, 2, 4, GATED>(a, st) : launch_rows_w<E, MT, 4, 5, GATED>(a, st);
 }
 
-// Tiles of bm rows and cols columns that a launch comes to: experts' rows end
-// on average half a tile early.
-inline int64_t tiles_about(const pesti::TileArgs& a, int bm, int cols) {
-  const int64_t half = a.experts < a.rows ? (a.experts + 1) / 2 : 0;
-  const int64_t row_tiles = a.offsets && half ? a.rows / bm + half : most_row_tiles(a, bm);
+// Tiles of bm rows and cols columns that a launch comes to, in tenths: a half
+// tile takes 6 tenths of a whole one's time, and an expert's last tile,
+// anywhere from empty to full, on average 3 more than its rows' share.
+inline int64_t tenths_of_tiles(const pesti::TileArgs& a, int64_t bm, int64_t cols) {
+  int64_t row_tiles;
+  if (a.offsets) {
+    row_tiles = a.rows * 10 / bm + 3 * std::min<int64_t>(a.experts, a.rows);
+  } else {
+    const int64_t left = a.rows % bm;
+    row_tiles = a.rows / bm * 10 + (left > bm / 2 ? 10 : left > 0 ? 6 : 0);
+  }
   return row_tiles * ((a.n + cols - 1) / cols);
 }
 
@@ -824,7 +886,9 @@ int launch_any(const pesti::TileArgs& a, hipStream_t st) {
     if constexpr (!GATED)
       if (r4 * cols <= kCus) return launch_rows<E, 4, GATED>(a, st);
   }
-  auto cost = [&](int bm, int bn, int64_t unit) { return (tiles_about(a, bm, bn / kG) + kCus - 1) / kCus * unit; };
+  auto cost = [&](int64_t bm, int64_t bn, int64_t unit) {
+    return (tenths_of_tiles(a, bm, bn / kG) + 10 * kCus - 1) / (10 * kCus) * unit;
+  };
   const int64_t c0 = cost(64, 128, 10), c1 = cost(128, 128, 16), c2 = cost(128, 256, 30), c3 = cost(256, 256, 53);
   const int64_t low = std::min(std::min(c0, c1), std::min(c2, c3));
   if (c3 == low) return launch_tile<E, 256, 256, 2, 4, GATED>(a, st);
