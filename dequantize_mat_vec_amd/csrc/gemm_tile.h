@@ -861,8 +861,12 @@ inline int64_t tenths_of_tiles(const pesti::TileArgs& a, int64_t bm, int64_t col
 // tile: 8-bit 64x896x4864 7.8 / 10 / 14 / 16, 128x896x4864 12 / 10 / 15 / 17,
 // 256x896x4864 21 / 18 / 15 / 18, 40x4864x896 6.8 / 7.6 / 7.1 / 7.4, 100x4864x896
 // 11 / 10 / 10 / 7.8; 8 experts of one row, gated 1024x2048, 9.9 against 13).
-// With more tiles, tiles win for one row as for many (8-bit 1x151936x896: 28
-// against 34 us; 50 experts of five rows, 1408x2048: 36 both).
+// With more tiles, tiles win for one row as for many (8-bit 1x151936x896 29
+// against 30 us, 16x151936x896 32 against 39), but for experts of up to four
+// rows with long rows of W or with few tiles: two tokens of four experts,
+// binary16 896x2432, 11 against 19 us, eight 23 against 27; 24 tokens of
+// eight of 64 experts, gated 8-bit 1024x2048, 44 against 48; but 60 experts of
+// two rows, 2944x896, 29 against 25, of 1024 and more tiles.
 //
 // Among the tiles, time goes by how many each compute unit gets (a 128 x 128
 // tile takes 1.6 times a 64 x 128 one, 128 x 256 3 times, 256 x 256 5.3
@@ -878,7 +882,10 @@ inline int64_t tenths_of_tiles(const pesti::TileArgs& a, int64_t bm, int64_t col
 template <typename E, bool GATED>
 int launch_any(const pesti::TileArgs& a, hipStream_t st) {
   constexpr int kG = GATED ? 2 : 1;
-  if (most_row_tiles(a, 64) * ((a.n + 128 / kG - 1) / (128 / kG)) < kCus) {
+  const int64_t tiles = most_row_tiles(a, 64) * ((a.n + 128 / kG - 1) / (128 / kG));
+  if (a.offsets && a.rows <= 4 * a.experts && (tiles < 2 * kCus || a.kbytes >= 2048))
+    return launch_rows<E, 1, GATED>(a, st);
+  if (tiles < kCus) {
     const int64_t cols = (a.n + 15) / 16, limit = kCus * 3 / 2;
     const int64_t r1 = most_row_tiles(a, 16), r2 = most_row_tiles(a, 32), r4 = most_row_tiles(a, 64);
     if (r1 * cols <= limit || r1 == r4) return launch_rows<E, 1, GATED>(a, st);
