@@ -19,7 +19,7 @@ int run(int32_t format, pesti::TileArgs a, int64_t experts, int64_t in_features,
   const bool i8 = format == PESTI_FMT_I8ROW;
   if (!i8 && format != PESTI_FMT_F16) return PESTI_ERR_SHAPE;
   if (y_format != PESTI_FMT_F32 && y_format != PESTI_FMT_F16) return PESTI_ERR_SHAPE;
-  if (a.n < 0 || in_features < 0 || in_features % 32 != 0 || in_features > PESTI_MAX_IN_FEATURES)
+  if (a.n < 0 || a.n > INT32_MAX || in_features < 0 || in_features % 32 != 0 || in_features > PESTI_MAX_IN_FEATURES)
     return PESTI_ERR_SHAPE;
   if (experts < 0 || experts > PESTI_MAX_EXPERTS) return PESTI_ERR_SHAPE;
   if (a.rows < 0 || a.rows > PESTI_MAX_TOKENS || a.x_tokens < 0 || a.x_tokens > PESTI_MAX_TOKENS)

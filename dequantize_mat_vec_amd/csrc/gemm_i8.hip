@@ -13,7 +13,8 @@ extern "C" int pesti_gemm_i8row_i8token(int64_t m, int64_t out_features, int64_t
                                         const float* row_scales, const int8_t* x_codes, const float* x_scales,
                                         int32_t y_format, void* y, const float* bias, void* stream) {
   if (y_format != PESTI_FMT_F32 && y_format != PESTI_FMT_F16) return PESTI_ERR_SHAPE;
-  if (out_features < 0 || in_features < 0 || in_features % 32 != 0 || in_features > PESTI_MAX_IN_FEATURES)
+  if (out_features < 0 || out_features > INT32_MAX || in_features < 0 || in_features % 32 != 0 ||
+      in_features > PESTI_MAX_IN_FEATURES)
     return PESTI_ERR_SHAPE;
   if (m < 0 || m > PESTI_MAX_TOKENS) return PESTI_ERR_BATCH;
   if (m == 0 || out_features == 0) return PESTI_OK;

@@ -813,7 +813,7 @@ inline int launch_tiles(const void* fn, pesti::TileArgs a, int bm, int cols, int
   const int64_t tn = (a.n + cols - 1) / cols;
   const int64_t total = most_row_tiles(a, bm) * tn;
   // Tiles are numbered in 31 bits; the grid is rounded up to whole turns of the XCDs.
-  if (tn > (1 << 27) || total > INT32_MAX - pesti::kXcds) return PESTI_ERR_SHAPE;
+  if (total > INT32_MAX - pesti::kXcds) return PESTI_ERR_SHAPE;
   a.tiles_n = static_cast<int32_t>(tn);
   void* params[] = {&a};
   unsigned grid = static_cast<unsigned>((total + pesti::kXcds - 1) / pesti::kXcds * pesti::kXcds);

@@ -361,8 +361,9 @@ int pesti_gemm_smallm_noalloc(int32_t format, int64_t m, int64_t out_features, i
  * PESTI_FMT_F16 rounded once from float32).  The float32 value is
  * fma(float(sum) * x_scale, row_scale, bias): three roundings.
  *
- * m in [0, PESTI_MAX_TOKENS], else PESTI_ERR_BATCH; codes, x and Y 16-byte
- * aligned, scales and bias 4; an unknown format is PESTI_ERR_SHAPE. */
+ * m in [0, PESTI_MAX_TOKENS], else PESTI_ERR_BATCH; out_features below 2^31
+ * and fewer than 2^31 tiles of Y, else PESTI_ERR_SHAPE, as is an unknown
+ * format; codes, x and Y 16-byte aligned, scales and bias 4. */
 int pesti_quant_i8token(int32_t x_format, int64_t m, int64_t in_features, const void* x,
                         int8_t* codes, float* scales, void* stream);
 int pesti_gemm_i8row_i8token(int64_t m, int64_t out_features, int64_t in_features,
@@ -390,9 +391,10 @@ int pesti_gemm_i8row_i8token(int64_t m, int64_t out_features, int64_t in_feature
  *   x_rows   int32 [rows] in device memory, the row of X for each row of Y
  *            (the same one any number of times), or NULL for row r itself,
  *            which needs x_tokens >= rows (else PESTI_ERR_BATCH).  An index
- *            outside 0..x_tokens-1 stands for a row of zeros.  Rows that are
- *            picked are addressed in 32 bits: X of 4 GiB or more with x_rows
- *            is PESTI_ERR_SHAPE.
+ *            outside 0..x_tokens-1 stands for a row of zeros: in binary16 its
+ *            sums are 0 whatever W holds, in 8 bits codes and scale are 0.
+ *            Rows that are picked are addressed in 32 bits: X of 4 GiB or
+ *            more with x_rows is PESTI_ERR_SHAPE.
  *   y        [rows][out] in y_format (PESTI_FMT_F32 or PESTI_FMT_F16)
  *
  * pesti_gemm_experts_swiglu joins the gate and up products of the same rows
@@ -401,9 +403,9 @@ int pesti_gemm_i8row_i8token(int64_t m, int64_t out_features, int64_t in_feature
  * h [rows][out] in h_format; no bias.
  *
  * rows and x_tokens in [0, PESTI_MAX_TOKENS] (PESTI_ERR_BATCH), experts in
- * [0, PESTI_MAX_EXPERTS] (PESTI_ERR_SHAPE); sums in float32 (binary16) or
- * exactly in 32-bit integers.  rows, out_features or experts of 0 return 0
- * without touching a pointer. */
+ * [0, PESTI_MAX_EXPERTS] and out_features below 2^31 (PESTI_ERR_SHAPE); sums
+ * in float32 (binary16) or exactly in 32-bit integers.  rows, out_features or
+ * experts of 0 return 0 without touching a pointer. */
 int pesti_gemm_experts(int32_t format, int64_t rows, int64_t experts, int64_t out_features,
                        int64_t in_features, const int32_t* offsets, const void* w,
                        const float* w_scales, int64_t x_tokens, const void* x,

@@ -104,6 +104,16 @@ def test_experts_refusals(gated):
         assert call(**kw, **empty) == _lib.PESTI_OK
 
 
+@pytest.mark.parametrize("n", [1 << 31, 1 << 62, (1 << 63) - 1])
+def test_columns_beyond_31_bits_are_refused(n):
+    """Column tiles are numbered in 27 bits, and sums with so large a number would leave 64."""
+    f = _lib.load().pesti_gemm_i8row_i8token
+    assert f(4, n, 64, FAKE, FAKE, FAKE, FAKE, F32, FAKE, None, None) == _lib.PESTI_ERR_SHAPE
+    for gated in (False, True):
+        for rows in (4, 4096):
+            assert experts_call(gated, n=n, rows=rows, t=rows) == _lib.PESTI_ERR_SHAPE
+
+
 def test_binding_refuses_host_tensors_and_unknown_types():
     import torch
     with pytest.raises(ValueError):
