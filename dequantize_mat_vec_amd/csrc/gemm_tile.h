@@ -292,11 +292,16 @@ __device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const
 // buffers.  Loads go from memory straight into LDS, 1 KB (8 rows of 128
 // bytes, whole cache lines) per wavefront instruction.
 //
-// What bounds it is those loads, not the matrix cores: a step of a 256 x 256
-// tile is 2048 cycles of products per SIMD and 64 KB through the CU's vector
-// memory path.  So they run all the time, one step's worth in flight, and a
-// buffer is refilled in two parts, each as soon as it has been read.  A
-// wavefront takes a step in four phases,
+// What bounds it where there are enough rows is power: 8192x4096x4096 in 8
+// bits takes 85 us with operands of zeros and 114-118 with random ones (126
+// on a slower card, where products and barriers alone, with nothing loaded,
+// read or stored, took 103), and the matrix cores by themselves reach 4400-4800 and
+// 3570-3990 TOP/s (binary16 2260-2410 and 1730-1840).  Short rows are bound
+// by stores as well, experts of few rows by reading W.  A step of a 256 x 256
+// tile is 2048 cycles of products per SIMD and 64 KB of loads, one step's
+// worth in flight (three and four steps of 64-byte rows took as long): loads
+// run all the time, and a buffer is refilled in two parts, each as soon as
+// it has been read.  A wavefront takes a step in four phases,
 //
 //   phase  products           reads for the next       refills
 //     0    rows half 0, k 0   half 0, k 1; W k 1
@@ -325,7 +330,7 @@ __device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const
 // 2048 x 1024 (now 114; the K loop alone about 70).
 //
 // 8192x4096x4096 in 8 bits, binary16 Y: 114 us (2.4 POP/s) in 256 x 256
-// tiles; the products alone (nothing loaded or read) take 78 us.
+// tiles; the same kernel without its loads and reads takes 78 us.
 // ---------------------------------------------------------------------------
 #ifdef __HIP_DEVICE_COMPILE__   // the host compiler needs only the kernels' names
 // A value that what is computed from it is computed from again: the compiler
@@ -667,6 +672,9 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
 // What bounds it is latency: finding the expert, the picked rows, one trip
 // for W, the sum.  So NW and D are the fewest that have a whole row of common
 // lengths in flight at once; loads past the row's end cost their issue.
+// Four experts of one row, binary16 896x2432 (17.4 MB of W): 6.6 us, 2.6 TB/s;
+// eight, gated 8-bit 1024x2048 (33.6 MB): 9.2 us, 3.7 TB/s; one token, 8-bit
+// 896x896: 4.0.
 // ---------------------------------------------------------------------------
 template <typename E, int MT, int NW, int D, bool GATED>
 __global__ __launch_bounds__(NW * 64) void gemm_rows_kernel(TileArgs a) {
@@ -870,7 +878,7 @@ inline int64_t tenths_of_tiles(const pesti::TileArgs& a, int64_t bm, int64_t col
 //
 // Among the tiles, time goes by how many each compute unit gets (a 128 x 128
 // tile takes 1.6 times a 64 x 128 one, 128 x 256 3 times, 256 x 256 5.3
-// times: bytes into LDS bound them, (BM + BN) / (BM BN) per product), so the
+// times: a product costs (BM + BN) / (BM BN) bytes into LDS), so the
 // least of tiles per unit times that is taken.  Measured (us at 64x128 /
 // 128x128 / 128x256 / 256x256): 8-bit 8192x4096x4096 175 / 153 / 135 / 114,
 // 4096x4096x4096 91 / 70 / 67 / 60, 2048x4864x896 19 / 19 / 22 / 20,
