@@ -170,6 +170,55 @@ def test_gemm_i8_larger(m, n, k):
     close(run_i8(q, s, w, ws, None, "f32"), y, i8_tolerance(y, size, "f32"), "gemm_i8")
 
 
+@pytest.mark.parametrize("kind", ["f32", "f16"])
+@pytest.mark.parametrize("m,n,k", [(8064, 4096, 32), (8065, 4096, 32), (8193, 4096, 32), (1984, 4096, 160),
+                                   (1985, 4096, 160), (1921, 4096, 160), (4160, 896, 288), (4161, 896, 288),
+                                   (4097, 896, 288), (544, 2304, 96), (545, 2304, 96)])
+def test_gemm_i8_rows_end_at_half_a_tile(m, n, k, kind):
+    """The last rows are half a tile, one more, or one alone, in tiles of 256, 128 (by 256 and by 128 columns) and
+    64 rows; the rows behind Y stay as they were."""
+    announce(f"gemm_i8 ends {kind} m{m} n{n} k{k}")
+    rng = np.random.default_rng([21, m, n])
+    q, w, s, ws = codes(rng, m, k), codes(rng, n, k), scales(rng, m), scales(rng, n)
+    y, size = oracle.gemm_i8(q, s, w, ws)
+    close(run_i8(q, s, w, ws, None, kind), y, i8_tolerance(y, size, kind), "gemm_i8")
+
+
+@pytest.mark.parametrize("m", [1, 50, 700])
+def test_linear_layer_captured_and_replayed(m):
+    """Quantizer and product in a graph on new tokens each time: every replay has the eager calls' bits."""
+    torch, dev = torch_dev()
+    rng = np.random.default_rng([22, m])
+    n, k = 200, 352
+    w, ws, bias = to_dev(codes(rng, n, k)), to_dev(scales(rng, n)), to_dev(rng.standard_normal(n).astype(np.float32))
+    x = torch.empty(m, k, device=dev)
+    q, s = torch.empty(m, k, dtype=torch.int8, device=dev), torch.empty(m, device=dev)
+    y = torch.empty(m, n, device=dev)
+
+    def run():
+        dmv.pesti_quant_i8token("f32", m, k, x, q, s)
+        dmv.pesti_gemm_i8row_i8token(m, n, k, w, ws, q, s, y, bias)
+    x.normal_()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            run()
+    for r in range(4):
+        announce(f"linear graph m{m} replay {r}")
+        x.copy_(to_dev(rng.standard_normal((m, k)).astype(np.float32)))
+        y.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        replayed = y.clone()
+        run()
+        torch.cuda.synchronize()
+        assert torch.equal(replayed, y), r
+
+
 @pytest.mark.parametrize("m", [1, 40, 200])
 def test_gemm_i8_sums_are_exact_at_the_limits(m):
     """The largest sums there are (128^2 * 32768 = 2^29), and unit scales: every output an integer, exact
