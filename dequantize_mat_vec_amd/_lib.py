@@ -307,9 +307,9 @@ def _sized(dev, obj, nbytes, what, dtype=None):
                          f"got {obj.device}")
     if not obj.is_contiguous():
         raise ValueError(f"{what}: tensor arguments must be contiguous")
-    if dtype is not None and obj.dtype != dtype:
-        raise ValueError(f"{what} must be a {dtype} tensor, got {obj.dtype}")
-    raise ValueError(f"{what} holds {obj.nbytes} bytes, the call needs {nbytes}")
+    if obj.nbytes < nbytes:
+        raise ValueError(f"{what} holds {obj.nbytes} bytes, the call needs {nbytes}")
+    raise ValueError(f"{what} must be a {dtype} tensor, got {obj.dtype}")
 
 
 def _place(stream):
@@ -325,6 +325,15 @@ def _place(stream):
 
 
 _TYPE_FORMATS = {"torch.float32": 17, "torch.float16": 16}   # by str(dtype)
+_TYPES = {17: "float32", 16: "float16", 3: "int8"}           # the torch type of a format's values
+
+
+def _type_of(torch, fid):
+    """The tensor type that format fid's values must have: bfloat16 has binary16's
+    size and uint8 the codes', so sizes alone would let them pass as those.
+    None for an id that the library refuses."""
+    name = _TYPES.get(fid)
+    return name and getattr(torch, name)
 
 
 def _value_format(fmt, obj, what):
@@ -344,8 +353,8 @@ def pesti_quant_i8token(x_format, m, in_features, x, codes, scales, stream=None)
     fid, size = _value_format(x_format, x, "x")
     torch, dev, st = _place(stream)
     return _check("pesti_quant_i8token", load().pesti_quant_i8token(
-        fid, m, in_features, _sized(dev, x, m * in_features * size, "x"), _sized(dev, codes, m * in_features, "codes"),
-        _sized(dev, scales, 4 * m, "scales", torch.float32), st))
+        fid, m, in_features, _sized(dev, x, m * in_features * size, "x", _type_of(torch, fid)),
+        _sized(dev, codes, m * in_features, "codes", torch.int8), _sized(dev, scales, 4 * m, "scales", torch.float32), st))
 
 
 def pesti_gemm_i8row_i8token(m, out_features, in_features, codes, row_scales, x_codes, x_scales, y, bias=None,
@@ -354,9 +363,10 @@ def pesti_gemm_i8row_i8token(m, out_features, in_features, codes, row_scales, x_
     fid, size = _value_format(y_format, y, "y")
     torch, dev, st = _place(stream)
     return _check("pesti_gemm_i8row_i8token", load().pesti_gemm_i8row_i8token(
-        m, out_features, in_features, _sized(dev, codes, out_features * in_features, "codes"),
-        _sized(dev, row_scales, 4 * out_features, "row_scales", torch.float32), _sized(dev, x_codes, m * in_features, "x_codes"),
-        _sized(dev, x_scales, 4 * m, "x_scales", torch.float32), fid, _sized(dev, y, m * out_features * size, "y"),
+        m, out_features, in_features, _sized(dev, codes, out_features * in_features, "codes", torch.int8),
+        _sized(dev, row_scales, 4 * out_features, "row_scales", torch.float32),
+        _sized(dev, x_codes, m * in_features, "x_codes", torch.int8), _sized(dev, x_scales, 4 * m, "x_scales", torch.float32),
+        fid, _sized(dev, y, m * out_features * size, "y", _type_of(torch, fid)),
         _sized(dev, bias, 4 * out_features, "bias", torch.float32), st))
 
 
@@ -373,12 +383,14 @@ def pesti_gemm_experts(fmt, rows, experts, out_features, in_features, offsets, w
     fid, size = _expert_format(fmt)
     yid, ysize = _value_format(y_format, y, "y")
     torch, dev, st = _place(stream)
+    values = _type_of(torch, fid)
     return _check("pesti_gemm_experts", load().pesti_gemm_experts(
         fid, rows, experts, out_features, in_features, _sized(dev, offsets, 4 * (experts + 1), "offsets", torch.int32),
-        _sized(dev, w, experts * out_features * in_features * size, "w"),
+        _sized(dev, w, experts * out_features * in_features * size, "w", values),
         _sized(dev, w_scales, 4 * experts * out_features, "w_scales", torch.float32), x_tokens,
-        _sized(dev, x, x_tokens * in_features * size, "x"), _sized(dev, x_scales, 4 * x_tokens, "x_scales", torch.float32),
-        _sized(dev, x_rows, 4 * rows, "x_rows", torch.int32), yid, _sized(dev, y, rows * out_features * ysize, "y"),
+        _sized(dev, x, x_tokens * in_features * size, "x", values), _sized(dev, x_scales, 4 * x_tokens, "x_scales", torch.float32),
+        _sized(dev, x_rows, 4 * rows, "x_rows", torch.int32), yid,
+        _sized(dev, y, rows * out_features * ysize, "y", _type_of(torch, yid)),
         _sized(dev, bias, 4 * experts * out_features, "bias", torch.float32), st))
 
 
@@ -389,14 +401,15 @@ def pesti_gemm_experts_swiglu(fmt, rows, experts, out_features, in_features, off
     fid, size = _expert_format(fmt)
     hid, hsize = _value_format(h_format, h, "h")
     torch, dev, st = _place(stream)
+    values = _type_of(torch, fid)
     w_bytes, s_bytes = experts * out_features * in_features * size, 4 * experts * out_features
     return _check("pesti_gemm_experts_swiglu", load().pesti_gemm_experts_swiglu(
         fid, rows, experts, out_features, in_features, _sized(dev, offsets, 4 * (experts + 1), "offsets", torch.int32),
-        _sized(dev, w_gate, w_bytes, "w_gate"), _sized(dev, w_up, w_bytes, "w_up"),
+        _sized(dev, w_gate, w_bytes, "w_gate", values), _sized(dev, w_up, w_bytes, "w_up", values),
         _sized(dev, gate_scales, s_bytes, "gate_scales", torch.float32), _sized(dev, up_scales, s_bytes, "up_scales", torch.float32),
-        x_tokens, _sized(dev, x, x_tokens * in_features * size, "x"), _sized(dev, x_scales, 4 * x_tokens, "x_scales", torch.float32),
-        _sized(dev, x_rows, 4 * rows, "x_rows", torch.int32), hid, _sized(dev, h, rows * out_features * hsize, "h"),
-        st))
+        x_tokens, _sized(dev, x, x_tokens * in_features * size, "x", values), _sized(dev, x_scales, 4 * x_tokens, "x_scales", torch.float32),
+        _sized(dev, x_rows, 4 * rows, "x_rows", torch.int32), hid,
+        _sized(dev, h, rows * out_features * hsize, "h", _type_of(torch, hid)), st))
 
 
 def gemv_ops(ops):
