@@ -210,14 +210,6 @@ struct TileMap {
   }
 };
 
-// Row of X for row r of Y; *ok says whether there is one (an index outside
-// X stands for a row of zeros: row 0 is loaded in its place and dropped).
-__device__ __forceinline__ int64_t x_row(const TileArgs& a, int64_t r, bool* ok) {
-  int64_t i = a.x_rows ? a.x_rows[r] : r;
-  *ok = i >= 0 && i < a.x_tokens;
-  return *ok ? i : 0;
-}
-
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
 // Stores N consecutive columns n..n+N-1 of row r, rounding once to binary16
