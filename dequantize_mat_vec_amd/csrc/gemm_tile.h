@@ -13,10 +13,10 @@
 // consecutive output columns of one row of X and stores them at once.
 #pragma once
 
-#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
+#include "tile_choice.h"
 
 namespace pesti {
 
@@ -335,8 +335,6 @@ __device__ __forceinline__ int again(int v) {
 }
 #endif
 
-template <int BM, int BN>
-constexpr int tile_lds() { return (BM + BN) * 128 * 2 + 2 * 4 * (BM + 2 * BN) + 4 * BM; }
 // Steps of a tile at least: what is loaded for the next tile's turn (rows of
 // X at a tile's start, scales two steps before its end) has then been waited
 // for by the steps' own waits when it is read.
@@ -797,21 +795,15 @@ namespace pesti_host {
 int gemm_tiles_i8(const pesti::TileArgs& a, bool gated, hipStream_t st);
 int gemm_tiles_f16(const pesti::TileArgs& a, bool gated, hipStream_t st);
 
-constexpr int64_t kCus = 256, kCuLds = 160 * 1024;   // compute units, bytes of LDS on each
-
-// Most row tiles of height bm there can be: each expert with rows ends in at
-// most one partial tile.
-inline int64_t most_row_tiles(const pesti::TileArgs& a, int bm) {
-  if (!a.offsets) return (a.rows + bm - 1) / bm;
-  const int64_t used = a.experts < a.rows ? a.experts : a.rows;
-  return a.rows / bm + used;
+inline TileShape shape_of(const pesti::TileArgs& a, bool gated) {
+  return TileShape{a.rows, a.n, a.offsets ? a.experts : 0, a.kbytes, gated};
 }
 
 // most: workgroups to launch at most (each then takes several tiles in turn), 0 for one tile each.
 inline int launch_tiles(const void* fn, pesti::TileArgs a, int bm, int cols, int threads, size_t lds, int64_t most,
                         hipStream_t st) {
   const int64_t tn = (a.n + cols - 1) / cols;
-  const int64_t total = most_row_tiles(a, bm) * tn;
+  const int64_t total = most_row_tiles(shape_of(a, false), bm) * tn;
   // Tiles are numbered in 31 bits; the grid is rounded up to whole turns of the XCDs.
   if (total > INT32_MAX - pesti::kXcds) return PESTI_ERR_SHAPE;
   a.tiles_n = static_cast<int32_t>(tn);
@@ -824,9 +816,9 @@ inline int launch_tiles(const void* fn, pesti::TileArgs a, int bm, int cols, int
 
 template <typename E, int BM, int BN, int WM, int WN, bool GATED>
 int launch_tile(const pesti::TileArgs& a, hipStream_t st) {
-  const int64_t lds = pesti::tile_lds<BM, BN>() + (a.offsets ? 16 * a.experts : 0);
+  const TileShape s = shape_of(a, GATED);
   return launch_tiles(reinterpret_cast<const void*>(&pesti::gemm_tile_kernel<E, BM, BN, WM, WN, GATED>), a, BM,
-                      GATED ? BN / 2 : BN, WM * WN * 64, lds, kCus * (kCuLds / lds), st);
+                      GATED ? BN / 2 : BN, WM * WN * 64, tile_lds(s, BM, BN), tile_workgroups(s, BM, BN), st);
 }
 
 template <typename E, int MT, int NW, int D, bool GATED>
@@ -836,72 +828,24 @@ int launch_rows_w(const pesti::TileArgs& a, hipStream_t st) {
 }
 template <typename E, int MT, bool GATED>
 int launch_rows(const pesti::TileArgs& a, hipStream_t st) {
-  return a.kbytes <= 2048 ? launch_rows_w<E, MT, 2, 4, GATED>(a, st) : launch_rows_w<E, MT, 4, 5, GATED>(a, st);
+  return rows_wavefronts(a.kbytes) == 2 ? launch_rows_w<E, MT, 2, 4, GATED>(a, st)
+                                        : launch_rows_w<E, MT, 4, 5, GATED>(a, st);
 }
 
-// Tiles of bm rows and cols columns that a launch comes to, in tenths: a half
-// tile takes 6 tenths of a whole one's time, and an expert's last tile,
-// anywhere from empty to full, on average 3 more than its rows' share.
-inline int64_t tenths_of_tiles(const pesti::TileArgs& a, int64_t bm, int64_t cols) {
-  int64_t row_tiles;
-  if (a.offsets) {
-    row_tiles = a.rows * 10 / bm + 3 * std::min<int64_t>(a.experts, a.rows);
-  } else {
-    const int64_t left = a.rows % bm;
-    row_tiles = a.rows / bm * 10 + (left > bm / 2 ? 10 : left > 0 ? 6 : 0);
-  }
-  return row_tiles * ((a.n + cols - 1) / cols);
-}
-
-// The kernel for a shape.
-//
-// Fewer 64 x 128 tiles than compute units leave them idle: the rows kernel
-// takes over as long as its workgroups fit the chip about once, with the
-// fewest rows each that do it (us for 16, 32 and 64 rows and the 64 x 128
-// tile: 8-bit 64x896x4864 7.8 / 10 / 14 / 16, 128x896x4864 12 / 10 / 15 / 17,
-// 256x896x4864 21 / 18 / 15 / 18, 40x4864x896 6.8 / 7.6 / 7.1 / 7.4, 100x4864x896
-// 11 / 10 / 10 / 7.8; 8 experts of one row, gated 1024x2048, 9.9 against 13).
-// With more tiles, tiles win for one row as for many (8-bit 1x151936x896 29
-// against 30 us, 16x151936x896 32 against 39), but for experts of up to four
-// rows with long rows of W or with few tiles: two tokens of four experts,
-// binary16 896x2432, 11 against 19 us, eight 23 against 27; 24 tokens of
-// eight of 64 experts, gated 8-bit 1024x2048, 44 against 48; but 60 experts of
-// two rows, 2944x896, 29 against 25, of 1024 and more tiles.
-//
-// Among the tiles, time goes by how many each compute unit gets (a 128 x 128
-// tile takes 1.6 times a 64 x 128 one, 128 x 256 3 times, 256 x 256 5.3
-// times: a product costs (BM + BN) / (BM BN) bytes into LDS), so the
-// least of tiles per unit times that is taken.  Measured (us at 64x128 /
-// 128x128 / 128x256 / 256x256): 8-bit 8192x4096x4096 175 / 153 / 135 / 114,
-// 4096x4096x4096 91 / 70 / 67 / 60, 2048x4864x896 19 / 19 / 22 / 20,
-// 4096x896x4864 28 / 24 / 32 / 49, 513x2304x768 7.6 / 8.9 / 11 / 16; 64
-// experts, 512 rows each, 2048x1024 147 / 129 / 118 / 114; 60 experts, 173
-// rows, 1408x2048 78 / 66 / 68 / 69; binary16, 8 experts, 255 rows,
-// 2429x1056 28 / 28 / 26 / 36, gated, 32 experts, 256 rows, 1408x2048 196 /
-// 159 / 158 / 172.
 template <typename E, bool GATED>
 int launch_any(const pesti::TileArgs& a, hipStream_t st) {
-  constexpr int kG = GATED ? 2 : 1;
-  const int64_t tiles = most_row_tiles(a, 64) * ((a.n + 128 / kG - 1) / (128 / kG));
-  if (a.offsets && a.rows <= 4 * a.experts && (tiles < 2 * kCus || a.kbytes >= 2048))
-    return launch_rows<E, 1, GATED>(a, st);
-  if (tiles < kCus) {
-    const int64_t cols = (a.n + 15) / 16, limit = kCus * 3 / 2;
-    const int64_t r1 = most_row_tiles(a, 16), r2 = most_row_tiles(a, 32), r4 = most_row_tiles(a, 64);
-    if (r1 * cols <= limit || r1 == r4) return launch_rows<E, 1, GATED>(a, st);
-    if (r2 * cols <= limit || (GATED && r2 == r4)) return launch_rows<E, 2, GATED>(a, st);
-    if constexpr (!GATED)
-      if (r4 * cols <= kCus) return launch_rows<E, 4, GATED>(a, st);
+  switch (tile_kernel(shape_of(a, GATED))) {
+    case TileKernel::kRows16: return launch_rows<E, 1, GATED>(a, st);
+    case TileKernel::kRows32: return launch_rows<E, 2, GATED>(a, st);
+    case TileKernel::kRows64:
+      if constexpr (!GATED) return launch_rows<E, 4, GATED>(a, st);
+      break;   // not chosen for gated products
+    case TileKernel::kTile64x128: return launch_tile<E, 64, 128, 2, 2, GATED>(a, st);
+    case TileKernel::kTile128x128: return launch_tile<E, 128, 128, 2, 2, GATED>(a, st);
+    case TileKernel::kTile128x256: return launch_tile<E, 128, 256, 2, 4, GATED>(a, st);
+    case TileKernel::kTile256x256: return launch_tile<E, 256, 256, 2, 4, GATED>(a, st);
   }
-  auto cost = [&](int64_t bm, int64_t bn, int64_t unit) {
-    return (tenths_of_tiles(a, bm, bn / kG) + 10 * kCus - 1) / (10 * kCus) * unit;
-  };
-  const int64_t c0 = cost(64, 128, 10), c1 = cost(128, 128, 16), c2 = cost(128, 256, 30), c3 = cost(256, 256, 53);
-  const int64_t low = std::min(std::min(c0, c1), std::min(c2, c3));
-  if (c3 == low) return launch_tile<E, 256, 256, 2, 4, GATED>(a, st);
-  if (c2 == low) return launch_tile<E, 128, 256, 2, 4, GATED>(a, st);
-  if (c1 == low) return launch_tile<E, 128, 128, 2, 2, GATED>(a, st);
-  return launch_tile<E, 64, 128, 2, 2, GATED>(a, st);
+  return PESTI_ERR_SHAPE;
 }
 
 }  // namespace pesti_host
