@@ -284,12 +284,14 @@ __device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const
 // buffers.  Loads go from memory straight into LDS, 1 KB (8 rows of 128
 // bytes, whole cache lines) per wavefront instruction.
 //
-// What bounds it where there are enough rows is power: 8192x4096x4096 in 8
-// bits takes 85 us with operands of zeros and 114-118 with random ones (126
-// on a slower card, where products and barriers alone, with nothing loaded,
-// read or stored, took 103), and the matrix cores by themselves reach 4400-4800 and
-// 3570-3990 TOP/s (binary16 2260-2410 and 1730-1840).  Short rows are bound
-// by stores as well, experts of few rows by reading W.  A step of a 256 x 256
+// What bounds it where there are enough rows is power first: 8192x4096x4096
+// in 8 bits takes 85 us with operands of zeros and 110-118 with random ones,
+// and the matrix cores by themselves reach 4400-4800 and 3570-3990 TOP/s
+// (binary16 2260-2410 and 1730-1840), 69-77 us with random operands.  On a
+// slower card, 126 us, the kernel took 103 with nothing loaded, read or
+// stored: between that and the products by themselves lie the barriers, the
+// epilogue's arithmetic and that card's clock, not told apart.  Short rows are
+// bound by stores as well, experts of few rows by reading W.  A step of a 256 x 256
 // tile is 2048 cycles of products per SIMD and 64 KB of loads, one step's
 // worth in flight (three and four steps of 64-byte rows took as long): loads
 // run all the time, and a buffer is refilled in two parts, each as soon as
@@ -319,10 +321,10 @@ __device__ __forceinline__ void scaled(const typename E::Acc& c, float xs, const
 // of the next tile's first two steps running under the last steps and the
 // epilogue of the one before: with a workgroup per tile, finding it, filling
 // the buffers and storing took 59 of 127 us for 64 experts of 512 rows,
-// 2048 x 1024 (now 114; the K loop alone about 70).
+// 2048 x 1024 (this kernel: 108-110).
 //
-// 8192x4096x4096 in 8 bits, binary16 Y: 114 us (2.4 POP/s) in 256 x 256
-// tiles; the same kernel without its loads and reads takes 78 us.
+// 8192x4096x4096 in 8 bits, binary16 Y: 110 us (2.5 POP/s) in 256 x 256
+// tiles.
 // ---------------------------------------------------------------------------
 #ifdef __HIP_DEVICE_COMPILE__   // the host compiler needs only the kernels' names
 // A value that what is computed from it is computed from again: the compiler
@@ -659,12 +661,12 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(TileArgs a) {
 // wavefronts split K into contiguous slices, each streaming its part of W and
 // X from memory straight into operand registers, D lines of 128 bytes (two
 // k-steps) per row in flight; the partial sums meet in LDS in wavefront order.
-// What bounds it is latency: finding the expert, the picked rows, one trip
-// for W, the sum.  So NW and D are the fewest that have a whole row of common
-// lengths in flight at once; loads past the row's end cost their issue.
+// What bounds it is latency: finding the expert, the picked rows, the trips
+// for W, the sum.  NW * D lines of a row are in flight at once: 1 KB with 2 x 4
+// and 2.5 KB with 4 x 5, so 896 bytes come in one trip, 2048 and 4864 in two.
 // Four experts of one row, binary16 896x2432 (17.4 MB of W): 6.6 us, 2.6 TB/s;
 // eight, gated 8-bit 1024x2048 (33.6 MB): 9.2 us, 3.7 TB/s; one token, 8-bit
-// 896x896: 4.0.
+// 896x896: 3.9-4.7 by itself, 3.2 after another launch of its kind.
 // ---------------------------------------------------------------------------
 template <typename E, int MT, int NW, int D, bool GATED>
 __global__ __launch_bounds__(NW * 64) void gemm_rows_kernel(TileArgs a) {

@@ -21,7 +21,14 @@ struct TileShape {
 // kRows*: the rows kernel with that many rows of Y a workgroup.
 enum class TileKernel { kRows16, kRows32, kRows64, kTile64x128, kTile128x128, kTile128x256, kTile256x256 };
 
-// Wavefronts of the rows kernel.
+// Wavefronts of the rows kernel, of 4 lines in flight each where there are 2
+// and of 5 where there are 4.  Few lines are issued in vain past the end of
+// short rows, more are in flight for long ones (us for 2 x 4 and 4 x 5): one
+// row of 8-bit 896x896 3.2 / 3.6, 16x4864x896 4.5 / 5.2, eight experts of one row,
+// 1024x2048, 6.6 / 6.8, gated 9.5 / 9.8; against these 8x896x2080 4.0 / 3.9, rows
+// of 4864 bytes 6.3 / 6.3, four binary16 experts of one row, 896x2432,
+// 7.4 / 6.9.  Not on the better side: eight gated binary16 ones, 1024x2048 (rows
+// of 4096 bytes), 13.4 / 14.9.
 constexpr int rows_wavefronts(int64_t kbytes) { return kbytes <= 2048 ? 2 : 4; }
 
 // Dynamic LDS of the tile kernel: two steps of X and W, two sets of scales and
@@ -60,27 +67,28 @@ inline int64_t tenths_of_tiles(const TileShape& s, int64_t bm, int64_t cols) {
 // Fewer 64 x 128 tiles than compute units leave them idle: the rows kernel
 // takes over as long as its workgroups fit the chip about once, with the
 // fewest rows each that do it (us for 16, 32 and 64 rows and the 64 x 128
-// tile: 8-bit 64x896x4864 7.8 / 10 / 14 / 16, 128x896x4864 12 / 10 / 15 / 17,
-// 256x896x4864 21 / 18 / 15 / 18, 40x4864x896 6.8 / 7.6 / 7.1 / 7.4, 100x4864x896
-// 11 / 10 / 10 / 7.8; 8 experts of one row, gated 1024x2048, 9.9 against 13).
-// With more tiles, tiles win for one row as for many (8-bit 1x151936x896 29
-// against 30 us, 16x151936x896 32 against 39), but for experts of up to four
+// tile: 8-bit 64x896x4864 7.2 / 9.4 / 13 / 16, 128x896x4864 12 / 9.7 / 14 / 17,
+// 256x896x4864 21 / 16 / 14 / 17, 100x4864x896 10 / 9.3 / 9.4 / 7.3; 8 experts of one
+// row, gated 1024x2048, 9.4 against 12; but 40x4864x896 6.1 / 6.9 / 6.3 / 6.9, whose
+// workgroups of 16 rows fit the chip three and a half times).
+// With more tiles, tiles win for one row as for many (8-bit 1x151936x896 27
+// against 28 us, 16x151936x896 31 against 38), but for experts of up to four
 // rows with long rows of W or with few tiles: two tokens of four experts,
-// binary16 896x2432, 11 against 19 us, eight 23 against 27; 24 tokens of
-// eight of 64 experts, gated 8-bit 1024x2048, 44 against 48; but 60 experts of
-// two rows, 2944x896, 29 against 25, of 1024 and more tiles.
+// binary16 896x2432, 9.9 against 18 us, eight 21 against 25; 24 tokens of
+// eight of 64 experts, gated 8-bit 1024x2048, 43 against 46; but 60 experts of
+// two rows, 2944x896, 26 against 24, of 1024 and more tiles.
 //
-// Among the tiles, time goes by how many each compute unit gets (a 128 x 128
-// tile takes 1.6 times a 64 x 128 one, 128 x 256 3 times, 256 x 256 5.3
-// times: a product costs (BM + BN) / (BM BN) bytes into LDS), so the
-// least of tiles per unit times that is taken.  Measured (us at 64x128 /
-// 128x128 / 128x256 / 256x256): 8-bit 8192x4096x4096 175 / 153 / 135 / 114,
-// 4096x4096x4096 91 / 70 / 67 / 60, 2048x4864x896 19 / 19 / 22 / 20,
-// 4096x896x4864 28 / 24 / 32 / 49, 513x2304x768 7.6 / 8.9 / 11 / 16; 64
-// experts, 512 rows each, 2048x1024 147 / 129 / 118 / 114; 60 experts, 173
-// rows, 1408x2048 78 / 66 / 68 / 69; binary16, 8 experts, 255 rows,
-// 2429x1056 28 / 28 / 26 / 36, gated, 32 experts, 256 rows, 1408x2048 196 /
-// 159 / 158 / 172.
+// Among the tiles, time goes by how many each compute unit gets.  The price
+// of a tile, in tenths of a 64 x 128 one: 128 x 128 16, 128 x 256 30,
+// 256 x 256 53 (a product costs (BM + BN) / (BM BN) bytes into LDS).  The least
+// of tiles per unit times price is taken.  Measured (us at 64x128 / 128x128 /
+// 128x256 / 256x256; the rule's choice in brackets): 8-bit 8192x4096x4096
+// 167 / 144 / 130 / [110], 4096x4096x4096 80 / 65 / 64 / [57], 2048x4864x896
+// 19 / [20] / 22 / 20, 4096x896x4864 28 / [26] / 34 / 52, 513x2304x768 [6.9] / 8.5 /
+// 14 / 18; 64 experts, 512 rows each, 2048x1024 147 / 120 / 113 / [110]; 60
+// experts, 173 rows, 1408x2048 77 / [63] / 67 / 60; binary16, 8 experts, 255
+// rows, 2429x1056 28 / 28 / [25] / 34, gated, 32 experts, 256 rows, 1408x2048
+// 194 / 155 / 151 / [149].
 inline TileKernel tile_kernel(const TileShape& s) {
   const int64_t g = s.gated ? 2 : 1;
   const int64_t tiles = most_row_tiles(s, 64) * ((s.n + 128 / g - 1) / (128 / g));
