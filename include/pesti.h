@@ -79,10 +79,14 @@ extern "C" {
 
 #define PESTI_OK 0
 #define PESTI_ERR_NULL (-1)   /* a required pointer is NULL                 */
-#define PESTI_ERR_SHAPE (-2)  /* negative size, in_features % 32 != 0, or  */
-                              /* in_features above PESTI_MAX_IN_FEATURES    */
+#define PESTI_ERR_SHAPE (-2)  /* negative size, in_features % 32 != 0,     */
+                              /* in_features above PESTI_MAX_IN_FEATURES,   */
+                              /* another limit that a call states, or an    */
+                              /* unknown format                             */
 #define PESTI_ERR_BATCH (-3)  /* batch outside [0, 8]; GEMM m outside [0,  */
-                              /* PESTI_MAX_GEMM_M]                           */
+                              /* PESTI_MAX_GEMM_M]; rows of X or Y of the   */
+                              /* 8-bit and expert GEMMs outside [0,         */
+                              /* PESTI_MAX_TOKENS]                          */
 #define PESTI_ERR_ALIGN (-4)  /* a pointer breaks the alignment rule above  */
 #define PESTI_ERR_LAUNCH (-5) /* the HIP launch reported an error           */
 #define PESTI_ERR_DEVICE (-6) /* current device is not gfx950, or no device */
@@ -346,6 +350,15 @@ int pesti_gemm_smallm_noalloc(int32_t format, int64_t m, int64_t out_features, i
  * sum_i x_codes[t][i] * codes[o][i] + bias[o], the sum taken exactly in
  * 32-bit integers on the matrix cores.  X is quantized once and serves every
  * layer that reads it (Q, K and V; gate and up).
+ *
+ * For 1..8 rows of float32 X pesti_gemv_i8row does the same layer in one
+ * launch and does not round X.  It is also the faster one for one or two
+ * rows, and for four of short layers (us a layer, mat-vec against the two
+ * calls here: 896x896 at 1 / 4 / 8 rows 2.9 / 3.9 / 5.1 against 4.9 / 5.4 / 5.5,
+ * 4864x896 4.0 / 5.1 / 6.8 against 6.1 / 6.6 / 6.9, 4096x4096 7.1 / 14 / 31 against
+ * 9.6 / 10 / 10, 151936x896 25 / 35 / 50 against 29 / 30 / 31).  These calls are
+ * for more rows, for large layers from four rows on, and for X that is in
+ * 8 bits already or that several layers share (the quantizer is 2.3-2.9 of it).
  *
  * pesti_quant_i8token: x [m][in] in x_format (PESTI_FMT_F32 or
  * PESTI_FMT_F16) to codes int8 [m][in] and scales float32 [m], the rule of
