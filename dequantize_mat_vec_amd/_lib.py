@@ -309,6 +309,8 @@ def _sized(dev, obj, nbytes, what, dtype=None):
         raise ValueError(f"{what}: tensor arguments must be contiguous")
     if obj.nbytes < nbytes:
         raise ValueError(f"{what} holds {obj.nbytes} bytes, the call needs {nbytes}")
+    if str(dtype) == "torch.float16" and str(obj.dtype) == "torch.uint16":   # binary16 bits, as the C ABI holds them
+        return obj.data_ptr()
     raise ValueError(f"{what} must be a {dtype} tensor, got {obj.dtype}")
 
 

@@ -85,6 +85,18 @@ def test_tensors_of_other_types_are_refused():
                     getattr(dmv, name)(**bad, stream=0)
 
 
+def test_binary16_may_be_held_as_its_bits():
+    """uint16 tensors, the type of binary16 in the C ABI, as the small-M GEMMs are given them."""
+    import torch
+    for name, kw, others in calls(torch):
+        for what in others:
+            if kw[what].dtype == torch.float16:
+                bits = dict(kw, **{what: DeviceTensor(torch.uint16, kw[what].nbytes // 2)})
+                with pytest.raises(_lib.PestiError) as e:
+                    getattr(dmv, name)(**bits, stream=0)
+                assert e.value.status == _lib.PESTI_ERR_SHAPE, (name, what)
+
+
 def test_a_tensor_too_small_is_named_by_its_size():
     import torch
     for name, kw, others in calls(torch):
