@@ -32,6 +32,8 @@ FORMAT_IDS = {"q8_0": 0, "q4_k": 1, "q6_k": 2, "i8row": 3, "q5_k": 4, "q2_k": 5,
 # formats of the values of X and Y where a call takes them, and of the expert GEMMs' matrices
 VALUE_FORMAT_IDS = {"f32": 17, "f16": 16}
 EXPERT_FORMAT_IDS = {"f16": 16, "i8row": 3}
+# formats of the key-value cache's pages
+CACHE_FORMAT_IDS = {"f16": 16, "i8row": 3}
 # formats of the small-M GEMM calls that take a format id
 GEMM_FORMAT_IDS = {"f16": 16, "q8_0": 0, "q2_k": 5, "q3_k": 6, "q4_k": 1, "q5_k": 4, "q6_k": 2}
 
@@ -66,6 +68,20 @@ _SIGNATURES = {
                                     _vp]),
     "pesti_gemm_experts_swiglu": (_c_int, [_i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp,
                                            _i32, _vp, _vp]),
+    "pesti_gemv_i4group": (_c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp]),
+    "pesti_gemv_group_i4group": (_c_int, [_i32, _vp, _i64, _i32, _vp]),
+    "pesti_gemv_i4group_swiglu": (_c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp]),
+    "pesti_dequant_i4group": (_c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "pesti_cache_extend": (_c_int, [_vp, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "pesti_cache_append": (_c_int, [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp]),
+    "pesti_attn_paged_workspace_bytes": (_i64, [_vp, _i64, _i64, _i64]),
+    "pesti_attn_paged": (_c_int, [_vp, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _i64, _i32, _vp, ctypes.c_float, _i64, _vp,
+                                  _i64, _vp]),
+    "pesti_cache_workspace_bytes": (_i64, [_vp, _vp]),
+    "pesti_cache_fork": (_c_int, [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "pesti_cache_free": (_c_int, [_vp, _vp, _i64, _vp, _vp]),
+    "pesti_cache_compact": (_c_int, [_vp, _vp, _vp, _vp, _i64, _vp]),
+    "pesti_cache_copy_pages": (_c_int, [_vp, _i64, _vp, _vp, _vp]),
     "pesti_dequant_q8_0": (_c_int, [_i64, _i64, _vp, _vp, _vp]),
     "pesti_dequant_q4_k": (_c_int, [_i64, _i64, _vp, _vp, _vp]),
     "pesti_dequant_q4_k_stream": (_c_int, [_i64, _i64, _vp, _vp, _vp]),
@@ -92,6 +108,27 @@ class GemvOp(ctypes.Structure):
     _fields_ = [("out_features", ctypes.c_int64), ("in_features", ctypes.c_int64),
                 ("w", ctypes.c_void_p), ("row_scales", ctypes.c_void_p),
                 ("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class GemvI4GroupOp(ctypes.Structure):
+    """pesti_gemv_i4group_op: one mat-vec of a grouped launch on 4-bit weights with group scales."""
+    _fields_ = [("out_features", ctypes.c_int64), ("in_features", ctypes.c_int64),
+                ("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class KvCache(ctypes.Structure):
+    """pesti_kv_cache: the pools of pages (made by kv_cache, which checks the tensors)."""
+    _fields_ = [("format", ctypes.c_int64), ("layers", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class KvTable(ctypes.Structure):
+    """pesti_kv_table: the sequences' pages (made by kv_table)."""
+    _fields_ = [("seqs", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("refs", ctypes.c_void_p)]
 
 
 class PestiError(RuntimeError):
@@ -412,6 +449,223 @@ def pesti_gemm_experts_swiglu(fmt, rows, experts, out_features, in_features, off
         x_tokens, _sized(dev, x, x_tokens * in_features * size, "x", values), _sized(dev, x_scales, 4 * x_tokens, "x_scales", torch.float32),
         _sized(dev, x_rows, 4 * rows, "x_rows", torch.int32), hid,
         _sized(dev, h, rows * out_features * hsize, "h", _type_of(torch, hid)), st))
+
+
+# --- 4-bit weights with group scales --------------------------------------------
+def _groups(in_features, group):
+    return -(-in_features // group) if group > 0 else 0
+
+
+def _i4group(dev, torch, out_features, in_features, group, packed, scales, zeros, what=""):
+    """Pointers of one matrix, its tensors' sizes and types checked."""
+    n = out_features * _groups(in_features, group)
+    return (_sized(dev, packed, out_features * (in_features // 2), what + "packed", torch.uint8),
+            _sized(dev, scales, 2 * n, what + "scales", torch.float16), _sized(dev, zeros, n, what + "zeros", torch.uint8))
+
+
+def pesti_gemv_i4group(out_features, in_features, group, packed, scales, zeros, x, y, bias=None, batch=1, stream=None):
+    """y = W x + bias, W in 4-bit codes with a binary16 scale per `group` weights of a row and a zero point (None: 8)."""
+    torch, dev, st = _place(stream)
+    return _check("pesti_gemv_i4group", load().pesti_gemv_i4group(
+        out_features, in_features, group, *_i4group(dev, torch, out_features, in_features, group, packed, scales, zeros),
+        _sized(dev, x, 4 * batch * in_features, "x", torch.float32), _sized(dev, y, 4 * batch * out_features, "y", torch.float32),
+        _sized(dev, bias, 4 * out_features, "bias", torch.float32), batch, st))
+
+
+def gemv_i4group_ops(ops, group, batch=1):
+    """ctypes array of pesti_gemv_i4group_op from (out, in, packed, scales, zeros, x, y, bias) tuples whose pointer
+    fields are tensors, ints or None."""
+    torch, dev, _ = _place(0)
+    arr = (GemvI4GroupOp * max(len(ops), 1))()
+    for i, (out, inf, packed, scales, zeros, x, y, bias) in enumerate(ops):
+        arr[i] = GemvI4GroupOp(out, inf, *_i4group(dev, torch, out, inf, group, packed, scales, zeros, f"op {i}: "),
+                               _sized(dev, x, 4 * batch * inf, f"op {i}: x", torch.float32),
+                               _sized(dev, y, 4 * batch * out, f"op {i}: y", torch.float32),
+                               _sized(dev, bias, 4 * out, f"op {i}: bias", torch.float32))
+    arr.made_for = (len(ops), group, batch)
+    return arr
+
+
+def pesti_gemv_group_i4group(ops, group, batch=1, stream=None):
+    """Grouped launch.  `ops` is a list of (out, in, packed, scales, zeros, x, y, bias) tuples, or an array built by
+    gemv_i4group_ops() for this group size and this batch or a larger one."""
+    arr = ops if isinstance(ops, ctypes.Array) else gemv_i4group_ops(ops, group, batch)
+    n, made_group, made_batch = getattr(arr, "made_for", (len(arr), group, batch))
+    if made_group != group or made_batch < batch:
+        raise ValueError(f"the ops were built for groups of {made_group} and batch {made_batch}, not {group} and {batch}")
+    return _check("pesti_gemv_group_i4group", load().pesti_gemv_group_i4group(
+        n, ctypes.cast(arr, ctypes.c_void_p), group, batch, _stream(stream)))
+
+
+def pesti_gemv_i4group_swiglu(out_features, in_features, group, gate_packed, gate_scales, gate_zeros, up_packed, up_scales,
+                              up_zeros, x, h, batch=1, stream=None):
+    """h = silu(W_gate x) * (W_up x) in one launch."""
+    torch, dev, st = _place(stream)
+    return _check("pesti_gemv_i4group_swiglu", load().pesti_gemv_i4group_swiglu(
+        out_features, in_features, group,
+        *_i4group(dev, torch, out_features, in_features, group, gate_packed, gate_scales, gate_zeros, "gate_"),
+        *_i4group(dev, torch, out_features, in_features, group, up_packed, up_scales, up_zeros, "up_"),
+        _sized(dev, x, 4 * batch * in_features, "x", torch.float32), _sized(dev, h, 4 * batch * out_features, "h", torch.float32),
+        batch, st))
+
+
+def pesti_dequant_i4group(rows, in_features, group, packed, scales, zeros, w_out, stream=None):
+    torch, dev, st = _place(stream)
+    return _check("pesti_dequant_i4group", load().pesti_dequant_i4group(
+        rows, in_features, group, *_i4group(dev, torch, rows, in_features, group, packed, scales, zeros),
+        _sized(dev, w_out, 4 * rows * in_features, "w_out", torch.float32), st))
+
+
+# --- paged key-value cache --------------------------------------------------------
+def kv_cache(fmt, layers, pages, page_size, kv_heads, head_dim, k, v, k_scales=None, v_scales=None):
+    """The pools of a cache as the calls take them.  The struct keeps the tensors alive; it is built anew when one is
+    replaced."""
+    fid = CACHE_FORMAT_IDS[fmt] if isinstance(fmt, str) else int(fmt)
+    torch, dev, _ = _place(0)
+    values = _type_of(torch, fid)
+    rows = layers * pages * kv_heads * page_size
+    size = rows * head_dim * (2 if fid == CACHE_FORMAT_IDS["f16"] else 1)
+    c = KvCache(fid, layers, pages, page_size, kv_heads, head_dim, _sized(dev, k, size, "k", values),
+                _sized(dev, v, size, "v", values), _sized(dev, k_scales, 4 * rows, "k_scales", torch.float32),
+                _sized(dev, v_scales, 4 * rows, "v_scales", torch.float32))
+    c.device, c.tensors = dev, (k, v, k_scales, v_scales)
+    return c
+
+
+def kv_table(table, lengths, refs=None, seqs=None, width=None):
+    """The sequences' pages: table int32 [seqs][width], lengths int32 [seqs], refs int32 [pages] (None where no call
+    takes pages or gives them back).  seqs and width from the table's shape if not given."""
+    torch, dev, _ = _place(0)
+    if seqs is None or width is None:
+        seqs, width = table.shape
+    t = KvTable(seqs, width, _sized(dev, table, 4 * seqs * width, "table", torch.int32),
+                _sized(dev, lengths, 4 * seqs, "lengths", torch.int32), _sized(dev, refs, 0, "refs", torch.int32))
+    t.device, t.tensors = dev, (table, lengths, refs)
+    t.refs_held = refs.numel() if hasattr(refs, "numel") else None
+    return t
+
+
+def _kv(dev, cache, table=None):
+    """Addresses of the structs, with what they were built for checked against each other and the current device."""
+    for s in (cache, table):
+        if getattr(s, "device", dev) != dev:
+            raise ValueError(f"the cache's tensors are on device {s.device}, the current one is {dev}")
+    held = getattr(table, "refs_held", None)
+    if held is not None and held < cache.pages:
+        raise ValueError(f"refs holds {held} pages, the cache has {cache.pages}")
+    return (None if cache is None else ctypes.addressof(cache)), (None if table is None else ctypes.addressof(table))
+
+
+def _rows(dev, obj, rows, width, stride, size, what, dtype):
+    """Pointer and row stride of [rows][width] values: a tensor whose rows may lie apart (a part of a fused
+    projection's output), its shape, type and device checked, or a pointer."""
+    if obj is None or type(obj) is int:
+        return obj, width if stride is None else stride
+    if not hasattr(obj, "data_ptr"):
+        return _ptr(obj), stride
+    if obj.get_device() != dev:
+        raise ValueError(f"{what}: tensor arguments must live in device memory, on the current device {dev}; got {obj.device}")
+    if dtype is not None and obj.dtype != dtype and not (str(dtype) == "torch.float16" and str(obj.dtype) == "torch.uint16"):
+        raise ValueError(f"{what} must be a {dtype} tensor, got {obj.dtype}")
+    shape, strides = obj.shape, obj.stride()
+    inner = 1   # values of one row (all of them where the tensor has one dimension)
+    for n, s in zip(reversed(shape[1:] if len(shape) > 1 else shape), reversed(strides[1:] if len(shape) > 1 else strides)):
+        if n != 1 and s != inner:
+            raise ValueError(f"{what}: the values of a row must be contiguous")
+        inner *= n
+    if stride is None:
+        stride = strides[0] if len(shape) > 1 and shape[0] > 1 else width
+    # values from the first row to the last one's end, within the tensor's memory
+    if rows > 0 and (rows - 1) * stride + width > obj.untyped_storage().nbytes() // size - obj.storage_offset():
+        raise ValueError(f"{what}: {rows} rows of {width} values, {stride} apart, do not fit in its memory")
+    return obj.data_ptr(), stride
+
+
+def pesti_cache_extend(cache, table, n, seq_ids=None, counts=None, status=None, stream=None):
+    """Pages for counts[i] (None: 1) more tokens of sequence seq_ids[i] (None: i)."""
+    torch, dev, st = _place(stream)
+    return _check("pesti_cache_extend", load().pesti_cache_extend(
+        *_kv(dev, cache, table), n, _sized(dev, seq_ids, 4 * n, "seq_ids", torch.int32),
+        _sized(dev, counts, 4 * n, "counts", torch.int32), _sized(dev, status, 4, "status", torch.int32), st))
+
+
+def pesti_cache_append(cache, table, layer, rows, k, v, stride=None, seq_ids=None, positions=None, x_format=None,
+                       stream=None):
+    """K and V of `rows` new tokens into layer `layer`; stride: values from row to row (by default the tensors')."""
+    fid, size = _value_format(x_format, k, "k")
+    torch, dev, st = _place(stream)
+    values, width = _type_of(torch, fid), cache.kv_heads * cache.head_dim
+    kp, ks = _rows(dev, k, rows, width, stride, size, "k", values)
+    vp, vs = _rows(dev, v, rows, width, stride, size, "v", values)
+    if ks != vs:
+        raise ValueError(f"k and v must have one row stride, got {ks} and {vs}")
+    return _check("pesti_cache_append", load().pesti_cache_append(
+        *_kv(dev, cache, table), layer, rows, fid, kp, vp, ks, _sized(dev, seq_ids, 4 * rows, "seq_ids", torch.int32),
+        _sized(dev, positions, 4 * rows, "positions", torch.int32), st))
+
+
+def pesti_attn_paged_workspace_bytes(cache, rows, heads, max_length):
+    """Workspace bytes of pesti_attn_paged (0: none); negative status on bad input."""
+    return int(load().pesti_attn_paged_workspace_bytes(ctypes.addressof(cache), rows, heads, max_length))
+
+
+def pesti_attn_paged(cache, table, layer, rows, heads, q, y, scale, q_stride=None, max_length=None, seq_ids=None,
+                     workspace=None, workspace_bytes=None, q_format=None, y_format=None, stream=None):
+    """Attention of one new token per row over its sequence's cache; max_length: the bound that the workspace was
+    sized for (by default the table's width)."""
+    qid, qsize = _value_format(q_format, q, "q")
+    yid, ysize = _value_format(y_format, y, "y")
+    torch, dev, st = _place(stream)
+    width = heads * cache.head_dim
+    qp, qs = _rows(dev, q, rows, width, q_stride, qsize, "q", _type_of(torch, qid))
+    if max_length is None:
+        max_length = max(1, table.width * cache.page_size)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return _check("pesti_attn_paged", load().pesti_attn_paged(
+        *_kv(dev, cache, table), layer, rows, heads, _sized(dev, seq_ids, 4 * rows, "seq_ids", torch.int32), qid, qp, qs, yid,
+        _sized(dev, y, rows * width * ysize, "y", _type_of(torch, yid)), scale, max_length,
+        _sized(dev, workspace, workspace_bytes, "workspace"), workspace_bytes, st))
+
+
+def pesti_cache_workspace_bytes(cache, table):
+    """Workspace bytes of pesti_cache_fork and pesti_cache_compact; negative status on bad input."""
+    return int(load().pesti_cache_workspace_bytes(ctypes.addressof(cache), ctypes.addressof(table)))
+
+
+def pesti_cache_fork(cache, table, n, parents, children, status, workspace, workspace_bytes=None, stream=None):
+    """Sequence children[i] becomes a copy of parents[i]: whole pages shared, a last one that is not full copied."""
+    torch, dev, st = _place(stream)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return _check("pesti_cache_fork", load().pesti_cache_fork(
+        *_kv(dev, cache, table), n, _sized(dev, parents, 4 * n, "parents", torch.int32),
+        _sized(dev, children, 4 * n, "children", torch.int32), _sized(dev, status, 4, "status", torch.int32),
+        _sized(dev, workspace, workspace_bytes, "workspace"), workspace_bytes, st))
+
+
+def pesti_cache_free(cache, table, n, seq_ids=None, stream=None):
+    """The listed sequences (None: 0..n-1) become empty, their pages free."""
+    torch, dev, st = _place(stream)
+    return _check("pesti_cache_free", load().pesti_cache_free(
+        *_kv(dev, cache, table), n, _sized(dev, seq_ids, 4 * n, "seq_ids", torch.int32), st))
+
+
+def pesti_cache_compact(cache, table, live, workspace, workspace_bytes=None, stream=None):
+    """Live pages move to the front of the pool; live[0] gets their number."""
+    torch, dev, st = _place(stream)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return _check("pesti_cache_compact", load().pesti_cache_compact(
+        *_kv(dev, cache, table), _sized(dev, live, 4, "live", torch.int32),
+        _sized(dev, workspace, workspace_bytes, "workspace"), workspace_bytes, st))
+
+
+def pesti_cache_copy_pages(cache, n, src, dst, stream=None):
+    """Page src[i] to page dst[i], in every layer."""
+    torch, dev, st = _place(stream)
+    return _check("pesti_cache_copy_pages", load().pesti_cache_copy_pages(
+        _kv(dev, cache)[0], n, _sized(dev, src, 4 * n, "src", torch.int32), _sized(dev, dst, 4 * n, "dst", torch.int32), st))
 
 
 def gemv_ops(ops):

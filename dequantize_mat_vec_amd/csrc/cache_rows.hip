@@ -1,0 +1,151 @@
+// New tokens' K and V into their places in the paged key-value cache: a row of
+// head_dim values is rounded to binary16, or to 8 bits with a scale of its own
+// by the rule of quant_i8token.hip (scale = max / 127, codes the exact quotient
+// rounded half away from zero), and written once.
+//
+// A group of lanes serves a row, 8 values per lane: one page number, one or two
+// 16-byte loads and one store each.
+#include "i8_round.h"
+#include "kv_cache.h"
+
+namespace pesti {
+
+struct AppendArgs {
+  KvArgs kv;
+  const void* x[2];        // K and V, [rows][stride]
+  int64_t stride;
+  const int32_t* seq_ids;
+  const int32_t* positions;
+  int64_t items;           // rows * 2 * kv_heads
+};
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8), aligned(16)));
+
+// T: type of x; LANES per row: head_dim / 8 rounded up to a power of two.
+template <typename T, bool I8, int LANES>
+__global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
+  const KvArgs& a = p.kv;
+  const int lane = threadIdx.x % LANES;
+  constexpr int kRows = 256 / LANES;
+  // whole groups of lanes take a row or pass over it together
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / LANES; item < p.items;
+       item += static_cast<int64_t>(gridDim.x) * kRows) {
+    const int32_t head = static_cast<int32_t>(item % a.kv_heads);
+    const int64_t rest = item / a.kv_heads, row = rest >> 1;
+    const int which = static_cast<int>(rest & 1);
+    const int64_t s = p.seq_ids ? p.seq_ids[row] : row;
+    if (s < 0 || s >= a.seqs) continue;
+    const int32_t length = kv_length(a, static_cast<int32_t>(s));
+    const int32_t pos = p.positions ? p.positions[row] : length - 1;
+    if (pos < 0 || pos >= length) continue;
+    const int32_t page = a.table[s * a.width + (pos >> a.page_shift)];
+    if (!kv_page_ok(a, page)) continue;
+    const int64_t at = page * a.page_rows + (static_cast<int64_t>(head) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+    const bool live = lane * 8 < a.head_dim;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    if (live) {
+      const T* src = static_cast<const T*>(p.x[which]) + row * p.stride + static_cast<int64_t>(head) * a.head_dim + lane * 8;
+      if constexpr (sizeof(T) == 4) {
+        const f32x4 lo = reinterpret_cast<const f32x4*>(src)[0], hi = reinterpret_cast<const f32x4*>(src)[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { x[e] = lo[e]; x[e + 4] = hi[e]; }
+      } else {
+        const f16x8 v = *reinterpret_cast<const f16x8*>(src);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = static_cast<float>(v[e]);
+      }
+    }
+    uint8_t* pool = which ? a.v : a.k;
+    if constexpr (!I8) {
+      if (!live) continue;
+      f16x8 v;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = static_cast<_Float16>(x[e]);   // to nearest even
+      reinterpret_cast<f16x8*>(pool)[(at * a.head_dim >> 3) + lane] = v;
+    } else {
+      // magnitudes compare as bit patterns: infinities and NaN lie above
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, x[e]) & 0x7FFFFFFFu;
+        m = m > u ? m : u;
+      }
+#pragma unroll
+      for (int d = 1; d < LANES; d *= 2) {
+        const uint32_t o = __shfl_xor(m, d, LANES);
+        m = m > o ? m : o;
+      }
+      const bool finite = m < 0x7F800000u;
+      float scale = finite ? __builtin_bit_cast(float, m) / 127.f : __builtin_nanf("");
+      if (lane == 0) (which ? a.v_scales : a.k_scales)[at] = scale;
+      // 1 / scale overflows below 2^-128 and scale has few bits among the
+      // subnormals: there both sides of the quotient are scaled by a power of two
+      const bool some = finite && scale > 0.f;
+      const float up = scale < 0x1p-100f ? 0x1p100f : 1.f;
+      scale = some ? scale * up : 1.f;
+      const float inv = some ? 1.f / scale : 0.f;
+      uint32_t w[2] = {0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        w[e / 4] |= static_cast<uint32_t>(code_of(some ? x[e] * up : 0.f, inv, scale) & 0xFF) << (8 * (e % 4));
+      if (live) reinterpret_cast<uint2*>(pool)[(at * a.head_dim >> 3) + lane] = make_uint2(w[0], w[1]);
+    }
+  }
+}
+
+}  // namespace pesti
+
+namespace {
+
+template <typename T, bool I8, int LANES>
+int launch(const pesti::AppendArgs& p, hipStream_t st) {
+  pesti::AppendArgs args = p;
+  void* params[] = {&args};
+  return pesti_kv::launch(reinterpret_cast<const void*>(&pesti::append_kernel<T, I8, LANES>),
+                          dim3(pesti_host::grid_for((p.items * LANES + 255) / 256, 1 << 20)), dim3(256), params, 0, st);
+}
+
+template <typename T, bool I8>
+int launch_lanes(const pesti::AppendArgs& p, hipStream_t st) {
+  if (p.kv.head_dim <= 32) return launch<T, I8, 4>(p, st);
+  if (p.kv.head_dim <= 64) return launch<T, I8, 8>(p, st);
+  if (p.kv.head_dim <= 128) return launch<T, I8, 16>(p, st);
+  return launch<T, I8, 32>(p, st);
+}
+
+}  // namespace
+
+extern "C" int pesti_cache_append(const pesti_kv_cache* cache, const pesti_kv_table* table, int64_t layer, int64_t rows,
+                                  int32_t x_format, const void* k, const void* v, int64_t stride,
+                                  const int32_t* seq_ids, const int32_t* positions, void* stream) {
+  int st = pesti_kv::check_sizes(cache);
+  if (st == PESTI_OK) st = pesti_kv::check_table_sizes(cache, table);
+  if (st != PESTI_OK) return st;
+  if (layer < 0 || layer >= cache->layers) return PESTI_ERR_SHAPE;
+  if (x_format != PESTI_FMT_F16 && x_format != PESTI_FMT_F32) return PESTI_ERR_SHAPE;
+  if (rows < 0 || rows > PESTI_MAX_TOKENS) return PESTI_ERR_BATCH;
+  if (stride < cache->kv_heads * cache->head_dim || stride > (int64_t{1} << 40)) return PESTI_ERR_SHAPE;
+  if (rows == 0) return PESTI_OK;
+  if (!k || !v) return PESTI_ERR_NULL;
+  if ((st = pesti_kv::check_table(cache, table, false)) != PESTI_OK) return st;
+  if ((st = pesti_kv::check_pages(cache)) != PESTI_OK) return st;
+  const int64_t size = x_format == PESTI_FMT_F32 ? 4 : 2;
+  if (!pesti_host::aligned(k, 16) || !pesti_host::aligned(v, 16) || (stride * size) % 16 != 0 ||
+      !pesti_host::aligned(seq_ids, 4) || !pesti_host::aligned(positions, 4))
+    return PESTI_ERR_ALIGN;
+  int dev = 0;
+  size_t lds = 0;
+  if ((st = pesti_host::current_device(&dev, &lds)) != PESTI_OK) return st;
+  pesti::AppendArgs p{pesti_kv::args_of(cache, table), {k, v}, stride, seq_ids, positions, rows * 2 * cache->kv_heads};
+  const int64_t page0 = layer * cache->pages;
+  p.kv.k += page0 * p.kv.page_bytes;
+  p.kv.v += page0 * p.kv.page_bytes;
+  const hipStream_t sh = static_cast<hipStream_t>(stream);
+  const bool f32 = x_format == PESTI_FMT_F32;
+  if (cache->format == PESTI_FMT_F16) return f32 ? launch_lanes<float, false>(p, sh) : launch_lanes<_Float16, false>(p, sh);
+  p.kv.k_scales += page0 * p.kv.page_rows;
+  p.kv.v_scales += page0 * p.kv.page_rows;
+  return f32 ? launch_lanes<float, true>(p, sh) : launch_lanes<_Float16, true>(p, sh);
+}

@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "i8_round.h"
 
 namespace pesti {
 
@@ -85,16 +86,6 @@ struct Vec<float> {
 };
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
-__device__ __forceinline__ int code_of(float x, float inv, float s) {
-  float q = __builtin_rintf(x * inv);
-  const float r = __builtin_fmaf(-q, s, x);
-  const float d = 2.f * __builtin_fabsf(r);
-  // A tie (d == s) moves away from zero only from the side nearer to it.
-  if (d > s || (d == s && (r > 0.f) == (x > 0.f))) q += r > 0.f ? 1.f : -1.f;
-  q = q > 127.f ? 127.f : (q < -127.f ? -127.f : q);
-  return static_cast<int>(q);
-}
 
 // Largest value of a wavefront, in a scalar register.
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {

@@ -86,11 +86,12 @@ extern "C" {
 #define PESTI_ERR_BATCH (-3)  /* batch outside [0, 8]; GEMM m outside [0,  */
                               /* PESTI_MAX_GEMM_M]; rows of X or Y of the   */
                               /* 8-bit and expert GEMMs outside [0,         */
-                              /* PESTI_MAX_TOKENS]                          */
+                              /* PESTI_MAX_TOKENS]; rows or lists of the    */
+                              /* key-value cache outside their limits       */
 #define PESTI_ERR_ALIGN (-4)  /* a pointer breaks the alignment rule above  */
 #define PESTI_ERR_LAUNCH (-5) /* the HIP launch reported an error           */
 #define PESTI_ERR_DEVICE (-6) /* current device is not gfx950, or no device */
-#define PESTI_ERR_WORKSPACE (-7) /* GEMM workspace missing or too small     */
+#define PESTI_ERR_WORKSPACE (-7) /* workspace missing or too small          */
 
 #define PESTI_FMT_Q8_0 0
 #define PESTI_FMT_Q4_K 1
@@ -430,6 +431,213 @@ int pesti_gemm_experts_swiglu(int32_t format, int64_t rows, int64_t experts,
                               const float* up_scales, int64_t x_tokens, const void* x,
                               const float* x_scales, const int32_t* x_rows, int32_t h_format,
                               void* h, void* stream);
+
+/* --- 4-bit weights with a scale and a zero point per group ----------------
+ * The mat-vec of the formats above for 4-bit matrices whose scales lie in an
+ * array of their own, one per group of consecutive weights of a row:
+ *
+ *   w[o][i] = scales[o][i / group] * (q[o][i] - zeros[o][i / group])
+ *
+ *   packed  4-bit codes 0..15, two per byte (weight 2k in the low nibble of
+ *           byte k, 2k + 1 in the high one); rows of in_features / 2 bytes
+ *   scales  binary16 [out][groups], groups = ceil(in_features / group)
+ *   zeros   uint8 [out][groups] (any value), or NULL: 8 for every group
+ *   group   weights per scale: a power of two, 32..PESTI_MAX_IN_FEATURES (the
+ *           last group of a row may be short), else PESTI_ERR_SHAPE
+ *
+ * x, y, bias, batch, stream and errors as for pesti_gemv_q8_0; packed 16-byte
+ * aligned, scales 2.  The codes less their zero points are exact binary16
+ * integers and are multiplied on the matrix cores with x in two binary16
+ * parts: x is scaled by a power of two that brings the largest finite |x| of a
+ * column (of each 128-weight multiple of it that is staged at once) to
+ * [2^14, 2^15), and what the first part leaves is held 2^11 times as large in
+ * the second, which adds at most 2^-22 |x_i| + 2^-50 max|x| per element to the
+ * float32 error.  Group sums are float32 and take their scale once.
+ *
+ * pesti_gemv_group_i4group: up to PESTI_MAX_GROUP such mat-vecs of one group
+ * size and batch in one launch, as pesti_gemv_group; every op's y has the bits
+ * of its single call.
+ * pesti_gemv_i4group_swiglu: h = silu(W_gate x) * (W_up x) of two matrices of
+ * one shape and group size in one launch, rows of any length (no bias).
+ * pesti_dequant_i4group: the weights in float32, bit-exact (each product of a
+ * binary16 scale and q - z has a float32 value). */
+typedef struct pesti_gemv_i4group_op {
+  int64_t out_features;
+  int64_t in_features;
+  const void* packed;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+  const float* x;
+  float* y;
+  const float* bias;
+} pesti_gemv_i4group_op;
+
+int pesti_gemv_i4group(int64_t out_features, int64_t in_features, int64_t group, const void* packed,
+                       const uint16_t* scales, const uint8_t* zeros, const float* x, float* y,
+                       const float* bias, int32_t batch, void* stream);
+int pesti_gemv_group_i4group(int32_t n_ops, const pesti_gemv_i4group_op* ops, int64_t group,
+                             int32_t batch, void* stream);
+int pesti_gemv_i4group_swiglu(int64_t out_features, int64_t in_features, int64_t group,
+                              const void* gate_packed, const uint16_t* gate_scales,
+                              const uint8_t* gate_zeros, const void* up_packed,
+                              const uint16_t* up_scales, const uint8_t* up_zeros, const float* x,
+                              float* h, int32_t batch, void* stream);
+int pesti_dequant_i4group(int64_t rows, int64_t in_features, int64_t group, const void* packed,
+                          const uint16_t* scales, const uint8_t* zeros, float* w_out, void* stream);
+
+/* --- paged key-value cache --------------------------------------------------
+ * What stands between a decode step's Q/K/V and O projections ("PESTI ..."
+ * README, "Conformance": grouped-query attention, 14 query and 2 KV heads of
+ * 64; "Current Status": paged attention and KV updates during generation).
+ * K and V of all layers lie in pools of pages of page_size tokens; a page
+ * number stands for the same page of every layer, of K and of V.  The caller
+ * owns every array; the library keeps nothing between calls.
+ *
+ *   format     PESTI_FMT_F16, or PESTI_FMT_I8ROW: int8 codes with a float32
+ *              scale per token and head, by the rule of pesti_quant_i8token
+ *   layers     1..PESTI_MAX_LAYERS;  pages 0..PESTI_MAX_PAGES
+ *   page_size  a power of two, 8..1024
+ *   kv_heads   1..PESTI_MAX_HEADS;  head_dim a multiple of 32, 32..256
+ *   k, v       [layers][pages][kv_heads][page_size][head_dim], 16-byte aligned
+ *   k_scales, v_scales  (I8ROW) [layers][pages][kv_heads][page_size], 16-byte
+ *
+ * pesti_kv_table holds which pages the sequences have:
+ *   seqs       sequence slots, 0..PESTI_MAX_SEQS
+ *   width      page numbers per slot; width * page_size <= 2^30
+ *   table      int32 [seqs][width]: token t of a sequence is token t %
+ *              page_size of page table[seq][t / page_size]
+ *   lengths    int32 [seqs]: tokens of each sequence (below 0 counts as 0,
+ *              above width * page_size as that)
+ *   refs       int32 [pages]: how many sequences hold the page; 0: it is free
+ * Only entries of a sequence's ceil(length / page_size) pages are read.  A page
+ * number outside 0..pages-1 names no page: attention leaves its tokens out,
+ * rows for it are not written, and page upkeep passes over it.
+ *
+ * The structs are host data, read during the call; a field outside its limits
+ * is PESTI_ERR_SHAPE, a missing array PESTI_ERR_NULL (table and lengths always,
+ * refs where pages are taken or given back, k, v and the scales where pages are
+ * touched), an unaligned one PESTI_ERR_ALIGN (int32 arrays 4 bytes).  Lists
+ * (seq_ids, positions, parents, ...) are int32 in device memory; a list entry
+ * outside 0..seqs-1 names no sequence and is passed over (attention: a row of
+ * zeros).  rows and n are 0..PESTI_MAX_SEQS (pesti_cache_append: 0..
+ * PESTI_MAX_TOKENS, pesti_cache_copy_pages: 0..PESTI_MAX_PAGES), else
+ * PESTI_ERR_BATCH; 0 returns 0 without touching a pointer.  Calls that change
+ * one table or pool have to be ordered with the others that use it, as on one
+ * stream. */
+#define PESTI_MAX_LAYERS 1024
+#define PESTI_MAX_PAGES (1 << 22)
+#define PESTI_MAX_HEADS 1024
+#define PESTI_MAX_SEQS 4096
+
+typedef struct pesti_kv_cache {
+  int64_t format;
+  int64_t layers;
+  int64_t pages;
+  int64_t page_size;
+  int64_t kv_heads;
+  int64_t head_dim;
+  void* k;
+  void* v;
+  float* k_scales;
+  float* v_scales;
+} pesti_kv_cache;
+
+typedef struct pesti_kv_table {
+  int64_t seqs;
+  int64_t width;
+  int32_t* table;
+  int32_t* lengths;
+  int32_t* refs;
+} pesti_kv_table;
+
+/* Pages for more tokens: lengths[seq] += counts[i] (NULL: 1; below 0 counts as
+ * 0) for every listed sequence seq_ids[i] (NULL: i), and the pages that this
+ * needs are taken, the lowest free ones in list order.  A sequence listed
+ * again is passed over.  *status (int32 in device memory): 0, or the number of
+ * free pages that are missing, or -1 where a sequence would outgrow its row of
+ * the table; nothing has changed then. */
+int pesti_cache_extend(const pesti_kv_cache* cache, const pesti_kv_table* table, int64_t n,
+                       const int32_t* seq_ids, const int32_t* counts, int32_t* status, void* stream);
+
+/* K and V of new tokens into their places in one layer's pages: row r is token
+ * positions[r] (NULL: the last one) of sequence seq_ids[r] (NULL: r), all KV
+ * heads, k and v [rows][stride] in x_format (PESTI_FMT_F32 or PESTI_FMT_F16)
+ * with kv_heads * head_dim values a row (so parts of a fused projection's
+ * output do as they are).  Rows of positions outside the sequence are not
+ * written.  Into binary16 values are rounded to nearest even.  k and v 16-byte
+ * aligned, stride * value size a multiple of 16 (else PESTI_ERR_ALIGN) and
+ * stride >= kv_heads * head_dim (PESTI_ERR_SHAPE).  Two rows for one place: it
+ * holds one of them, which is not specified (in 8 bits perhaps the scale of the
+ * other). */
+int pesti_cache_append(const pesti_kv_cache* cache, const pesti_kv_table* table, int64_t layer,
+                       int64_t rows, int32_t x_format, const void* k, const void* v, int64_t stride,
+                       const int32_t* seq_ids, const int32_t* positions, void* stream);
+
+/* Attention of one new token per row over its sequence's cache:
+ *   y[r][h] = sum_t softmax_t(scale * q[r][h] . k[t][h / g]) v[t][h / g]
+ * over the lengths[seq_ids[r]] tokens of the sequence (NULL: sequence r), g =
+ * heads / kv_heads query heads to a KV head (heads a multiple, up to
+ * PESTI_MAX_HEADS).  The new token's own K and V are in the cache already
+ * (pesti_cache_extend, pesti_cache_append).  q [rows][q_stride] in q_format, y
+ * [rows][heads][head_dim] in y_format (PESTI_FMT_F32 or PESTI_FMT_F16); q and
+ * y 16-byte aligned, q_stride >= heads * head_dim and its bytes a multiple of
+ * 16.  A row without tokens (length 0, or no valid page) is zeros, as is one
+ * whose every score is -infinity; a NaN of q, K or V makes NaN of the heads
+ * that it enters.
+ *
+ * Scores, maximum, sum and result are float32.  q times scale and the softmax's
+ * weights enter the matrix cores in two binary16 parts each (22 bits), K and V
+ * as they are (the int8 codes exactly, scales applied in float32).
+ *
+ * The cache's length is split over workgroups where rows and KV heads do not
+ * fill the GPU, and the parts are joined in a fixed order.  max_length, 1..
+ * 2^30, is the caller's bound of the rows' lengths, which chooses the split; a
+ * longer sequence is attended whole all the same.  workspace: device memory of
+ * pesti_attn_paged_workspace_bytes(cache, rows, heads, max_length) bytes (0:
+ * none needed), 16-byte aligned, for one call at a time; PESTI_ERR_WORKSPACE if
+ * NULL or smaller.  Nothing in it needs to start at zero.  The function is
+ * host-only and gives a negative PESTI_ERR_* for bad arguments. */
+int64_t pesti_attn_paged_workspace_bytes(const pesti_kv_cache* cache, int64_t rows, int64_t heads,
+                                         int64_t max_length);
+int pesti_attn_paged(const pesti_kv_cache* cache, const pesti_kv_table* table, int64_t layer,
+                     int64_t rows, int64_t heads, const int32_t* seq_ids, int32_t q_format,
+                     const void* q, int64_t q_stride, int32_t y_format, void* y, float scale,
+                     int64_t max_length, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* pesti_cache_fork: sequence children[i] becomes a copy of parents[i]: it
+ * shares the parent's whole pages (refs + 1), and a last page that is not full
+ * is copied, in every layer, to the lowest free page, in list order.  A child
+ * has to be empty (length 0) and to be listed once: other pairs, and a child
+ * listed again, are passed over.  Parents are taken as they were before the
+ * call.  *status: 0, or the number of free pages that are missing; nothing has
+ * changed then.  n up to seqs (else PESTI_ERR_BATCH).
+ *
+ * pesti_cache_free: the listed sequences (seq_ids; NULL: 0..n-1; each any
+ * number of times) become empty: refs - 1 for each of their pages, their table entries -1.
+ *
+ * pesti_cache_compact: live pages (refs > 0) move to 0..live-1: the i-th live
+ * page from live on to the i-th free page below it, with its contents in every
+ * layer; refs and the sequences' table entries follow.  *live (int32 in device
+ * memory) is their number.
+ *
+ * pesti_cache_copy_pages: page src[i] to page dst[i], K, V and scales of every
+ * layer.  A dst that is also another pair's src or dst holds a mixture that is
+ * not specified.  Table and refs are not looked at.
+ *
+ * fork and compact need a workspace of pesti_cache_workspace_bytes(cache,
+ * table) bytes, 16-byte aligned, for one call at a time (host-only function,
+ * negative PESTI_ERR_* for bad arguments); PESTI_ERR_WORKSPACE if NULL or
+ * smaller. */
+int64_t pesti_cache_workspace_bytes(const pesti_kv_cache* cache, const pesti_kv_table* table);
+int pesti_cache_fork(const pesti_kv_cache* cache, const pesti_kv_table* table, int64_t n,
+                     const int32_t* parents, const int32_t* children, int32_t* status,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+int pesti_cache_free(const pesti_kv_cache* cache, const pesti_kv_table* table, int64_t n,
+                     const int32_t* seq_ids, void* stream);
+int pesti_cache_compact(const pesti_kv_cache* cache, const pesti_kv_table* table, int32_t* live,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+int pesti_cache_copy_pages(const pesti_kv_cache* cache, int64_t n, const int32_t* src,
+                           const int32_t* dst, void* stream);
 
 /* --- dequantization to float32 (bit-exact; checks the unpacking) --------
  * w_out float32 [rows][in_features]: each weight rounded once from its
