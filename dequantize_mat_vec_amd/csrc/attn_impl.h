@@ -1,0 +1,559 @@
+// Attention of one new token per sequence over the paged key-value cache
+// ("PESTI ..." README, "Conformance" and "Current Status": grouped-query
+// attention, paged attention during generation), for the query heads h of one
+// KV head:
+//   y[h] = sum_t p_t v[t] / sum_t p_t,  p_t = 2^(s_t - max), s_t = scale log2(e) q[h] . k[t]
+// in one pass over the cache with the running maximum and sum of the softmax.
+//
+// What bounds it is the cache's bytes: a step of one wavefront is 32 tokens of
+// one KV head, and the matrix cores' time for it (D / 32 + D / 16 of
+// v_mfma_f32_16x16x32_f16 per head tile and half of the tokens) is a small part
+// of what its loads take.  So precision is free there and the layout is chosen
+// for the loads:
+//   * S = K Q^T: A is 16 tokens (rows) of K as they lie in a page, 16 bytes a
+//     lane; B is Q.  The 16 columns are 8 heads, each twice: columns 0-7 hold
+//     the first binary16 part of q, 8-15 what it leaves, 2^11 times as large.
+//   * Column c of S is one head in all 64 lanes' registers, so the softmax's
+//     maximum, weights and sums stay in the lanes of their column: one exchange
+//     joins the parts, two the maximum of a column.
+//   * y = V^T P: the weights of 32 tokens are B as S left them in the registers
+//     (no exchange: lane group g holds tokens 4g..4g+3 of both halves, so those
+//     are the k indices of its lanes), in two parts over the columns as q was.
+//     A needs 8 tokens of one dimension per lane: each lane loads 8 token rows,
+//     the same run of up to 8 dimensions of each, and the transposition is the
+//     choice of which 16-bit halves form a register (v_perm), with the
+//     dimensions of a run spread over as many matrix instructions.  No LDS.
+// LDS is used once, to join the four wavefronts of a workgroup, which take the
+// tiles of its part of the sequence in turn.  Parts are joined by a second
+// kernel (attn_paged.hip) where a sequence has more than one.
+#pragma once
+
+#include "kv_cache.h"
+
+namespace pesti {
+
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2a __attribute__((ext_vector_type(2), aligned(8)));
+
+struct AttnArgs {
+  KvArgs kv;               // pools of the layer
+  const int32_t* seq_ids;
+  const void* q;
+  int64_t q_stride;
+  void* y;
+  float* parts;            // [rows][heads][splits][head_dim], unnormalised
+  float* stats;            // [rows][heads][splits][2]: maximum (base 2), sum
+  float scale;             // scale * log2(e)
+  int32_t heads;
+  int32_t group;           // query heads per KV head
+  int32_t head_blocks;     // workgroups per KV head
+  int32_t splits;
+  int32_t q_f32, y_f32;
+};
+
+constexpr int kAttnWaves = 4;
+constexpr int kTile = 32;            // tokens of one step of a wavefront
+constexpr int kMinPartTiles = 8;     // a workgroup's part of a sequence is at least two steps of each wavefront
+
+// Tiles per part, and parts, of a sequence of `length` tokens.
+__device__ __forceinline__ int32_t attn_part_tiles(int32_t length, int32_t splits) {
+  const int32_t tiles = (length + kTile - 1) / kTile, per = (tiles + splits - 1) / splits;
+  return per > kMinPartTiles ? per : kMinPartTiles;
+}
+__device__ __forceinline__ int32_t attn_parts(int32_t length, int32_t per) {
+  return ((length + kTile - 1) / kTile + per - 1) / per;
+}
+
+__device__ __forceinline__ int32_t attn_length(const AttnArgs& p, int64_t row, int64_t* seq) {
+  *seq = p.seq_ids ? p.seq_ids[row] : row;
+  if (*seq < 0 || *seq >= p.kv.seqs || p.kv.pages == 0) return 0;
+  return kv_length(p.kv, static_cast<int32_t>(*seq));
+}
+
+#ifdef __HIP_DEVICE_COMPILE__
+
+// Largest value of a column: over the four lane groups.
+__device__ __forceinline__ float column_max(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  v = fmaxf(__builtin_bit_cast(float, static_cast<uint32_t>(h[0])), __builtin_bit_cast(float, static_cast<uint32_t>(h[1])));
+  const uint32_t c = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+  return fmaxf(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
+}
+__device__ __forceinline__ float column_sum(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  v = __builtin_bit_cast(float, static_cast<uint32_t>(h[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(h[1]));
+  const uint32_t c = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+  return __builtin_bit_cast(float, static_cast<uint32_t>(r[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(r[1]));
+}
+__device__ __forceinline__ float other_part(float v) { return dpp<0x128>(v); }   // row_ror:8, column c ^ 8
+
+constexpr float kPart = 0x1p-11f;   // the second part is held 2^11 times as large
+
+// First and second binary16 part of x (|x| < 2^15); an infinity or NaN is all in the first.
+__device__ __forceinline__ _Float16 part_of(float x, bool second) {
+  const _Float16 hi = static_cast<_Float16>(x);
+  const float lo = (x - static_cast<float>(hi)) * 0x1p11f;
+  return second ? static_cast<_Float16>(lo - lo == 0.f ? lo : 0.f) : hi;
+}
+
+// Both parts of a sum of products: an infinity of the first stands, since the
+// second's products with it are infinities or NaN of any kind.
+__device__ __forceinline__ float both_parts(float hi, float lo) {
+  return __builtin_fabsf(hi) == INFINITY ? hi : fmaf(lo, kPart, hi);
+}
+
+// Four signed bytes as binary16: xor 0x80 makes them 0..255 (code + 128), which
+// over 0x6400 read as 1024 + u.
+__device__ __forceinline__ h2 bytes_h2(uint32_t u, uint32_t sel) {
+  const uint32_t v = __builtin_amdgcn_perm(0x64646464u, u, sel);   // bytes 4-7 of the pair are 0x64
+  return __builtin_bit_cast(h2, v) - h2{static_cast<_Float16>(1152.f), static_cast<_Float16>(1152.f)};
+}
+__device__ __forceinline__ h8 codes_h8(uint32_t a, uint32_t b) {
+  a ^= 0x80808080u;
+  b ^= 0x80808080u;
+  const h2 v0 = bytes_h2(a, 0x04010400u), v1 = bytes_h2(a, 0x04030402u), v2 = bytes_h2(b, 0x04010400u),
+           v3 = bytes_h2(b, 0x04030402u);
+  return h8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+}
+
+// One run of dimensions of V: 16 lanes hold E neighbouring ones each, of 8
+// tokens; frag(n) is dimension n of the lanes' runs as a matrix operand.
+template <bool I8, int E>
+struct VRun {
+  static constexpr int kWords = I8 ? (E + 3) / 4 : E / 2;
+  uint32_t w[8][kWords];
+  __device__ __forceinline__ void load(int j, const uint8_t* p) {
+    if constexpr (I8 && E == 2) {
+      w[j][0] = *reinterpret_cast<const uint16_t*>(p);
+    } else if constexpr (kWords == 1) {
+      w[j][0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (kWords == 2) {
+      const u32x2a v = *reinterpret_cast<const u32x2a*>(p);
+      w[j][0] = v.x;
+      w[j][1] = v.y;
+    } else {
+      const u32x4a v = *reinterpret_cast<const u32x4a*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[j][i] = v[i];
+    }
+  }
+  __device__ __forceinline__ void clear(int j) {   // codes of zero too
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[j][i] = 0;
+  }
+  __device__ __forceinline__ h8 frag(int n) const {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    u4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (!I8) {
+        r[j] = __builtin_amdgcn_perm(w[2 * j + 1][n / 2], w[2 * j][n / 2], n % 2 ? 0x07060302u : 0x05040100u);
+      } else {
+        const uint32_t b = n % 4;
+        const uint32_t u = __builtin_amdgcn_perm(w[2 * j + 1][n / 4], w[2 * j][n / 4], 0x0C000C00u | b | ((b + 4) << 16));
+        const h2 v = __builtin_bit_cast(h2, (u ^ 0x00800080u) | 0x64006400u) -
+                     h2{static_cast<_Float16>(1152.f), static_cast<_Float16>(1152.f)};
+        r[j] = __builtin_bit_cast(uint32_t, v);
+      }
+    }
+    return __builtin_bit_cast(h8, r);
+  }
+};
+
+// head_dim as runs of 128, 64 and 32 dimensions (8, 4 and 2 a lane).
+template <bool I8, int D>
+struct VTile {
+  static constexpr int kA = D / 128, kB = D % 128 / 64, kC = D % 64 / 32;
+  VRun<I8, 8> a[kA ? kA : 1];
+  VRun<I8, 4> b[1];
+  VRun<I8, 2> c[1];
+  static constexpr int kSize = I8 ? 1 : 2;
+  __device__ __forceinline__ void load(int j, const uint8_t* row, int col) {
+#pragma unroll
+    for (int r = 0; r < kA; ++r) a[r].load(j, row + (128 * r + 8 * col) * kSize);
+    if constexpr (kB) b[0].load(j, row + (128 * kA + 4 * col) * kSize);
+    if constexpr (kC) c[0].load(j, row + (128 * kA + 64 * kB + 2 * col) * kSize);
+  }
+  __device__ __forceinline__ void clear(int j) {
+#pragma unroll
+    for (int r = 0; r < kA; ++r) a[r].clear(j);
+    if constexpr (kB) b[0].clear(j);
+    if constexpr (kC) c[0].clear(j);
+  }
+  __device__ __forceinline__ h8 frag(int f) const {
+    if (f < 8 * kA) return a[f / 8].frag(f % 8);
+    if (f < 8 * kA + 4 * kB) return b[0].frag(f - 8 * kA);
+    return c[0].frag(f - 8 * kA - 4 * kB);
+  }
+  // The dimension that row `row` of operand f is.
+  __device__ __forceinline__ static int dim(int f, int row) {
+    if (f < 8 * kA) return 128 * (f / 8) + 8 * row + f % 8;
+    if (f < 8 * kA + 4 * kB) return 128 * kA + 4 * row + (f - 8 * kA);
+    return 128 * kA + 64 * kB + 2 * row + (f - 8 * kA - 4 * kB);
+  }
+};
+
+// The first of the 8 dimensions that lane group g holds in step s of the
+// scores.  In 8 bits two steps share a 16-byte load.
+template <bool I8>
+__device__ __forceinline__ constexpr int k_dim(int s, int steps, int g) {
+  return I8 && s < steps / 2 * 2 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
+}
+
+#endif  // __HIP_DEVICE_COMPILE__
+
+// One workgroup: the NT * 8 query heads of block blockIdx.y of a KV head, part
+// blockIdx.x of row blockIdx.z's sequence.  SMALL: pages of 8 or 16 tokens, up
+// to four in a tile; else a tile lies in one page.
+template <bool I8, int D, int NT, bool SMALL>
+__global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int kSteps = D / 32, kFrags = D / 16, kSize = I8 ? 1 : 2, kPages = SMALL ? 4 : 1;
+  __shared__ float joint[kAttnWaves][8 * NT][D];
+  __shared__ float wave_max[kAttnWaves][8 * NT], wave_sum[kAttnWaves][8 * NT];
+  const KvArgs& a = p.kv;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const bool second = col >= 8;
+  const int64_t row = blockIdx.z;
+  const int kvh = blockIdx.y / p.head_blocks, hb = blockIdx.y % p.head_blocks;
+  const int head0 = hb * 8 * NT, heads_here = p.group - head0 < 8 * NT ? p.group - head0 : 8 * NT;
+  const int64_t first_head = static_cast<int64_t>(kvh) * p.group + head0;
+
+  int64_t seq;
+  const int32_t length = attn_length(p, row, &seq);
+  const int32_t per = attn_part_tiles(length, p.splits), parts = attn_parts(length, per);
+  const int32_t part = blockIdx.x;
+  if (part >= parts && part > 0) return;   // (a sequence without tokens: part 0 writes the zeros)
+  const int32_t tiles = (length + kTile - 1) / kTile;
+  const int32_t end = part * per + per < tiles ? part * per + per : tiles;
+
+  // Q: columns 0-7 the first parts, 8-15 the second ones, of heads that exist;
+  // scaled so that a head's largest finite value lies in [2^14, 2^15).
+  h8 qf[NT][kSteps];
+  float factor[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int h = 8 * n + (col & 7);
+    const bool there = h < heads_here;
+    const int64_t at = row * p.q_stride + (first_head + (there ? h : 0)) * D;
+    float v[kSteps][8];
+    uint32_t most = 0;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int64_t e0 = at + k_dim<I8>(s, kSteps, g);
+      if (p.q_f32) {
+        const f32x4* src = reinterpret_cast<const f32x4*>(static_cast<const float*>(p.q) + e0);
+        const f32x4 lo = src[0], hi = src[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { v[s][e] = lo[e]; v[s][e + 4] = hi[e]; }
+      } else {
+        const h8 x = *reinterpret_cast<const h8*>(static_cast<const _Float16*>(p.q) + e0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[s][e] = static_cast<float>(x[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v[s][e]) & 0x7FFFFFFFu;
+        most = u < 0x7F800000u && u > most ? u : most;
+      }
+    }
+    // magnitudes are ordered as floats too
+    const uint32_t big = __builtin_bit_cast(uint32_t, column_max(__builtin_bit_cast(float, most)));
+    int up = 14 + 127 - static_cast<int>(big >> 23);   // the exponent to add
+    up = big == 0 ? 0 : (up > 126 ? 126 : up);
+    const float lift = __builtin_bit_cast(float, static_cast<uint32_t>(up + 127) << 23);
+    factor[n] = p.scale * __builtin_bit_cast(float, static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) qf[n][s][e] = there ? part_of(v[s][e] * lift, second) : static_cast<_Float16>(0.f);
+  }
+
+  f32x4 acc[NT][kFrags];
+  float most[NT], sum[NT], ref[NT];   // ref: y is held as acc * 2^ref (8 bits; else the maximum alone scales it)
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    most[n] = -INFINITY;
+    sum[n] = 0.f;
+    ref[n] = -126.f;
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) acc[n][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const int32_t* row_pages = a.table + seq * a.width;
+  const int32_t held = kv_pages_of(a, length);
+  const int32_t page_mask = (1 << a.page_shift) - 1;
+  int32_t ids[kPages];   // lane i: the pages of the wavefront's i-th tile from here
+  const int32_t first_tile = part * per + wave;
+  for (int32_t tile = first_tile; tile < end; tile += kAttnWaves) {
+    const int step = (tile - first_tile) / kAttnWaves & 63;
+    if (step == 0) {
+#pragma unroll
+      for (int j = 0; j < kPages; ++j) {
+        const int64_t idx = ((static_cast<int64_t>(tile) + lane * kAttnWaves) * kTile + 8 * j) >> a.page_shift;
+        ids[j] = idx < held ? row_pages[idx] : -1;
+      }
+    }
+    // Pages, and which tokens of the tile there are.
+    const int32_t t0 = tile * kTile, left = length - t0;
+    uint32_t there = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1;
+    // Rows of the layer's pools that the tile's token 0 would have in the page
+    // of K's tokens (column col) and of V's (lane group g), by half.
+    int64_t k_row[2], v_row[2];
+    auto row_in = [&](int32_t page, int first) {
+      return page * a.page_rows + (static_cast<int64_t>(kvh) << a.page_shift) + ((t0 + first) & page_mask) - first;
+    };
+    int32_t page[kPages];
+#pragma unroll
+    for (int j = 0; j < kPages; ++j) {
+      page[j] = __builtin_amdgcn_readlane(ids[j], step);
+      if (!kv_page_ok(a, page[j])) {
+        there &= SMALL ? ~(0xFFu << (8 * j)) : 0u;
+        page[j] = 0;   // read instead, and not used
+      }
+    }
+    if (there == 0) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (SMALL) {
+        k_row[h] = row_in(second ? page[2 * h + 1] : page[2 * h], 16 * h + (second ? 8 : 0));
+        v_row[h] = row_in(g >= 2 ? page[2 * h + 1] : page[2 * h], 16 * h + (g >= 2 ? 8 : 0));
+      } else {
+        k_row[h] = v_row[h] = row_in(page[0], 0);
+      }
+    }
+
+    // K: token col of each half.
+    u32x4a kw[2][I8 ? (kSteps + 1) / 2 : kSteps];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* r = a.k + k_row[h] * (D * kSize) + (16 * h + col) * (D * kSize);
+      if constexpr (!I8) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) kw[h][s] = *reinterpret_cast<const u32x4a*>(r + (32 * s + 8 * g) * 2);
+      } else {
+#pragma unroll
+        for (int s = 0; s < kSteps / 2; ++s) kw[h][s] = *reinterpret_cast<const u32x4a*>(r + 64 * s + 16 * g);
+        if constexpr (kSteps % 2) {
+          const u32x2a v = *reinterpret_cast<const u32x2a*>(r + 32 * (kSteps - 1) + 8 * g);
+          kw[h][kSteps / 2] = u32x4a{v.x, v.y, 0u, 0u};
+        }
+      }
+    }
+    // V: tokens 4g..4g+3 of each half, in the lane's runs of dimensions.
+    VTile<I8, D> v;
+    f32x4 ks[2], vs[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* r = a.v + v_row[h] * (D * kSize) + (16 * h + 4 * g) * (D * kSize);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v.load(4 * h + i, r + i * (D * kSize), col);
+      if constexpr (I8) {
+        ks[h] = *reinterpret_cast<const f32x4*>(a.k_scales + v_row[h] + 16 * h + 4 * g);
+        vs[h] = *reinterpret_cast<const f32x4*>(a.v_scales + v_row[h] + 16 * h + 4 * g);
+      }
+    }
+    const bool whole = there == 0xFFFFFFFFu;
+    uint32_t mine = 0xFFu;   // bit 4h + i: the lane's token is there
+    if (!whole) mine = (there >> (4 * g) & 15u) | (there >> (16 + 4 * g) & 15u) << 4;
+
+    f32x4 s[NT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        s[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t) {
+          h8 kf;
+          if constexpr (!I8) kf = __builtin_bit_cast(h8, kw[h][t]);
+          else kf = t % 2 ? codes_h8(kw[h][t / 2].z, kw[h][t / 2].w) : codes_h8(kw[h][t / 2].x, kw[h][t / 2].y);
+          s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][t], s[n][h], 0, 0, 0);
+        }
+      }
+    if (!whole) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!(mine >> j & 1)) v.clear(j);
+    }
+
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float x[8], w[8];
+      float now, add;
+      auto weigh = [&](bool careful) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float own = s[n][j / 4][j % 4], oth = other_part(own);
+          float t;
+          if (careful) t = second ? both_parts(oth, own) : both_parts(own, oth);
+          else t = second ? fmaf(own, kPart, oth) : fmaf(oth, kPart, own);
+          t *= factor[n];
+          if constexpr (I8) t *= ks[j / 4][j % 4];
+          if (!whole) t = mine >> j & 1 ? t : -INFINITY;
+          x[j] = t;
+          top = fmaxf(top, t);
+        }
+        now = fmaxf(most[n], column_max(top));
+        const float base = now == -INFINITY ? 0.f : now;
+        add = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          w[j] = __builtin_amdgcn_exp2f(x[j] - base);
+          add += w[j];
+        }
+      };
+      weigh(false);
+      if (__any(add != add)) weigh(true);   // an infinity of K or q, or a NaN
+      sum[n] = now > most[n] ? sum[n] * __builtin_amdgcn_exp2f(most[n] - now) + add : sum[n] + add;
+      float old = 1.f;   // what y so far is to be scaled by
+      bool moved;
+      if constexpr (!I8) {
+        moved = now > most[n];
+        if (moved) old = __builtin_amdgcn_exp2f(most[n] - now);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] *= 0x1p14f;
+      } else {
+        // The weights of the codes are p times the token's scale: y is held
+        // relative to the largest of them, 2^ref, as p is to the maximum.
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          w[j] *= vs[j / 4][j % 4];
+          if (!whole) w[j] = mine >> j & 1 ? w[j] : 0.f;
+          top = fmaxf(top, __builtin_fabsf(w[j]));
+        }
+        top = column_max(top);
+        const float r = now > most[n] && most[n] > -INFINITY ? ref[n] + (most[n] - now) : ref[n];
+        const float need = static_cast<float>(static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 127 - 13);
+        const float to = fmaxf(fmaxf(need, r), -126.f);
+        moved = to > r;
+        if (moved) old = __builtin_amdgcn_exp2f(r - to);
+        ref[n] = to;
+        const float lift = __builtin_amdgcn_exp2f(-to);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] *= lift;
+      }
+      most[n] = now;
+      if (__any(moved)) {
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][f][i] *= old;
+      }
+      h8 pf;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) pf[j] = part_of(w[j], second);
+      // V's operands are formed again for a second head tile rather than held
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f) acc[n][f] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v.frag(f), pf, acc[n][f], 0, 0, 0);
+    }
+  }
+
+  // Join the wavefronts: y relative to the workgroup's maximum.
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const float all = column_sum(sum[n]);
+    if (lane < 8) {
+      wave_max[wave][8 * n + lane] = most[n];
+      wave_sum[wave][8 * n + lane] = all;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, wave_max[w][8 * n + (col & 7)]);
+    float scale = most[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(most[n] - top + (I8 ? ref[n] : -14.f));
+    if (sum[n] != sum[n]) scale = 1.f;   // NaN without a maximum: y is NaN already
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float own = acc[n][f][i], oth = other_part(own);
+        if (!second) joint[wave][8 * n + col][VTile<I8, D>::dim(f, 4 * g + i)] = both_parts(own, oth) * scale;
+      }
+  }
+  __syncthreads();
+  for (int e = tid; e < heads_here * D; e += 64 * kAttnWaves) {
+    const int h = e / D, d = e % D;
+    float top = -INFINITY, total = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, wave_max[w][h]);
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+      const float m = wave_max[w][h], l = wave_sum[w][h];
+      total += m == -INFINITY ? l : l * __builtin_amdgcn_exp2f(m - top);   // l is 0 there, or NaN
+      y += joint[w][h][d];
+    }
+    const int64_t at = row * p.heads + first_head + h;
+    if (parts <= 1) {
+      const float r = total == 0.f ? 0.f : y / total;
+      if (p.y_f32) static_cast<float*>(p.y)[at * D + d] = r;
+      else static_cast<_Float16*>(p.y)[at * D + d] = static_cast<_Float16>(r);
+    } else {
+      const int64_t slot = at * p.splits + part;
+      p.parts[slot * D + d] = y;
+      if (d == 0) {
+        p.stats[2 * slot] = top;
+        p.stats[2 * slot + 1] = total;
+      }
+    }
+  }
+#endif
+}
+
+}  // namespace pesti
+
+namespace pesti_attn {
+
+// Head tiles of 8 that a workgroup takes: two where a KV head has more than 8
+// query heads and the registers hold them.
+inline int head_tiles(int64_t group, int64_t head_dim) { return group > 8 && head_dim <= 128 ? 2 : 1; }
+
+template <bool I8, int D, int NT, bool SMALL>
+int launch(const pesti::AttnArgs& p, int64_t rows, hipStream_t st) {
+  pesti::AttnArgs args = p;
+  void* params[] = {&args};
+  return pesti_kv::launch(reinterpret_cast<const void*>(&pesti::attn_kernel<I8, D, NT, SMALL>),
+                          dim3(static_cast<unsigned>(p.splits), static_cast<unsigned>(p.kv.kv_heads * p.head_blocks),
+                               static_cast<unsigned>(rows)),
+                          dim3(64 * pesti::kAttnWaves), params, 0, st);
+}
+
+template <bool I8, int D>
+int launch_d(const pesti::AttnArgs& p, int64_t rows, hipStream_t st) {
+  const bool small = p.kv.page_shift < 5;
+  if constexpr (D <= 128) {
+    if (head_tiles(p.group, D) == 2) return small ? launch<I8, D, 2, true>(p, rows, st) : launch<I8, D, 2, false>(p, rows, st);
+  }
+  return small ? launch<I8, D, 1, true>(p, rows, st) : launch<I8, D, 1, false>(p, rows, st);
+}
+
+template <bool I8>
+int launch_format(const pesti::AttnArgs& p, int64_t rows, hipStream_t st) {
+  switch (p.kv.head_dim) {
+    case 32: return launch_d<I8, 32>(p, rows, st);
+    case 64: return launch_d<I8, 64>(p, rows, st);
+    case 96: return launch_d<I8, 96>(p, rows, st);
+    case 128: return launch_d<I8, 128>(p, rows, st);
+    case 160: return launch_d<I8, 160>(p, rows, st);
+    case 192: return launch_d<I8, 192>(p, rows, st);
+    case 224: return launch_d<I8, 224>(p, rows, st);
+    case 256: return launch_d<I8, 256>(p, rows, st);
+    default: return PESTI_ERR_SHAPE;
+  }
+}
+
+int launch_f16(const pesti::AttnArgs& p, int64_t rows, hipStream_t st);
+int launch_i8(const pesti::AttnArgs& p, int64_t rows, hipStream_t st);
+
+}  // namespace pesti_attn
