@@ -1,7 +1,25 @@
 // Mat-vec of 4-bit weights with a scale and a zero point per group:
 //   y[b][o] = sum_i s[o][i / G] (q[o][i] - z[o][i / G]) x[b][i] + bias[o]
 //
-// The plainest form: a wavefront per row, 8 weights (a dword) per lane and step.
+// Codes become binary16 integers in pairs: two 4-bit codes of a register under
+// the exponent of 1024 (or of 16 codes higher, and a sixteenth of it), and one
+// packed addition of -(1024 + z): q - z exactly, 9 vector instructions for 8
+// weights.  Two kernels multiply them:
+//
+//   one or two columns of x   on the vector ALUs, with one fma of a binary16 and
+//     a float32 factor per weight and column.  x stays in registers as it is: a
+//     lane holds the same 32 (or 64) elements for every row it serves, so
+//     nothing is staged and a short launch is one memory round trip.
+//   more columns              on the matrix cores, v_mfma_f32_16x16x32_f16, with
+//     x as the 16-row operand and 16 rows of W as the columns.  Rows 0-7 of x
+//     are the first binary16 parts of up to eight columns, rows 8-15 what these
+//     leave, 2^11 times as large.  A column of the result is one row of W in all
+//     lanes that hold it, so the lane that unpacks a row's codes also has the
+//     scales that its sums take.
+//
+// In both a group's sum is finished in float32 and takes its scale in one fma.
+#include <type_traits>
+
 #include "common.h"
 
 namespace pesti {
@@ -22,10 +40,33 @@ struct I4Op {
 };
 struct I4Args {
   I4Op op[PESTI_MAX_GROUP];
-  int32_t shift;   // log2 of the group size
+  int32_t shift;          // log2 of the group size
   int32_t batch;
-  int32_t pair;
+  int32_t k_waves;        // wavefronts that share a tile's row length
+  int32_t phase_chunks;   // chunks of x staged at once
+  int32_t batch_magic;    // ceil(2^16 / batch)
 };
+
+// Sum over groups of L lanes, in every lane: rows of 16 by DPP, then exchanges
+// of quarters and halves of the wavefront.
+template <int L>
+__device__ __forceinline__ float row_sum(float v) {
+#ifdef __HIP_DEVICE_COMPILE__
+  v = group_sum<16>(v);
+  auto add = [](auto h) {
+    return __builtin_bit_cast(float, static_cast<uint32_t>(h[0])) + __builtin_bit_cast(float, static_cast<uint32_t>(h[1]));
+  };
+  if constexpr (L >= 32) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    v = add(__builtin_amdgcn_permlane16_swap(b, b, false, false));
+  }
+  if constexpr (L >= 64) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    v = add(__builtin_amdgcn_permlane32_swap(b, b, false, false));
+  }
+#endif
+  return v;
+}
 
 __device__ __forceinline__ float i4_scale(const I4Matrix& m, int64_t row, int32_t groups, int32_t g) {
   return f16_lo(m.scales[row * groups + g]);
@@ -34,30 +75,497 @@ __device__ __forceinline__ int i4_zero(const I4Matrix& m, int64_t row, int32_t g
   return m.zeros ? m.zeros[row * groups + g] : 8;
 }
 
-__global__ __launch_bounds__(64) void gemv_i4group_kernel(I4Args p) {
-  const I4Op& o = p.op[blockIdx.y];
-  const int64_t row = blockIdx.x;
-  if (row >= o.out) return;
-  const int lane = threadIdx.x;
-  for (int b = 0; b < p.batch; ++b) {
-    float y[2] = {0.f, 0.f};
-    for (int k = 0; k <= p.pair; ++k) {
-      const I4Matrix& m = k ? o.b : o.a;
-      float acc = 0.f;
-      for (int i = 8 * lane; i < o.in; i += 512) {
-        const uint32_t w = load_u32(m.packed + row * (o.in / 2) + i / 2);
-        const int g = i >> p.shift, z = i4_zero(m, row, o.groups, g);
-        float s = 0.f;
+constexpr int kChunk = 128;        // weights of a row that a wavefront takes at once
+constexpr int kI4MaxWaves = 8;
+// LDS bytes of a chunk of x in operand order: 16 runs (step, lane group) of the
+// parts of the columns, one unused place behind each run so that the 16 lanes
+// that write a chunk do not meet in one bank.
+constexpr int chunk_bytes(int batch) { return 256 * (2 * batch + 1); }
+
+#ifdef __HIP_DEVICE_COMPILE__
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef uint16_t u16u1 __attribute__((aligned(1)));
+typedef uint32_t u32u1 __attribute__((aligned(1)));
+typedef uint32_t u32u2 __attribute__((aligned(2)));
+typedef uint32_t u32x2u2 __attribute__((ext_vector_type(2), aligned(2)));
+
+// -(1024 + z) twice, of byte i of z; i4_operand's zero.
+__device__ __forceinline__ h2 i4_zero_pair(uint32_t z, int i) {
+  return __builtin_bit_cast(h2, __builtin_amdgcn_perm(0xE4E4E4E4u, z, 0x04000400u | i | i << 16));
+}
+
+// q - z of 8 codes, in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ h8 i4_operand(uint32_t w, h2 zero, uint32_t magic) {
+  const h2 sixteenth = {static_cast<_Float16>(0.0625f), static_cast<_Float16>(0.0625f)};
+  const h2 zero16 = zero + h2{static_cast<_Float16>(960.f), static_cast<_Float16>(960.f)};   // -(64 + z)
+  auto low = [&](uint32_t v) { return __builtin_bit_cast(h2, (v & 0x000F000Fu) | magic) + zero; };
+  auto high = [&](uint32_t v) {
+    return __builtin_elementwise_fma(__builtin_bit_cast(h2, (v & 0x00F000F0u) | magic), sixteenth, zero16);
+  };
+  const h2 a = low(w), b = high(w), c = low(w >> 8), d = high(w >> 8);
+  return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// 0x64006400 in a register, so that mask and exponent are one instruction
+// (v_and_or_b32 takes no literals).
+__device__ __forceinline__ uint32_t i4_magic() {
+  uint32_t v = 0x64006400u;
+  asm volatile("" : "+v"(v));
+  return v;
+}
+#endif
+
+// ---------------------------------------------------------------------------
+// One or two columns: L lanes per row, J dwords (8 weights) a lane, R rows a
+// lane group (PAIR: a row of each matrix).  A lane's dwords lie L apart, so a
+// load of codes, and of the 32 bytes of x behind each, is one run of memory.
+// Rows longer than 8 J L weights (L = 64) are walked in passes.  A workgroup
+// takes slabs of rows in turn; the next slab's codes are in flight under the
+// arithmetic of this one.
+// ---------------------------------------------------------------------------
+template <int B, int L, int J, int R, bool PAIR>
+__global__ __launch_bounds__(256) void gemv_i4group_few_kernel(I4Args p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  static_assert(!PAIR || R == 2, "a pair is two rows");
+  constexpr int kGroups = 4 * 64 / L, kRows = PAIR ? kGroups : kGroups * R;   // lane groups, rows of y per slab
+  const I4Op o = p.op[blockIdx.y];
+  const int sub = threadIdx.x & (L - 1), mine = static_cast<int>(threadIdx.x / L);
+  const int64_t slabs = (o.out + kRows - 1) / kRows;
+  if (blockIdx.x >= slabs) return;
+  const int dwords = o.in / 8, passes = (dwords + L * J - 1) / (L * J), shift = p.shift - 3;
+  const uint32_t magic = i4_magic();
+
+  struct Codes {
+    uint32_t q, s, z;
+  };
+  Codes w[J][R];
+  auto row_of = [&](int64_t slab, int r) {
+    const int64_t row = slab * kRows + (PAIR ? mine : mine + kGroups * r);
+    return row < o.out ? row : o.out - 1;
+  };
+  // Dwords past the row's end stand for dword 0 (x is zero there).
+  auto load = [&](int64_t slab, int pass) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          s = fmaf(static_cast<float>(static_cast<int>(w >> (4 * e) & 15) - z), o.x[static_cast<int64_t>(b) * o.in + i + e], s);
-        acc = fmaf(s, i4_scale(m, row, o.groups, g), acc);
+    for (int r = 0; r < R; ++r) {
+      const I4Matrix& m = PAIR && r ? o.b : o.a;
+      const int64_t row = row_of(slab, r), g0 = row * o.groups;
+      const uint32_t* rp = reinterpret_cast<const uint32_t*>(m.packed + row * (o.in / 2));
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        int d = (pass * J + j) * L + sub;
+        d = d < dwords ? d : 0;
+        w[j][r].q = rp[d];
+        w[j][r].s = m.scales[g0 + (d >> shift)];
+        w[j][r].z = m.zeros ? m.zeros[g0 + (d >> shift)] : 8;
       }
-      y[k] = group_sum<64>(acc);
     }
-    if (lane == 0)
-      o.y[b * o.out + row] = p.pair ? y[0] / (1.f + expf(-y[0])) * y[1] : y[0] + (o.bias ? o.bias[row] : 0.f);
+  };
+  f32x4 x[B][J][2];
+  auto load_x = [&](int pass) {
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int d = (pass * J + j) * L + sub;
+        x[b][j][0] = x[b][j][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (d < dwords) {
+          const f32x4* src = reinterpret_cast<const f32x4*>(o.x + static_cast<int64_t>(b) * o.in + 8 * d);
+          x[b][j][0] = src[0];
+          x[b][j][1] = src[1];
+        }
+      }
+  };
+  int64_t slab = blockIdx.x;
+  load(slab, 0);
+  if (passes == 1) load_x(0);
+  for (; slab < slabs; slab += gridDim.x) {
+    float acc[R][B], bias[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      bias[r] = !PAIR && o.bias ? o.bias[row_of(slab, r)] : 0.f;
+#pragma unroll
+      for (int b = 0; b < B; ++b) acc[r][b] = 0.f;
+    }
+    for (int pass = 0; pass < passes; ++pass) {
+      if (passes > 1) load_x(pass);
+      Codes now[J][R];
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) now[j][r] = w[j][r];
+      if (pass + 1 < passes) load(slab, pass + 1);
+      else if (slab + gridDim.x < slabs) load(slab + gridDim.x, 0);
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const h8 q = i4_operand(now[j][r].q, i4_zero_pair(now[j][r].z, 0), magic);
+          const float scale = f16_lo(now[j][r].s);
+#pragma unroll
+          for (int b = 0; b < B; ++b) {
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(static_cast<float>(q[2 * (e % 4) + e / 4]), x[b][j][e / 4][e % 4], s);
+            acc[r][b] = fmaf(s, scale, acc[r][b]);
+          }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int b = 0; b < B; ++b) acc[r][b] = row_sum<L>(acc[r][b]);
+    if (sub == 0) {
+      if constexpr (PAIR) {
+        const int64_t row = slab * kRows + mine;
+        if (row < o.out)
+#pragma unroll
+          for (int b = 0; b < B; ++b) o.y[b * o.out + row] = acc[0][b] / (1.f + expf(-acc[0][b])) * acc[R - 1][b];
+      } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int64_t row = slab * kRows + mine + kGroups * r;
+          if (row < o.out)
+#pragma unroll
+            for (int b = 0; b < B; ++b) o.y[b * o.out + row] = acc[r][b] + bias[r];
+        }
+      }
+    }
   }
+#endif
+}
+
+// ---------------------------------------------------------------------------
+// More columns, on the matrix cores.
+//
+//   codes   a lane loads 16 bytes, 32 weights of its row; four lane groups hold
+//           128 (a chunk).  Two exchanges of halves and two of quarters of the
+//           wavefront (v_permlane32_swap, v_permlane16_swap) turn that into one
+//           32-weight step per register, so a step lies in one group.
+//   x       staged in LDS in operand order; each 128-weight chunk of a column is
+//           scaled by a power of two for itself, which its sums get back.
+// ---------------------------------------------------------------------------
+#ifdef __HIP_DEVICE_COMPILE__
+// A chunk of one row: codes, and the scales and zero points of its GS groups.
+template <int GS>
+struct I4Chunk {
+  u32x4 q;
+  uint32_t s[(GS + 1) / 2];   // binary16 pairs
+  uint32_t z;                 // bytes
+};
+
+// GS groups of a chunk from group g0 on; the last ones of a row may be missing
+// (they have no weights).  groups and g0 are the same in all lanes.
+template <int GS>
+__device__ __forceinline__ void load_groups(const I4Matrix& m, int64_t row_groups, int32_t groups, int32_t g0, I4Chunk<GS>& c) {
+  const uint16_t* sp = m.scales + row_groups + g0;
+  const uint8_t* zp = m.zeros ? m.zeros + row_groups + g0 : nullptr;
+  c.z = 0x08080808u;
+  if constexpr (GS == 1) {
+    c.s[0] = sp[0];
+    if (zp) c.z = zp[0];
+  } else if (g0 + GS <= groups) {
+    if constexpr (GS == 2) {
+      c.s[0] = *reinterpret_cast<const u32u2*>(sp);
+      if (zp) c.z = *reinterpret_cast<const u16u1*>(zp);
+    } else {
+      const u32x2u2 v = *reinterpret_cast<const u32x2u2*>(sp);
+      c.s[0] = v.x;
+      c.s[1] = v.y;
+      if (zp) c.z = *reinterpret_cast<const u32u1*>(zp);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < (GS + 1) / 2; ++i) c.s[i] = 0;
+    if (zp) c.z = 0;
+#pragma unroll
+    for (int i = 0; i < GS; ++i)
+      if (g0 + i < groups) {
+        c.s[i / 2] |= static_cast<uint32_t>(sp[i]) << (16 * (i % 2));
+        if (zp) c.z |= static_cast<uint32_t>(zp[i]) << (8 * i);
+      }
+  }
+}
+
+// Register s of a lane becomes the 8 codes that its lane group has of step s.
+__device__ __forceinline__ void steps_of(const u32x4& q, uint32_t (&w)[4]) {
+  const auto a = __builtin_amdgcn_permlane32_swap(q.x, q.z, false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(q.y, q.w, false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  w[0] = c[0];
+  w[1] = c[1];
+  w[2] = d[0];
+  w[3] = d[1];
+}
+#endif
+
+// A wavefront takes tiles of 16 rows (PAIR: of both matrices), U chunks in
+// flight.  ROWS: each its own tiles, in turn; else the workgroup's wavefronts
+// deal one tile's chunks among themselves and join their sums in LDS.
+template <int GS, bool PAIR, bool ROWS, int U>
+__global__ __launch_bounds__(64 * kI4MaxWaves) void gemv_i4group_kernel(I4Args p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  extern __shared__ uint8_t lds[];
+  constexpr int R = PAIR ? 2 : 1;
+  const I4Op& o = p.op[blockIdx.y];
+  const int tid = threadIdx.x, waves = blockDim.x >> 6;
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const int batch = p.batch, in = o.in, chunks = (in + kChunk - 1) / kChunk;
+  const int phase = p.phase_chunks < chunks ? p.phase_chunks : chunks;
+  const int64_t out = o.out;
+  const int32_t tiles = static_cast<int32_t>((out + 15) / 16);
+  int32_t tile = ROWS ? blockIdx.x * waves + wave : blockIdx.x;
+  if (ROWS ? static_cast<int64_t>(blockIdx.x) * waves >= tiles : tile >= tiles) return;   // the whole workgroup
+  const int step = ROWS ? 1 : waves, first = ROWS ? 0 : wave;   // the wavefront's chunks
+  const int stride = 2 * batch + 1;
+  const uint32_t magic = i4_magic();
+
+  // LDS: x in operand order [step][lane group][part, column], what its chunks'
+  // sums are scaled by [chunk][8], partial sums of the wavefronts.
+  float* lower = reinterpret_cast<float*>(lds + phase * chunk_bytes(batch));
+  float* joint = lower + 8 * phase;
+  const int slot = n < 8 ? (n < batch ? n : batch - 1) : batch + (n - 8 < batch ? n - 8 : batch - 1);
+
+  // Chunks c0 .. c0 + count - 1 of x: 16 lanes take a chunk of a column.
+  auto stage = [&](int c0, int count) {
+    constexpr int kAhead = 4;
+    const int items = count * batch;
+    for (int base = wave * 4 + g; base - g < items; base += waves * 4 * kAhead) {
+      f32x4 v[kAhead][2];
+      int at[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int item = base + k * waves * 4;
+        const int c = item * p.batch_magic >> 16, b = item - c * batch, i = (c0 + c) * kChunk + 8 * n;
+        at[k] = item < items ? c * 16 + n : -1;
+        v[k][0] = v[k][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (item < items && i < in) {
+          const f32x4* src = reinterpret_cast<const f32x4*>(o.x + static_cast<int64_t>(b) * in + i);
+          v[k][0] = src[0];
+          v[k][1] = src[1];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int item = base + k * waves * 4;
+        const int c = item * p.batch_magic >> 16, b = item - c * batch;
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float m = __builtin_fabsf(v[k][j / 4][j % 4]);
+          top = m < INFINITY && m > top ? m : top;
+        }
+        top = fmaxf(top, dpp<0xB1>(top));    // over the 16 lanes
+        top = fmaxf(top, dpp<0x4E>(top));
+        top = fmaxf(top, dpp<0x141>(top));
+        top = fmaxf(top, dpp<0x140>(top));
+        const uint32_t bits = __builtin_bit_cast(uint32_t, top);
+        int up = 14 + 127 - static_cast<int>(bits >> 23);   // brings the largest to [2^14, 2^15)
+        up = bits == 0 ? 0 : (up > 126 ? 126 : up);
+        const float lift = __builtin_bit_cast(float, static_cast<uint32_t>(up + 127) << 23);
+        h8 hi, lo;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = v[k][j / 4][j % 4] * lift;
+          const _Float16 h = static_cast<_Float16>(x);
+          const float rest = (x - static_cast<float>(h)) * 0x1p11f;
+          const int e = 2 * (j % 4) + j / 4;   // codes j and j + 4 share a register
+          hi[e] = h;
+          lo[e] = static_cast<_Float16>(rest - rest == 0.f ? rest : 0.f);   // an infinity is all in the first part
+        }
+        if (at[k] >= 0) {
+          h8* x = reinterpret_cast<h8*>(lds) + at[k] * stride + b;
+          x[0] = hi;
+          x[batch] = lo;
+          if (n == 0) lower[8 * c + b] = __builtin_bit_cast(float, static_cast<uint32_t>(127 - up) << 23);
+        }
+      }
+    }
+    __syncthreads();
+  };
+
+  // The load cursor runs U chunks ahead of the arithmetic.
+  I4Chunk<GS> w[U][R];
+  const uint8_t* rp[R];
+  int64_t row_groups[R];
+  auto point = [&](int32_t t) {
+    int64_t row = static_cast<int64_t>(t) * 16 + n;
+    row = row < out ? row : out - 1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      rp[r] = (PAIR && r ? o.b.packed : o.a.packed) + row * (in / 2);
+      row_groups[r] = row * o.groups;
+    }
+  };
+  auto load = [&](int c, I4Chunk<GS> (&d)[R]) {
+    const int at = c * kChunk + 32 * g < in ? c * 64 + 16 * g : 0;   // (past the row: x is zero there)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      d[r].q = load_u32x4_a16(rp[r] + at);
+      load_groups<GS>(PAIR && r ? o.b : o.a, row_groups[r], o.groups, c * kChunk >> p.shift, d[r]);
+    }
+  };
+  float total[R][4];
+  auto clear = [&]() {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total[r][i] = 0.f;
+  };
+  // c: chunk within the phase
+  auto multiply = [&](int c, const I4Chunk<GS> (&d)[R]) {
+    const h8* x = reinterpret_cast<const h8*>(lds) + (c * 16 + g) * stride + slot;
+    h8 xf[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) xf[s] = x[s * 4 * stride];
+    const f32x4 low = *reinterpret_cast<const f32x4*>(lower + 8 * c + (4 * g & 7));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      uint32_t q[4];
+      steps_of(d[r].q, q);
+      f32x4 part;
+      float acc[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int gi = s * GS / 4;
+        if (s * GS % 4 == 0) part = f32x4{0.f, 0.f, 0.f, 0.f};
+        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(xf[s], i4_operand(q[s], i4_zero_pair(d[r].z, gi), magic), part, 0, 0, 0);
+        if ((s + 1) * GS % 4 == 0) {
+          const float scale = gi % 2 ? f16_hi(d[r].s[gi / 2]) : f16_lo(d[r].s[gi / 2]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = gi == 0 ? part[i] * scale : fmaf(part[i], scale, acc[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total[r][i] = fmaf(acc[i], low[i], total[r][i]);
+    }
+  };
+
+  // The thread's element of a tile that the wavefronts join.
+  const int eb = tid >> 4 & 7, en = tid & 15;
+  const bool mine = !ROWS && tid < 128 && eb < batch;
+  auto bias_of = [&](int32_t t) {
+    const int64_t row = static_cast<int64_t>(t) * 16 + (ROWS ? n : en);
+    return !PAIR && o.bias && row < out && (ROWS ? g < 2 : mine) ? o.bias[row] : 0.f;
+  };
+  auto store_rows = [&](int32_t t, float bias) {
+    float y[R][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t v = __builtin_bit_cast(uint32_t, total[r][i]);
+        const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        y[r][i] = fmaf(__builtin_bit_cast(float, static_cast<uint32_t>(h[1])), 0x1p-11f,
+                       __builtin_bit_cast(float, static_cast<uint32_t>(h[0])));
+      }
+    const int64_t row = static_cast<int64_t>(t) * 16 + n;
+    if (g >= 2 || row >= out) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = 4 * g + i;
+      if (b < batch) o.y[b * out + row] = PAIR ? y[0][i] / (1.f + expf(-y[0][i])) * y[R - 1][i] : y[0][i] + bias;
+    }
+  };
+  auto store_joint = [&](int32_t t, float* at, float bias) {   // at: one of two buffers, used in turn
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) at[((wave * R + r) * 4 + i) * 64 + lane] = total[r][i];
+    __syncthreads();
+    const int64_t row = static_cast<int64_t>(t) * 16 + en;
+    if (!mine || row >= out) return;
+    float y[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float hi = 0.f, lo = 0.f;
+#pragma unroll
+      for (int j = 0; j < kI4MaxWaves; ++j) {
+        const float* src = at + (((j < waves ? j : 0) * R + r) * 4 + eb % 4) * 64 + eb / 4 * 16 + en;
+        const float a = src[0], b = src[32];
+        hi += j < waves ? a : 0.f;
+        lo += j < waves ? b : 0.f;
+      }
+      y[r] = fmaf(lo, 0x1p-11f, hi);
+    }
+    o.y[eb * out + row] = PAIR ? y[0] / (1.f + expf(-y[0])) * y[R - 1] : y[0] + bias;
+  };
+
+  if (ROWS || phase == chunks) {
+    // Every chunk of x is staged; tiles follow each other.
+    const int32_t apart = ROWS ? gridDim.x * waves : gridDim.x;
+    int32_t next = tile;   // the load cursor: tile and chunk
+    int nc = first;
+    auto ahead = [&](I4Chunk<GS> (&d)[R]) {
+      if (next >= tiles || first >= chunks) return;
+      load(nc, d);
+      nc += step;
+      if (nc >= chunks) {
+        nc = first;
+        next += apart;
+        if (next < tiles) point(next);
+      }
+    };
+    if (next < tiles) point(next);
+#pragma unroll
+    for (int u = 0; u < U; ++u) ahead(w[u]);
+    float bias = tile < tiles ? bias_of(tile) : 0.f;
+    stage(0, chunks);
+    clear();
+    int c = first, turn = 0;
+    while (tile < tiles) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (tile >= tiles) break;
+        if (c < chunks) {
+          multiply(c, w[u]);
+          ahead(w[u]);
+        }
+        c += step;
+        if (c < chunks) continue;
+        c = first;
+        if constexpr (ROWS) store_rows(tile, bias);
+        else store_joint(tile, joint + turn * waves * R * 256, bias);
+        turn ^= 1;
+        clear();
+        tile += apart;
+        if (tile < tiles) bias = bias_of(tile);
+      }
+    }
+  } else if constexpr (!ROWS) {
+    // x in phases, one tile
+    point(tile);
+    clear();
+    const float bias = bias_of(tile);
+    for (int c0 = 0; c0 < chunks; c0 += phase) {
+      const int count = chunks - c0 < phase ? chunks - c0 : phase;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (first + u * step < count) load(c0 + first + u * step, w[u]);
+      if (c0 > 0) __syncthreads();   // x of the phase before has been read
+      stage(c0, count);
+      for (int base = first; base < count; base += U * step) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int c = base + u * step;
+          if (c >= count) break;
+          multiply(c, w[u]);
+          if (c + U * step < count) load(c0 + c + U * step, w[u]);
+        }
+      }
+    }
+    store_joint(tile, joint, bias);
+  }
+#endif
+}
+
+__global__ __launch_bounds__(256) void i4group_bias_kernel(I4Args p) {   // rows of no columns
+  const I4Op& o = p.op[blockIdx.y];
+  const int64_t n = o.out * p.batch;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
+    o.y[i] = o.bias ? o.bias[i % o.out] : 0.f;
 }
 
 // Eight weights of one dword per thread.
@@ -125,13 +633,126 @@ int device() {
   return pesti_host::current_device(&dev, &lds);
 }
 
-int launch(I4Args& p, int n_ops, hipStream_t st) {
+// How an op is computed: it depends on the op and the batch alone, so an op of a
+// group has the bits of its single call.
+enum Kind { kFew, kDeal, kRows };
+struct Cut {
+  int kind, waves, phase;
+  bool operator==(const Cut& c) const { return kind == c.kind && waves == c.waves && phase == c.phase; }
+};
+Cut cut_of(const I4Op& o, int batch) {
+  const int chunks = (o.in + pesti::kChunk - 1) / pesti::kChunk, dwords = o.in / 8;
+  const int64_t tiles = (o.out + 15) / 16;
+  if (batch <= 2) {   // dwords per lane group and pass: 32 x 1, 2, 4 or 64 x 4, 8
+    int span = 32;
+    while (span < dwords && span < 512) span *= 2;
+    return Cut{kFew, 4, span};
+  }
+  const int fits = 120 * 1024 / (pesti::chunk_bytes(batch) + 32);   // chunks of x in LDS, beside 32 KiB of sums
+  if (tiles >= 2048 && chunks <= fits / 2) return Cut{kRows, 8, chunks};
+  // 128 threads store a tile of eight columns
+  const int waves = chunks < 2 ? 2 : (chunks < pesti::kI4MaxWaves ? chunks : pesti::kI4MaxWaves);
+  return Cut{kDeal, waves, chunks < fits ? chunks : fits};
+}
+
+int64_t most_rows(const I4Args& p, int n_ops) {
   int64_t rows = 0;
   for (int i = 0; i < n_ops; ++i) rows = p.op[i].out > rows ? p.op[i].out : rows;
+  return rows;
+}
+
+int submit(const void* kernel, I4Args& p, int64_t blocks, int n_ops, int threads, size_t lds, hipStream_t st) {
   void* params[] = {&p};
-  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel),
-                                       dim3(static_cast<unsigned>(rows), static_cast<unsigned>(n_ops)), dim3(64), params, 0, st);
+  const hipError_t e = hipLaunchKernel(kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(n_ops)), dim3(threads),
+                                       params, lds, st);
   return e == hipSuccess ? PESTI_OK : PESTI_ERR_LAUNCH;
+}
+
+template <int B, int L, int J, bool PAIR>
+int launch_few(I4Args& p, int n_ops, hipStream_t st) {
+  const int64_t groups = 4 * 64 / L, rows = most_rows(p, n_ops);
+  auto run = [&](auto r) {
+    constexpr int R = decltype(r)::value;
+    const int64_t slabs = (rows + groups * (PAIR ? 1 : R) - 1) / (groups * (PAIR ? 1 : R));
+    return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_few_kernel<B, L, J, R, PAIR>), p, slabs < 2048 ? slabs : 2048,
+                  n_ops, 256, 0, st);
+  };
+  if constexpr (PAIR) {
+    return run(std::integral_constant<int, 2>{});
+  } else {
+    if (rows >= 1024 * groups) return run(std::integral_constant<int, 2>{});
+    return run(std::integral_constant<int, 1>{});
+  }
+}
+
+template <int B, bool PAIR>
+int launch_few_span(I4Args& p, int n_ops, int span, hipStream_t st) {
+  if (span == 32) return launch_few<B, 32, 1, PAIR>(p, n_ops, st);
+  if (span == 64) return launch_few<B, 32, 2, PAIR>(p, n_ops, st);
+  if (span == 128) return launch_few<B, 32, 4, PAIR>(p, n_ops, st);
+  if (span == 256) return launch_few<B, 64, 4, PAIR>(p, n_ops, st);
+  return launch_few<B, 64, 8, PAIR>(p, n_ops, st);
+}
+
+template <int GS, bool PAIR>
+int launch_many(I4Args& p, int n_ops, const Cut& c, hipStream_t st) {
+  constexpr int R = PAIR ? 2 : 1;
+  const int64_t tiles = (most_rows(p, n_ops) + 15) / 16;
+  p.phase_chunks = c.phase;
+  p.batch_magic = (65536 + p.batch - 1) / p.batch;
+  const size_t x = static_cast<size_t>(c.phase) * (pesti::chunk_bytes(p.batch) + 32);
+  if (c.kind == kRows) {
+    const int64_t blocks = (tiles + c.waves - 1) / c.waves;
+    return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel<GS, PAIR, true, 4>), p, blocks < 512 ? blocks : 512,
+                  n_ops, 64 * c.waves, x, st);
+  }
+  // Workgroups that are resident together stage x once and take tiles in turn;
+  // where x comes in phases each has one tile.
+  const size_t lds = x + 2 * static_cast<size_t>(c.waves) * R * 1024;
+  int64_t blocks = tiles;
+  bool phased = false;
+  for (int i = 0; i < n_ops; ++i) phased = phased || (p.op[i].in + pesti::kChunk - 1) / pesti::kChunk > c.phase;
+  const int64_t resident = 256 * (lds > 80 * 1024 ? 1 : 2);
+  if (!phased && blocks > resident) blocks = resident;
+  return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel<GS, PAIR, false, 4>), p, blocks, n_ops, 64 * c.waves,
+                lds, st);
+}
+
+template <bool PAIR>
+int launch_cut(I4Args& p, int n_ops, const Cut& c, hipStream_t st) {
+  if (c.kind == kFew)
+    return p.batch == 1 ? launch_few_span<1, PAIR>(p, n_ops, c.phase, st) : launch_few_span<2, PAIR>(p, n_ops, c.phase, st);
+  if (p.shift == 5) return launch_many<4, PAIR>(p, n_ops, c, st);
+  if (p.shift == 6) return launch_many<2, PAIR>(p, n_ops, c, st);
+  return launch_many<1, PAIR>(p, n_ops, c, st);
+}
+
+// Ops of one cut share a launch.
+int launch(const I4Args& all, int n_ops, bool pair, hipStream_t st) {
+  bool taken[PESTI_MAX_GROUP] = {};
+  for (int i = 0; i < n_ops; ++i) {
+    if (taken[i]) continue;
+    I4Args p = all;
+    int n = 0;
+    const bool empty = all.op[i].in == 0;
+    const Cut c = empty ? Cut{} : cut_of(all.op[i], all.batch);
+    for (int j = i; j < n_ops; ++j) {
+      if (taken[j] || (all.op[j].in == 0) != empty) continue;
+      if (!empty && !(cut_of(all.op[j], all.batch) == c)) continue;
+      taken[j] = true;
+      p.op[n++] = all.op[j];
+    }
+    int r;
+    if (empty) {
+      void* params[] = {&p};
+      r = hipLaunchKernel(reinterpret_cast<const void*>(&pesti::i4group_bias_kernel), dim3(64, static_cast<unsigned>(n)), dim3(256),
+                          params, 0, st) == hipSuccess ? PESTI_OK : PESTI_ERR_LAUNCH;
+    } else {
+      r = pair ? launch_cut<true>(p, n, c, st) : launch_cut<false>(p, n, c, st);
+    }
+    if (r != PESTI_OK) return r;
+  }
+  return PESTI_OK;
 }
 
 }  // namespace
@@ -154,7 +775,7 @@ int pesti_gemv_group_i4group(int32_t n_ops, const pesti_gemv_i4group_op* ops, in
   if (st != PESTI_OK) return st;
   p.shift = __builtin_ctzll(static_cast<unsigned long long>(group));
   p.batch = batch;
-  return launch(p, n, static_cast<hipStream_t>(stream));
+  return launch(p, n, false, static_cast<hipStream_t>(stream));
 }
 
 int pesti_gemv_i4group(int64_t out_features, int64_t in_features, int64_t group, const void* packed, const uint16_t* scales,
@@ -182,8 +803,7 @@ int pesti_gemv_i4group_swiglu(int64_t out_features, int64_t in_features, int64_t
   p.op[0].b = op_of(up, group).a;
   p.shift = __builtin_ctzll(static_cast<unsigned long long>(group));
   p.batch = batch;
-  p.pair = 1;
-  return launch(p, 1, static_cast<hipStream_t>(stream));
+  return launch(p, 1, true, static_cast<hipStream_t>(stream));
 }
 
 int pesti_dequant_i4group(int64_t rows, int64_t in_features, int64_t group, const void* packed, const uint16_t* scales,
