@@ -6,8 +6,10 @@
 // Which pages: a page is free where its count in refs is 0, and the lowest free
 // ones are taken in list order, found by a prefix sum over refs.  Nothing
 // depends on the order of atomics: claims of a sequence go to the lowest list
-// entry, counts are sums.  One workgroup plans (a 32-page run of refs per
-// thread and round: 64 Ki pages are two rounds); the grid that follows copies.
+// entry, counts are sums.  One workgroup plans, a thread per 32-page run of refs
+// and round (32 Ki pages); then a thread per page taken or moved finds its page
+// by its rank, so a run of free pages is not one thread's work.  The grid that
+// follows copies.
 #include <climits>
 
 #include "kv_cache.h"
@@ -57,6 +59,30 @@ __device__ __forceinline__ uint32_t run_mask(const KvArgs& a, int32_t first, boo
   return live ? held : (n > 0 ? ~held & ((1u << n) - 1) : 0u);
 }
 
+// The pages of a round by rank: runs' exclusive counts and bits in LDS.
+struct RoundLds {
+  int32_t before[kPlanThreads];
+  uint32_t bits[kPlanThreads];
+};
+__device__ __forceinline__ int32_t page_of_rank(const RoundLds& r, int32_t rank, int32_t base) {
+  int lo = 0;   // the last run with before <= rank holds it: it has pages, those behind it start later
+#pragma unroll
+  for (int step = kPlanThreads / 2; step > 0; step /= 2)
+    if (r.before[lo + step] <= rank) lo += step;
+  uint32_t m = r.bits[lo];
+  int k = rank - r.before[lo], at = 0;   // the k-th set bit
+#pragma unroll
+  for (int half = 16; half > 0; half /= 2) {
+    const int n = __popc(m & ((1u << half) - 1));
+    if (k >= n) {
+      k -= n;
+      m >>= half;
+      at += half;
+    }
+  }
+  return base + lo * kRun + at;
+}
+
 struct TakeArgs {
   KvArgs kv;
   int32_t n;
@@ -70,12 +96,14 @@ struct TakeArgs {
 // pages of the children, and writes the plan that fork_kernel follows.
 template <bool FORK>
 __global__ __launch_bounds__(kPlanThreads) void take_kernel(TakeArgs t) {
-  __shared__ int32_t claim[PESTI_MAX_SEQS];       // lowest list entry that names the sequence
+  __shared__ int32_t claim[PESTI_MAX_SEQS];   // lowest list entry that names the sequence; then each entry's pages before (extend) or parent's last page (fork)
   __shared__ int32_t start[PESTI_MAX_SEQS];   // pages taken by the entries before
-  __shared__ int32_t after[PESTI_MAX_SEQS];       // tokens after the call, -1 where the entry does not count
+  __shared__ int32_t after[PESTI_MAX_SEQS];   // tokens after the call, -1 where the entry does not count
+  __shared__ RoundLds round;
   __shared__ int64_t sums[kPlanThreads / 64];
   const KvArgs& a = t.kv;
   const int tid = threadIdx.x, page = 1 << a.page_shift;
+  const uint32_t mask0 = run_mask(a, tid * kRun, false);   // the first round's, asked for ahead of all else
   for (int i = tid; i < a.seqs; i += kPlanThreads) claim[i] = INT_MAX;
   __syncthreads();
   auto seq = [&](int i) { return t.list ? t.list[i] : i; };
@@ -89,26 +117,34 @@ __global__ __launch_bounds__(kPlanThreads) void take_kernel(TakeArgs t) {
   __syncthreads();
   int64_t total = 0;
   bool outgrown = false;
-  for (int base = 0; base < t.n; base += kPlanThreads) {
-    const int i = base + tid;
+  int32_t info[PESTI_MAX_SEQS / kPlanThreads];   // of the thread's entries, until the claims have been read
+#pragma unroll
+  for (int j = 0; j < PESTI_MAX_SEQS / kPlanThreads; ++j) {
+    const int i = j * kPlanThreads + tid;
+    info[j] = 0;
+    if (j * kPlanThreads >= t.n) continue;
     int64_t need = 0;
     if (i < t.n) {
       const int32_t s = seq(i);
       int64_t len = -1;
       if (named(s) && claim[s] == i) {
+        const int32_t old = kv_length(a, s);
         if constexpr (FORK) {
-          if (kv_length(a, s) == 0) {
-            len = kv_length(a, t.second[i]);
+          const int32_t parent = t.second[i], tokens = kv_length(a, parent);
+          if (old == 0) {
+            len = tokens;
             need = (len & (page - 1)) != 0;
+            if (need) info[j] = a.table[static_cast<int64_t>(parent) * a.width + (len >> a.page_shift)];
           }
         } else {
-          const int32_t old = kv_length(a, s), more = t.second ? t.second[i] : 1;
+          const int32_t more = t.second ? t.second[i] : 1;
           len = static_cast<int64_t>(old) + (more > 0 ? more : 0);
           if (len > static_cast<int64_t>(a.width) << a.page_shift) {
             outgrown = true;
             len = old;
           }
-          need = kv_pages_of(a, static_cast<int32_t>(len)) - kv_pages_of(a, old);
+          info[j] = kv_pages_of(a, old);
+          need = kv_pages_of(a, static_cast<int32_t>(len)) - info[j];
         }
       }
       after[i] = static_cast<int32_t>(len);
@@ -119,11 +155,18 @@ __global__ __launch_bounds__(kPlanThreads) void take_kernel(TakeArgs t) {
     total += sum;
   }
   int64_t missing = __syncthreads_or(outgrown) ? -1 : 0;
+#pragma unroll
+  for (int j = 0; j < PESTI_MAX_SEQS / kPlanThreads; ++j)
+    if (j * kPlanThreads + tid < t.n) claim[j * kPlanThreads + tid] = info[j];
+  constexpr int32_t kRound = kPlanThreads * kRun;
+  int64_t found = 0, sum = 0, before = 0;
   if (missing == 0 && total > 0) {
-    int64_t found = 0, sum;
-    for (int32_t base = 0; base < a.pages && found < total; base += kPlanThreads * kRun) {
-      plan_scan(static_cast<int64_t>(__popc(run_mask(a, base + tid * kRun, false))), &sum, sums);
-      found += sum;
+    before = plan_scan(static_cast<int64_t>(__popc(mask0)), &sum, sums);
+    found = sum;
+    for (int32_t base = kRound; base < a.pages && found < total; base += kRound) {
+      int64_t more;
+      plan_scan(static_cast<int64_t>(__popc(run_mask(a, base + tid * kRun, false))), &more, sums);
+      found += more;
     }
     if (found < total) missing = total - found;
   }
@@ -133,40 +176,43 @@ __global__ __launch_bounds__(kPlanThreads) void take_kernel(TakeArgs t) {
       for (int i = tid; i < t.n; i += kPlanThreads) t.plan[i] = make_int4(-1, -1, 0, 0);
     return;
   }
-  if constexpr (FORK) {
-    for (int i = tid; i < t.n; i += kPlanThreads)
-      t.plan[i] = make_int4(-1, -1, after[i] < 0 ? 0 : after[i] >> a.page_shift, after[i] >= 0);
+  __syncthreads();   // claim holds the entries' places now
+  found = 0;
+  for (int32_t base = 0; found < total; base += kRound) {
+    uint32_t m = mask0;
+    if (base > 0) {
+      m = run_mask(a, base + tid * kRun, false);
+      before = plan_scan(static_cast<int64_t>(__popc(m)), &sum, sums);
+    }
+    round.before[tid] = static_cast<int32_t>(before);
+    round.bits[tid] = m;
     __syncthreads();
-  }
-  int64_t found = 0, sum = 0;
-  for (int32_t base = 0; base < a.pages && found < total; base += kPlanThreads * kRun, found += sum) {
-    const int32_t first = base + tid * kRun;
-    uint32_t m = run_mask(a, first, false);
-    int32_t rank = static_cast<int32_t>(found + plan_scan(static_cast<int64_t>(__popc(m)), &sum, sums));
-    for (; m && rank < total; ++rank, m &= m - 1) {
-      const int32_t p = first + __builtin_ctz(m);
+    const int32_t here = static_cast<int32_t>(sum < total - found ? sum : total - found);
+    for (int32_t r = tid; r < here; r += kPlanThreads) {
+      const int32_t p = page_of_rank(round, r, base), rank = static_cast<int32_t>(found) + r;
       int lo = 0, hi = t.n;   // the entry with start <= rank < its end
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if (start[mid] <= rank) lo = mid; else hi = mid;
       }
-      const int32_t s = seq(lo);
-      int32_t* row = a.table + static_cast<int64_t>(s) * a.width;
+      int32_t* row = a.table + static_cast<int64_t>(seq(lo)) * a.width;
       a.refs[p] = 1;
       if constexpr (FORK) {
-        const int32_t whole = after[lo] >> a.page_shift;
-        const int32_t from = a.table[static_cast<int64_t>(t.second[lo]) * a.width + whole];
-        row[whole] = p;
-        t.plan[lo].x = kv_page_ok(a, from) ? from : -1;
-        t.plan[lo].y = p;
+        row[after[lo] >> a.page_shift] = p;
+        t.plan[lo] = make_int4(kv_page_ok(a, claim[lo]) ? claim[lo] : -1, p, after[lo] >> a.page_shift, 1);
       } else {
-        row[kv_pages_of(a, kv_length(a, s)) + rank - start[lo]] = p;
+        row[claim[lo] + rank - start[lo]] = p;
       }
     }
+    found += sum;
+    __syncthreads();   // the round's runs have been read
   }
-  __syncthreads();   // lengths have been read
-  for (int i = tid; i < t.n; i += kPlanThreads)
+  for (int i = tid; i < t.n; i += kPlanThreads) {
     if (after[i] >= 0) a.lengths[seq(i)] = after[i];
+    if constexpr (FORK)   // (pairs whose last page is copied have theirs)
+      if (after[i] < 0 || (after[i] & (page - 1)) == 0)
+        t.plan[i] = make_int4(-1, -1, after[i] < 0 ? 0 : after[i] >> a.page_shift, after[i] >= 0);
+  }
   if (tid == 0) *t.status = 0;
 }
 
@@ -268,36 +314,46 @@ struct CompactArgs {
 
 __global__ __launch_bounds__(kPlanThreads) void compact_plan_kernel(CompactArgs c) {
   __shared__ int64_t sums[kPlanThreads / 64];
+  __shared__ RoundLds hole_runs, mover_runs;
   const KvArgs& a = c.kv;
+  const int tid = threadIdx.x;
+  constexpr int32_t kRound = kPlanThreads * kRun;
+  const uint32_t mask0 = run_mask(a, tid * kRun, true);
   int64_t live = 0, sum;
-  for (int32_t base = 0; base < a.pages; base += kPlanThreads * kRun) {
-    plan_scan(static_cast<int64_t>(__popc(run_mask(a, base + static_cast<int32_t>(threadIdx.x) * kRun, true))), &sum, sums);
+  for (int32_t base = 0; base < a.pages; base += kRound) {
+    plan_scan(static_cast<int64_t>(__popc(base == 0 ? mask0 : run_mask(a, base + tid * kRun, true))), &sum, sums);
     live += sum;
   }
   int64_t holes = 0, movers = 0;
-  for (int32_t base = 0; base < a.pages; base += kPlanThreads * kRun) {
-    const int32_t first = base + static_cast<int32_t>(threadIdx.x) * kRun;
-    const uint32_t held = run_mask(a, first, true);
-    const int64_t room = live - first;   // pages of the run below the border
+  for (int32_t base = 0; base < a.pages; base += kRound) {
+    const int32_t first = base + tid * kRun;
+    const uint32_t held = base == 0 ? mask0 : run_mask(a, first, true);
+    const int64_t room = live - first;   // pages of the run below the border; all of those exist
     const uint32_t below = room >= 32 ? 0xFFFFFFFFu : (room <= 0 ? 0u : (1u << room) - 1);
-    uint32_t hole = ~held & below, mover = held & ~below;   // below the border all pages exist
+    const uint32_t hole = ~held & below, mover = held & ~below;
     const int64_t before = plan_scan((static_cast<int64_t>(__popc(hole)) << 32) | __popc(mover), &sum, sums);
-    int64_t h = holes + (before >> 32), m = movers + (before & 0xFFFFFFFF);
-    for (; hole; ++h, hole &= hole - 1) c.dst[h] = first + __builtin_ctz(hole);
-    for (int j = 0; j < kRun && first + j < a.pages; ++j)
-      if (!(mover >> j & 1)) c.map[first + j] = first + j;
+    hole_runs.before[tid] = static_cast<int32_t>(before >> 32);
+    hole_runs.bits[tid] = hole;
+    mover_runs.before[tid] = static_cast<int32_t>(before & 0xFFFFFFFF);
+    mover_runs.bits[tid] = mover;
+    __syncthreads();
+    const int32_t new_holes = static_cast<int32_t>(sum >> 32), new_movers = static_cast<int32_t>(sum & 0xFFFFFFFF);
+    for (int32_t r = tid; r < new_holes; r += kPlanThreads) c.dst[holes + r] = page_of_rank(hole_runs, r, base);
+    for (int32_t i = tid; i < kRound && base + i < a.pages; i += kPlanThreads)
+      if (!(mover_runs.bits[i / kRun] >> (i % kRun) & 1)) c.map[base + i] = base + i;
     __syncthreads();   // a mover's hole lies before it: it stands in dst now
-    for (; mover; ++m, mover &= mover - 1) {
-      const int32_t p = first + __builtin_ctz(mover), to = c.dst[m];
-      c.src[m] = p;
+    for (int32_t r = tid; r < new_movers; r += kPlanThreads) {
+      const int32_t p = page_of_rank(mover_runs, r, base), to = c.dst[movers + r];
+      c.src[movers + r] = p;
       c.map[p] = to;
       a.refs[to] = a.refs[p];
       a.refs[p] = 0;
     }
-    holes += sum >> 32;
-    movers += sum & 0xFFFFFFFF;
+    holes += new_holes;
+    movers += new_movers;
+    __syncthreads();   // the round's runs have been read
   }
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     *c.live = static_cast<int32_t>(live);
     *c.moves = static_cast<int32_t>(movers);
   }

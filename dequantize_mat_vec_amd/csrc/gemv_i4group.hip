@@ -85,10 +85,10 @@ constexpr int chunk_bytes(int batch) { return 256 * (2 * batch + 1); }
 #ifdef __HIP_DEVICE_COMPILE__
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef uint16_t u16u1 __attribute__((aligned(1)));
-typedef uint32_t u32u1 __attribute__((aligned(1)));
-typedef uint32_t u32u2 __attribute__((aligned(2)));
-typedef uint32_t u32x2u2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2a __attribute__((ext_vector_type(2), aligned(8)));
+typedef uint32_t u32x2u1 __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32x4u2 __attribute__((ext_vector_type(4), aligned(2)));
 
 // -(1024 + z) twice, of byte i of z; i4_operand's zero.
 __device__ __forceinline__ h2 i4_zero_pair(uint32_t z, int i) {
@@ -246,47 +246,6 @@ __global__ __launch_bounds__(256) void gemv_i4group_few_kernel(I4Args p) {
 //           scaled by a power of two for itself, which its sums get back.
 // ---------------------------------------------------------------------------
 #ifdef __HIP_DEVICE_COMPILE__
-// A chunk of one row: codes, and the scales and zero points of its GS groups.
-template <int GS>
-struct I4Chunk {
-  u32x4 q;
-  uint32_t s[(GS + 1) / 2];   // binary16 pairs
-  uint32_t z;                 // bytes
-};
-
-// GS groups of a chunk from group g0 on; the last ones of a row may be missing
-// (they have no weights).  groups and g0 are the same in all lanes.
-template <int GS>
-__device__ __forceinline__ void load_groups(const I4Matrix& m, int64_t row_groups, int32_t groups, int32_t g0, I4Chunk<GS>& c) {
-  const uint16_t* sp = m.scales + row_groups + g0;
-  const uint8_t* zp = m.zeros ? m.zeros + row_groups + g0 : nullptr;
-  c.z = 0x08080808u;
-  if constexpr (GS == 1) {
-    c.s[0] = sp[0];
-    if (zp) c.z = zp[0];
-  } else if (g0 + GS <= groups) {
-    if constexpr (GS == 2) {
-      c.s[0] = *reinterpret_cast<const u32u2*>(sp);
-      if (zp) c.z = *reinterpret_cast<const u16u1*>(zp);
-    } else {
-      const u32x2u2 v = *reinterpret_cast<const u32x2u2*>(sp);
-      c.s[0] = v.x;
-      c.s[1] = v.y;
-      if (zp) c.z = *reinterpret_cast<const u32u1*>(zp);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < (GS + 1) / 2; ++i) c.s[i] = 0;
-    if (zp) c.z = 0;
-#pragma unroll
-    for (int i = 0; i < GS; ++i)
-      if (g0 + i < groups) {
-        c.s[i / 2] |= static_cast<uint32_t>(sp[i]) << (16 * (i % 2));
-        if (zp) c.z |= static_cast<uint32_t>(zp[i]) << (8 * i);
-      }
-  }
-}
-
 // Register s of a lane becomes the 8 codes that its lane group has of step s.
 __device__ __forceinline__ void steps_of(const u32x4& q, uint32_t (&w)[4]) {
   const auto a = __builtin_amdgcn_permlane32_swap(q.x, q.z, false, false);
@@ -300,15 +259,32 @@ __device__ __forceinline__ void steps_of(const u32x4& q, uint32_t (&w)[4]) {
 }
 #endif
 
+// Scales and zero points of a tile pass through LDS in windows of 32 groups of
+// 16 rows: a lane loads 8 groups of a row at once (a load per chunk would fetch
+// each row's line again and again), and reads its row's back by chunk.
+[[maybe_unused]] constexpr int kWindow = 32;
+constexpr int kScaleRow = 80, kZeroRow = 40;   // LDS bytes of a row's window, padded against bank conflicts
+constexpr int kWindowBytes = 16 * (kScaleRow + kZeroRow);
+
 // A wavefront takes tiles of 16 rows (PAIR: of both matrices), U chunks in
 // flight.  ROWS: each its own tiles, in turn; else the workgroup's wavefronts
-// deal one tile's chunks among themselves and join their sums in LDS.
+// share a tile's chunks and join their sums in LDS (two wavefronts at least: 128
+// threads store the tile).  GS: groups of a chunk (1 where a group is 128 weights
+// or more).
+//
+// Loads are unconditional, from stand-in places where there is nothing to load:
+// the compiler then knows how many are younger than the one that it waits for.
 template <int GS, bool PAIR, bool ROWS, int U>
-__global__ __launch_bounds__(64 * kI4MaxWaves) void gemv_i4group_kernel(I4Args p) {
+__global__ __launch_bounds__(64 * kI4MaxWaves) __attribute__((amdgpu_waves_per_eu(PAIR ? 2 : 4)))
+void gemv_i4group_kernel(I4Args p) {
 #ifdef __HIP_DEVICE_COMPILE__
   extern __shared__ uint8_t lds[];
-  constexpr int R = PAIR ? 2 : 1;
-  const I4Op& o = p.op[blockIdx.y];
+  constexpr int R = PAIR ? 2 : 1, kWindowChunks = kWindow / GS;
+  static_assert(kWindowChunks % U == 0, "a window is whole rounds");
+  const I4Op o = p.op[blockIdx.y];
+  asm volatile("" ::"s"(o.a.packed), "s"(o.a.scales), "s"(o.a.zeros), "s"(o.x), "s"(o.y), "s"(o.bias), "s"(o.out), "s"(o.in),
+               "s"(o.groups), "s"(p.shift), "s"(p.batch), "s"(p.phase_chunks), "s"(p.batch_magic));
+  if constexpr (PAIR) asm volatile("" ::"s"(o.b.packed), "s"(o.b.scales), "s"(o.b.zeros));
   const int tid = threadIdx.x, waves = blockDim.x >> 6;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
@@ -318,19 +294,19 @@ __global__ __launch_bounds__(64 * kI4MaxWaves) void gemv_i4group_kernel(I4Args p
   const int32_t tiles = static_cast<int32_t>((out + 15) / 16);
   int32_t tile = ROWS ? blockIdx.x * waves + wave : blockIdx.x;
   if (ROWS ? static_cast<int64_t>(blockIdx.x) * waves >= tiles : tile >= tiles) return;   // the whole workgroup
-  const int step = ROWS ? 1 : waves, first = ROWS ? 0 : wave;   // the wavefront's chunks
   const int stride = 2 * batch + 1;
   const uint32_t magic = i4_magic();
 
   // LDS: x in operand order [step][lane group][part, column], what its chunks'
-  // sums are scaled by [chunk][8], partial sums of the wavefronts.
+  // sums are scaled by [chunk][8], windows of the wavefronts, partial sums.
   float* lower = reinterpret_cast<float*>(lds + phase * chunk_bytes(batch));
-  float* joint = lower + 8 * phase;
+  uint8_t* window = reinterpret_cast<uint8_t*>(lower + 8 * phase) + wave * R * kWindowBytes;
+  float* joint = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lower + 8 * phase) + waves * R * kWindowBytes);
   const int slot = n < 8 ? (n < batch ? n : batch - 1) : batch + (n - 8 < batch ? n - 8 : batch - 1);
 
   // Chunks c0 .. c0 + count - 1 of x: 16 lanes take a chunk of a column.
   auto stage = [&](int c0, int count) {
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 2;
     const int items = count * batch;
     for (int base = wave * 4 + g; base - g < items; base += waves * 4 * kAhead) {
       f32x4 v[kAhead][2];
@@ -349,6 +325,7 @@ __global__ __launch_bounds__(64 * kI4MaxWaves) void gemv_i4group_kernel(I4Args p
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
+        if (wave * 4 + (base - g - wave * 4) + k * waves * 4 >= items) break;   // the same for the wavefront
         const int item = base + k * waves * 4;
         const int c = item * p.batch_magic >> 16, b = item - c * batch;
         float top = 0.f;
@@ -386,27 +363,73 @@ __global__ __launch_bounds__(64 * kI4MaxWaves) void gemv_i4group_kernel(I4Args p
     __syncthreads();
   };
 
-  // The load cursor runs U chunks ahead of the arithmetic.
-  I4Chunk<GS> w[U][R];
-  const uint8_t* rp[R];
-  int64_t row_groups[R];
-  auto point = [&](int32_t t) {
-    int64_t row = static_cast<int64_t>(t) * 16 + n;
-    row = row < out ? row : out - 1;
+  const int64_t all_groups = out * o.groups;   // 8 at least
+  const uint8_t* packed[R] = {o.a.packed};
+  const uint16_t* scales[R] = {o.a.scales};
+  const uint8_t* zeros[R] = {o.a.zeros};
+  if constexpr (PAIR) {
+    packed[R - 1] = o.b.packed;
+    scales[R - 1] = o.b.scales;
+    zeros[R - 1] = o.b.zeros;
+  }
+  // Offsets within a tile fit 32 bits; its start is the same in all lanes.
+  const int half = in / 2;
+  auto row_in = [&](int32_t t) {   // the lane's row of the tile; past the last one, that
+    const int64_t left = out - 1 - static_cast<int64_t>(t) * 16;
+    return left < n ? static_cast<int>(left) : n;
+  };
+  // Codes of chunk c of the lane's row; past the row's end (x is zero there) its
+  // last ones.
+  auto load = [&](int32_t t, int row_at, int c, u32x4 (&d)[R]) {
+    int at = c * 64 + 16 * g;
+    at = row_at + (at < half - 16 ? at : half - 16);
+#pragma unroll
+    for (int r = 0; r < R; ++r) d[r] = load_u32x4_a16(packed[r] + static_cast<int64_t>(t) * 16 * half + static_cast<uint32_t>(at));
+  };
+
+  // Groups g0 + 8 g .. + 7 of the lane's row.  At the arrays' end the load
+  // starts earlier, and the values are moved down when they are put in place.
+  u32x4 ws[R];
+  u32x2 wz[R];
+  auto fetch = [&](int32_t t, int row, int g0) {
+    const int64_t start = static_cast<int64_t>(t) * 16 * o.groups, base = start < all_groups - 8 ? start : all_groups - 8;
+    const int64_t room = all_groups - 8 - base;
+    const int most = room < (1 << 30) ? static_cast<int>(room) : 1 << 30;
+    int at = row * o.groups + g0 + 8 * g + static_cast<int>(start - base);
+    at = at < most ? at : most;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      rp[r] = (PAIR && r ? o.b.packed : o.a.packed) + row * (in / 2);
-      row_groups[r] = row * o.groups;
+      ws[r] = *reinterpret_cast<const u32x4u2*>(scales[r] + base + static_cast<uint32_t>(at));
+      wz[r] = *reinterpret_cast<const u32x2u1*>((zeros[r] ? zeros[r] : reinterpret_cast<const uint8_t*>(scales[r])) + base +
+                                                static_cast<uint32_t>(at));
     }
   };
-  auto load = [&](int c, I4Chunk<GS> (&d)[R]) {
-    const int at = c * kChunk + 32 * g < in ? c * 64 + 16 * g : 0;   // (past the row: x is zero there)
+  auto place = [&](int32_t t, int row, int g0) {
+    const int64_t start = static_cast<int64_t>(t) * 16 * o.groups;
+    if (start + 16 * o.groups + kWindow > all_groups) {   // the same in all lanes
+      const int64_t past = start + row * o.groups + g0 + 8 * g - (all_groups - 8);
+      const int k = past <= 0 ? 0 : (past < 8 ? static_cast<int>(past) : 7);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint64_t lo = ws[r].x | static_cast<uint64_t>(ws[r].y) << 32, hi = ws[r].z | static_cast<uint64_t>(ws[r].w) << 32;
+        const int s = 16 * (k & 3);
+        uint64_t a = k & 4 ? hi >> s : lo >> s, b = k & 4 ? 0 : hi >> s;
+        if (s && !(k & 4)) a |= hi << (64 - s);
+        ws[r] = u32x4{static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32), static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32)};
+        const uint64_t z = (wz[r].x | static_cast<uint64_t>(wz[r].y) << 32) >> (8 * k);
+        wz[r] = u32x2{static_cast<uint32_t>(z), static_cast<uint32_t>(z >> 32)};
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      d[r].q = load_u32x4_a16(rp[r] + at);
-      load_groups<GS>(PAIR && r ? o.b : o.a, row_groups[r], o.groups, c * kChunk >> p.shift, d[r]);
+      if (!zeros[r]) wz[r] = u32x2{0x08080808u, 0x08080808u};
+      *reinterpret_cast<u32x4a*>(window + r * kWindowBytes + n * kScaleRow + 16 * g) = ws[r];
+      *reinterpret_cast<u32x2a*>(window + r * kWindowBytes + 16 * kScaleRow + n * kZeroRow + 8 * g) = wz[r];
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
+
   float total[R][4];
   auto clear = [&]() {
 #pragma unroll
@@ -414,8 +437,8 @@ __global__ __launch_bounds__(64 * kI4MaxWaves) void gemv_i4group_kernel(I4Args p
 #pragma unroll
       for (int i = 0; i < 4; ++i) total[r][i] = 0.f;
   };
-  // c: chunk within the phase
-  auto multiply = [&](int c, const I4Chunk<GS> (&d)[R]) {
+  // c: chunk within the phase; gw: its first group within the window
+  auto multiply = [&](int c, int gw, const u32x4 (&d)[R]) {
     const h8* x = reinterpret_cast<const h8*>(lds) + (c * 16 + g) * stride + slot;
     h8 xf[4];
 #pragma unroll
@@ -423,17 +446,32 @@ __global__ __launch_bounds__(64 * kI4MaxWaves) void gemv_i4group_kernel(I4Args p
     const f32x4 low = *reinterpret_cast<const f32x4*>(lower + 8 * c + (4 * g & 7));
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      const uint8_t* sp = window + r * kWindowBytes + n * kScaleRow + 2 * gw;
+      const uint8_t* zp = window + r * kWindowBytes + 16 * kScaleRow + n * kZeroRow + gw;
+      uint32_t sc[(GS + 1) / 2], z;
+      if constexpr (GS == 1) {
+        sc[0] = *reinterpret_cast<const uint16_t*>(sp);
+        z = *zp;
+      } else if constexpr (GS == 2) {
+        sc[0] = *reinterpret_cast<const uint32_t*>(sp);
+        z = *reinterpret_cast<const uint16_t*>(zp);
+      } else {
+        const u32x2a v = *reinterpret_cast<const u32x2a*>(sp);
+        sc[0] = v.x;
+        sc[(GS - 1) / 2] = v.y;
+        z = *reinterpret_cast<const uint32_t*>(zp);
+      }
       uint32_t q[4];
-      steps_of(d[r].q, q);
+      steps_of(d[r], q);
       f32x4 part;
       float acc[4];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const int gi = s * GS / 4;
         if (s * GS % 4 == 0) part = f32x4{0.f, 0.f, 0.f, 0.f};
-        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(xf[s], i4_operand(q[s], i4_zero_pair(d[r].z, gi), magic), part, 0, 0, 0);
+        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(xf[s], i4_operand(q[s], i4_zero_pair(z, gi), magic), part, 0, 0, 0);
         if ((s + 1) * GS % 4 == 0) {
-          const float scale = gi % 2 ? f16_hi(d[r].s[gi / 2]) : f16_lo(d[r].s[gi / 2]);
+          const float scale = gi % 2 ? f16_hi(sc[gi / 2]) : f16_lo(sc[gi / 2]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[i] = gi == 0 ? part[i] * scale : fmaf(part[i], scale, acc[i]);
         }
@@ -448,7 +486,7 @@ __global__ __launch_bounds__(64 * kI4MaxWaves) void gemv_i4group_kernel(I4Args p
   const bool mine = !ROWS && tid < 128 && eb < batch;
   auto bias_of = [&](int32_t t) {
     const int64_t row = static_cast<int64_t>(t) * 16 + (ROWS ? n : en);
-    return !PAIR && o.bias && row < out && (ROWS ? g < 2 : mine) ? o.bias[row] : 0.f;
+    return *(o.bias && row < out ? o.bias + row : o.x);
   };
   auto store_rows = [&](int32_t t, float bias) {
     float y[R][4];
@@ -466,7 +504,7 @@ __global__ __launch_bounds__(64 * kI4MaxWaves) void gemv_i4group_kernel(I4Args p
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int b = 4 * g + i;
-      if (b < batch) o.y[b * out + row] = PAIR ? y[0][i] / (1.f + expf(-y[0][i])) * y[R - 1][i] : y[0][i] + bias;
+      if (b < batch) o.y[b * out + row] = PAIR ? y[0][i] / (1.f + expf(-y[0][i])) * y[R - 1][i] : (o.bias ? y[0][i] + bias : y[0][i]);
     }
   };
   auto store_joint = [&](int32_t t, float* at, float bias) {   // at: one of two buffers, used in turn
@@ -490,73 +528,63 @@ __global__ __launch_bounds__(64 * kI4MaxWaves) void gemv_i4group_kernel(I4Args p
       }
       y[r] = fmaf(lo, 0x1p-11f, hi);
     }
-    o.y[eb * out + row] = PAIR ? y[0] / (1.f + expf(-y[0])) * y[R - 1] : y[0] + bias;
+    o.y[eb * out + row] = PAIR ? y[0] / (1.f + expf(-y[0])) * y[R - 1] : (o.bias ? y[0] + bias : y[0]);
   };
 
-  if (ROWS || phase == chunks) {
-    // Every chunk of x is staged; tiles follow each other.
-    const int32_t apart = ROWS ? gridDim.x * waves : gridDim.x;
-    int32_t next = tile;   // the load cursor: tile and chunk
-    int nc = first;
-    auto ahead = [&](I4Chunk<GS> (&d)[R]) {
-      if (next >= tiles || first >= chunks) return;
-      load(nc, d);
-      nc += step;
-      if (nc >= chunks) {
-        nc = first;
-        next += apart;
-        if (next < tiles) point(next);
-      }
-    };
-    if (next < tiles) point(next);
+  // x is staged at once, and the workgroup takes tiles in turn; or in phases,
+  // and it has one.  A wavefront's chunks of a phase are first .. first + count - 1.
+  const int32_t apart = ROWS ? gridDim.x * waves : gridDim.x;
+  u32x4 w[U][R];
+  if (tile >= tiles) tile = -1;   // no tiles for this wavefront: it stages x only
+  int32_t here_tile = tile < 0 ? 0 : tile;
+  int row = row_in(here_tile);
+  int turn = 0;
+  float bias = bias_of(here_tile);
+  clear();
+  for (int c0 = 0; c0 < chunks; c0 += phase) {
+    const int here = chunks - c0 < phase ? chunks - c0 : phase;
+    const int share = ROWS ? here : (here + waves - 1) / waves, first = ROWS ? 0 : wave * share;
+    const int count = here - first < share ? (here - first > 0 ? here - first : 0) : share;
+    const int g_first = (c0 + first) * kChunk >> p.shift;
 #pragma unroll
-    for (int u = 0; u < U; ++u) ahead(w[u]);
-    float bias = tile < tiles ? bias_of(tile) : 0.f;
-    stage(0, chunks);
-    clear();
-    int c = first, turn = 0;
-    while (tile < tiles) {
+    for (int u = 0; u < U; ++u) load(here_tile, row * half, c0 + first + u, w[u]);
+    fetch(here_tile, row, g_first);
+    if (c0 > 0) __syncthreads();   // x of the phase before has been read
+    stage(c0, here);
+    if (tile < 0) break;
+    while (true) {
+      const int32_t next = here_tile + apart < tiles ? here_tile + apart : here_tile;
+      const int next_row = row_in(next);
+      for (int w0 = 0; w0 < count; w0 += kWindowChunks) {
+        const int gw0 = (c0 + first + w0) * kChunk >> p.shift;
+        place(here_tile, row, gw0);
+        const bool more = w0 + kWindowChunks < count;
+        fetch(more ? here_tile : next, more ? row : next_row, more ? (c0 + first + w0 + kWindowChunks) * kChunk >> p.shift : g_first);
+        const int end = more ? w0 + kWindowChunks : count;
+        for (int i = w0; i < end; i += U) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (tile >= tiles) break;
-        if (c < chunks) {
-          multiply(c, w[u]);
-          ahead(w[u]);
-        }
-        c += step;
-        if (c < chunks) continue;
-        c = first;
-        if constexpr (ROWS) store_rows(tile, bias);
-        else store_joint(tile, joint + turn * waves * R * 256, bias);
-        turn ^= 1;
-        clear();
-        tile += apart;
-        if (tile < tiles) bias = bias_of(tile);
-      }
-    }
-  } else if constexpr (!ROWS) {
-    // x in phases, one tile
-    point(tile);
-    clear();
-    const float bias = bias_of(tile);
-    for (int c0 = 0; c0 < chunks; c0 += phase) {
-      const int count = chunks - c0 < phase ? chunks - c0 : phase;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (first + u * step < count) load(c0 + first + u * step, w[u]);
-      if (c0 > 0) __syncthreads();   // x of the phase before has been read
-      stage(c0, count);
-      for (int base = first; base < count; base += U * step) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int c = base + u * step;
-          if (c >= count) break;
-          multiply(c, w[u]);
-          if (c + U * step < count) load(c0 + c + U * step, w[u]);
+          for (int u = 0; u < U; ++u) {
+            if (i + u >= end) break;
+            multiply(first + i + u, ((c0 + first + i + u) * kChunk >> p.shift) - gw0, w[u]);
+            const bool same = i + u + U < count;
+            load(same ? here_tile : next, (same ? row : next_row) * half, c0 + first + (same ? i + u + U : u), w[u]);
+            __builtin_amdgcn_sched_barrier(0);   // (steps side by side cost registers, and wavefronts)
+          }
         }
       }
+      if (phase < chunks) break;   // the tile's next phase
+      if constexpr (ROWS) store_rows(here_tile, bias);
+      else store_joint(here_tile, joint + turn * waves * R * 256, bias);
+      turn ^= 1;
+      clear();
+      if (here_tile + apart >= tiles) break;
+      here_tile = next;
+      row = next_row;
+      bias = bias_of(here_tile);
     }
-    store_joint(tile, joint, bias);
+  }
+  if constexpr (!ROWS) {
+    if (phase < chunks) store_joint(tile, joint, bias);
   }
 #endif
 }
@@ -643,12 +671,13 @@ struct Cut {
 Cut cut_of(const I4Op& o, int batch) {
   const int chunks = (o.in + pesti::kChunk - 1) / pesti::kChunk, dwords = o.in / 8;
   const int64_t tiles = (o.out + 15) / 16;
-  if (batch <= 2) {   // dwords per lane group and pass: 32 x 1, 2, 4 or 64 x 4, 8
+  // (the matrix kernel loads eight groups' scales at once)
+  if (batch <= 2 || o.out * o.groups < 8) {   // dwords per lane group and pass: 32 x 1, 2, 4 or 64 x 4, 8
     int span = 32;
     while (span < dwords && span < 512) span *= 2;
     return Cut{kFew, 4, span};
   }
-  const int fits = 120 * 1024 / (pesti::chunk_bytes(batch) + 32);   // chunks of x in LDS, beside 32 KiB of sums
+  const int fits = 96 * 1024 / (pesti::chunk_bytes(batch) + 32);   // chunks of x in LDS, beside 62 KiB of windows and sums
   if (tiles >= 2048 && chunks <= fits / 2) return Cut{kRows, 8, chunks};
   // 128 threads store a tile of eight columns
   const int waves = chunks < 2 ? 2 : (chunks < pesti::kI4MaxWaves ? chunks : pesti::kI4MaxWaves);
@@ -700,10 +729,10 @@ int launch_many(I4Args& p, int n_ops, const Cut& c, hipStream_t st) {
   const int64_t tiles = (most_rows(p, n_ops) + 15) / 16;
   p.phase_chunks = c.phase;
   p.batch_magic = (65536 + p.batch - 1) / p.batch;
-  const size_t x = static_cast<size_t>(c.phase) * (pesti::chunk_bytes(p.batch) + 32);
+  const size_t x = static_cast<size_t>(c.phase) * (pesti::chunk_bytes(p.batch) + 32) + static_cast<size_t>(c.waves) * R * pesti::kWindowBytes;
   if (c.kind == kRows) {
     const int64_t blocks = (tiles + c.waves - 1) / c.waves;
-    return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel<GS, PAIR, true, 4>), p, blocks < 512 ? blocks : 512,
+    return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel<GS, PAIR, true, 2>), p, blocks < 512 ? blocks : 512,
                   n_ops, 64 * c.waves, x, st);
   }
   // Workgroups that are resident together stage x once and take tiles in turn;
@@ -714,14 +743,25 @@ int launch_many(I4Args& p, int n_ops, const Cut& c, hipStream_t st) {
   for (int i = 0; i < n_ops; ++i) phased = phased || (p.op[i].in + pesti::kChunk - 1) / pesti::kChunk > c.phase;
   const int64_t resident = 256 * (lds > 80 * 1024 ? 1 : 2);
   if (!phased && blocks > resident) blocks = resident;
-  return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel<GS, PAIR, false, 4>), p, blocks, n_ops, 64 * c.waves,
+  return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel<GS, PAIR, false, 2>), p, blocks, n_ops, 64 * c.waves,
                 lds, st);
 }
 
 template <bool PAIR>
 int launch_cut(I4Args& p, int n_ops, const Cut& c, hipStream_t st) {
-  if (c.kind == kFew)
-    return p.batch == 1 ? launch_few_span<1, PAIR>(p, n_ops, c.phase, st) : launch_few_span<2, PAIR>(p, n_ops, c.phase, st);
+  if (c.kind == kFew) {
+    for (int b = 0; b < p.batch; b += 2) {   // two columns a launch
+      I4Args q = p;
+      q.batch = p.batch - b < 2 ? 1 : 2;
+      for (int i = 0; i < n_ops; ++i) {
+        q.op[i].x += static_cast<int64_t>(b) * q.op[i].in;
+        q.op[i].y += b * q.op[i].out;
+      }
+      const int r = q.batch == 1 ? launch_few_span<1, PAIR>(q, n_ops, c.phase, st) : launch_few_span<2, PAIR>(q, n_ops, c.phase, st);
+      if (r != PESTI_OK) return r;
+    }
+    return PESTI_OK;
+  }
   if (p.shift == 5) return launch_many<4, PAIR>(p, n_ops, c, st);
   if (p.shift == 6) return launch_many<2, PAIR>(p, n_ops, c, st);
   return launch_many<1, PAIR>(p, n_ops, c, st);
