@@ -153,6 +153,7 @@ def load(path: os.PathLike | None = None) -> ctypes.CDLL:
     # cross between the two.
     import torch  # noqa: F401
     lib = ctypes.CDLL(str(p))
+    _bind_fast_args()
     for name, (res, args) in _SIGNATURES.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -160,6 +161,19 @@ def load(path: os.PathLike | None = None) -> ctypes.CDLL:
     if path is None:
         _lib = lib
     return lib
+
+
+def _bind_fast_args():
+    """Put the compiled argument checks (csrc/tensor_args.cpp) before the ones below: the same answers and errors,
+    a fifth of the time.  Without them (built for another torch, say) those below do alone."""
+    global _sized, _rows, _current
+    try:
+        from . import _tensor_args
+    except ImportError:
+        return
+    if _sized is not _tensor_args.sized:
+        _tensor_args.bind(_sized, _rows)
+        _sized, _rows, _current = _tensor_args.sized, _tensor_args.rows, _tensor_args.place
 
 
 def _ptr(obj):
@@ -351,6 +365,11 @@ def _sized(dev, obj, nbytes, what, dtype=None):
     raise ValueError(f"{what} must be a {dtype} tensor, got {obj.dtype}")
 
 
+def _current():
+    """(current device, its current stream's handle); the compiled one gives None where there is no GPU."""
+    return None
+
+
 def _place(stream):
     """(torch, current device, raw stream) of a call: device 0 where no GPU
     is to be asked (the library then refuses the call itself)."""
@@ -358,6 +377,9 @@ def _place(stream):
     if torch is None:
         import torch
     if stream is None:
+        at = _current()
+        if at is not None:
+            return torch, at[0], at[1]
         dev = torch.cuda.current_device()
         return torch, dev, _raw_stream(torch, dev)
     return torch, torch.cuda.current_device() if torch.cuda.is_available() else 0, _stream(stream)
@@ -365,19 +387,26 @@ def _place(stream):
 
 _TYPE_FORMATS = {"torch.float32": 17, "torch.float16": 16}   # by str(dtype)
 _TYPES = {17: "float32", 16: "float16", 3: "int8"}           # the torch type of a format's values
+_by_dtype = {}   # (format id, bytes per value) of the types of X and Y, once torch is there
+_dtypes = {}     # format id -> torch type
 
 
 def _type_of(torch, fid):
     """The tensor type that format fid's values must have: bfloat16 has binary16's
     size and uint8 the codes', so sizes alone would let them pass as those.
     None for an id that the library refuses."""
-    name = _TYPES.get(fid)
-    return name and getattr(torch, name)
+    if not _dtypes:
+        _dtypes.update({f: getattr(torch, name) for f, name in _TYPES.items()})
+        _by_dtype.update({torch.float32: (17, 4), torch.float16: (16, 2)})
+    return _dtypes.get(fid)
 
 
 def _value_format(fmt, obj, what):
     """(PESTI_FMT_* id, bytes per value) of X or Y: as given, else by the tensor's type."""
     if fmt is None:
+        found = _by_dtype.get(getattr(obj, "dtype", None))
+        if found is not None:
+            return found
         kind = str(getattr(obj, "dtype", None))
         fid = _TYPE_FORMATS.get(kind)
         if fid is None:
@@ -456,20 +485,15 @@ def _groups(in_features, group):
     return -(-in_features // group) if group > 0 else 0
 
 
-def _i4group(dev, torch, out_features, in_features, group, packed, scales, zeros, what=""):
-    """Pointers of one matrix, its tensors' sizes and types checked."""
-    n = out_features * _groups(in_features, group)
-    return (_sized(dev, packed, out_features * (in_features // 2), what + "packed", torch.uint8),
-            _sized(dev, scales, 2 * n, what + "scales", torch.float16), _sized(dev, zeros, n, what + "zeros", torch.uint8))
-
-
 def pesti_gemv_i4group(out_features, in_features, group, packed, scales, zeros, x, y, bias=None, batch=1, stream=None):
     """y = W x + bias, W in 4-bit codes with a binary16 scale per `group` weights of a row and a zero point (None: 8)."""
     torch, dev, st = _place(stream)
-    return _check("pesti_gemv_i4group", load().pesti_gemv_i4group(
-        out_features, in_features, group, *_i4group(dev, torch, out_features, in_features, group, packed, scales, zeros),
-        _sized(dev, x, 4 * batch * in_features, "x", torch.float32), _sized(dev, y, 4 * batch * out_features, "y", torch.float32),
-        _sized(dev, bias, 4 * out_features, "bias", torch.float32), batch, st))
+    fn, n, f32 = load().pesti_gemv_i4group, out_features * _groups(in_features, group), torch.float32
+    return _check("pesti_gemv_i4group", fn(
+        out_features, in_features, group, _sized(dev, packed, out_features * (in_features // 2), "packed", torch.uint8),
+        _sized(dev, scales, 2 * n, "scales", torch.float16), _sized(dev, zeros, n, "zeros", torch.uint8),
+        _sized(dev, x, 4 * batch * in_features, "x", f32), _sized(dev, y, 4 * batch * out_features, "y", f32),
+        _sized(dev, bias, 4 * out_features, "bias", f32), batch, st))
 
 
 def gemv_i4group_ops(ops, group, batch=1):
@@ -478,7 +502,10 @@ def gemv_i4group_ops(ops, group, batch=1):
     torch, dev, _ = _place(0)
     arr = (GemvI4GroupOp * max(len(ops), 1))()
     for i, (out, inf, packed, scales, zeros, x, y, bias) in enumerate(ops):
-        arr[i] = GemvI4GroupOp(out, inf, *_i4group(dev, torch, out, inf, group, packed, scales, zeros, f"op {i}: "),
+        n = out * _groups(inf, group)
+        arr[i] = GemvI4GroupOp(out, inf, _sized(dev, packed, out * (inf // 2), f"op {i}: packed", torch.uint8),
+                               _sized(dev, scales, 2 * n, f"op {i}: scales", torch.float16),
+                               _sized(dev, zeros, n, f"op {i}: zeros", torch.uint8),
                                _sized(dev, x, 4 * batch * inf, f"op {i}: x", torch.float32),
                                _sized(dev, y, 4 * batch * out, f"op {i}: y", torch.float32),
                                _sized(dev, bias, 4 * out, f"op {i}: bias", torch.float32))
@@ -501,18 +528,23 @@ def pesti_gemv_i4group_swiglu(out_features, in_features, group, gate_packed, gat
                               up_zeros, x, h, batch=1, stream=None):
     """h = silu(W_gate x) * (W_up x) in one launch."""
     torch, dev, st = _place(stream)
-    return _check("pesti_gemv_i4group_swiglu", load().pesti_gemv_i4group_swiglu(
-        out_features, in_features, group,
-        *_i4group(dev, torch, out_features, in_features, group, gate_packed, gate_scales, gate_zeros, "gate_"),
-        *_i4group(dev, torch, out_features, in_features, group, up_packed, up_scales, up_zeros, "up_"),
+    fn, codes, n = load().pesti_gemv_i4group_swiglu, out_features * (in_features // 2), out_features * _groups(in_features, group)
+    u8, f16 = torch.uint8, torch.float16
+    return _check("pesti_gemv_i4group_swiglu", fn(
+        out_features, in_features, group, _sized(dev, gate_packed, codes, "gate_packed", u8),
+        _sized(dev, gate_scales, 2 * n, "gate_scales", f16), _sized(dev, gate_zeros, n, "gate_zeros", u8),
+        _sized(dev, up_packed, codes, "up_packed", u8), _sized(dev, up_scales, 2 * n, "up_scales", f16),
+        _sized(dev, up_zeros, n, "up_zeros", u8),
         _sized(dev, x, 4 * batch * in_features, "x", torch.float32), _sized(dev, h, 4 * batch * out_features, "h", torch.float32),
         batch, st))
 
 
 def pesti_dequant_i4group(rows, in_features, group, packed, scales, zeros, w_out, stream=None):
     torch, dev, st = _place(stream)
-    return _check("pesti_dequant_i4group", load().pesti_dequant_i4group(
-        rows, in_features, group, *_i4group(dev, torch, rows, in_features, group, packed, scales, zeros),
+    fn, n = load().pesti_dequant_i4group, rows * _groups(in_features, group)
+    return _check("pesti_dequant_i4group", fn(
+        rows, in_features, group, _sized(dev, packed, rows * (in_features // 2), "packed", torch.uint8),
+        _sized(dev, scales, 2 * n, "scales", torch.float16), _sized(dev, zeros, n, "zeros", torch.uint8),
         _sized(dev, w_out, 4 * rows * in_features, "w_out", torch.float32), st))
 
 
@@ -528,7 +560,7 @@ def kv_cache(fmt, layers, pages, page_size, kv_heads, head_dim, k, v, k_scales=N
     c = KvCache(fid, layers, pages, page_size, kv_heads, head_dim, _sized(dev, k, size, "k", values),
                 _sized(dev, v, size, "v", values), _sized(dev, k_scales, 4 * rows, "k_scales", torch.float32),
                 _sized(dev, v_scales, 4 * rows, "v_scales", torch.float32))
-    c.device, c.tensors = dev, (k, v, k_scales, v_scales)
+    c.device, c.tensors, c.address = dev, (k, v, k_scales, v_scales), ctypes.addressof(c)
     return c
 
 
@@ -540,13 +572,18 @@ def kv_table(table, lengths, refs=None, seqs=None, width=None):
         seqs, width = table.shape
     t = KvTable(seqs, width, _sized(dev, table, 4 * seqs * width, "table", torch.int32),
                 _sized(dev, lengths, 4 * seqs, "lengths", torch.int32), _sized(dev, refs, 0, "refs", torch.int32))
-    t.device, t.tensors = dev, (table, lengths, refs)
+    t.device, t.tensors, t.address = dev, (table, lengths, refs), ctypes.addressof(t)
     t.refs_held = refs.numel() if hasattr(refs, "numel") else None
     return t
 
 
 def _kv(dev, cache, table=None):
     """Addresses of the structs, with what they were built for checked against each other and the current device."""
+    try:
+        if cache.device == dev == table.device and (table.refs_held is None or table.refs_held >= cache.pages):
+            return cache.address, table.address
+    except AttributeError:   # a struct filled in by hand, or none
+        pass
     for s in (cache, table):
         if getattr(s, "device", dev) != dev:
             raise ValueError(f"the cache's tensors are on device {s.device}, the current one is {dev}")

@@ -17,6 +17,7 @@ REPO = PKG_DIR.parent
 SRC_DIR = PKG_DIR / "csrc"
 INCLUDE_DIR = REPO / "include"
 LIB_PATH = PKG_DIR / "libpesti.so"
+ARGS_PATH = PKG_DIR / "_tensor_args.so"   # the binding's argument checks (host code)
 ARCH = "gfx950"
 
 # Packed float32 VALU ops are turned off for every device compilation; the
@@ -39,12 +40,27 @@ def sources():
     return sorted(SRC_DIR.glob("*.hip"))
 
 
+def args_command(out: Path):
+    """The host compiler's command for the binding's argument checks, against the installed torch."""
+    import sysconfig
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib = Path(torch.__file__).resolve().parent / "lib"
+    return [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__",
+            *[f"-isystem{p}" for p in (*include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"])],
+            str(SRC_DIR / "tensor_args.cpp"), "-o", str(out), f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
+
+
 def build(verbose: bool = False) -> Path:
-    """Compile every source into libpesti.so (always recompiles)."""
+    """Compile every source into libpesti.so and the binding's argument checks (always recompiles)."""
     objs = []
     obj_dir = PKG_DIR / "_build"
     obj_dir.mkdir(exist_ok=True)
     procs = []
+    args_tmp = ARGS_PATH.with_suffix(".so.tmp")
+    args_src = SRC_DIR / "tensor_args.cpp"
+    procs.append((args_src, subprocess.Popen(args_command(args_tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     for src in sources():
         obj = obj_dir / (src.stem + ".o")
         cmd = [hipcc(), *[f for f in HIP_FLAGS if f != "-shared"], "-c", "-I", str(INCLUDE_DIR),
@@ -66,10 +82,11 @@ def build(verbose: bool = False) -> Path:
     if failed:
         for src, text in failed:
             sys.stderr.write(f"--- {src.name}\n{text}\n")
-        raise RuntimeError("HIP compilation failed")
+        raise RuntimeError("compilation failed")
     tmp = LIB_PATH.with_suffix(".so.tmp")
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", str(tmp), *map(str, objs)]
     subprocess.run(cmd, check=True)
+    os.replace(args_tmp, ARGS_PATH)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 
