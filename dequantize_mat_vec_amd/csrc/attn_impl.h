@@ -107,6 +107,15 @@ __device__ __forceinline__ float both_parts(float hi, float lo) {
   return __builtin_fabsf(hi) == INFINITY ? hi : fmaf(lo, kPart, hi);
 }
 
+// A column's score from its own and the other part, `share` being what its own
+// counts for.  Product, then sum, never one fma: both lanes have to get the same
+// bits, since one keeps the first and the other the second part of its weight.
+__device__ __forceinline__ float joined(float own, float share) {
+#pragma clang fp contract(off)
+  const float p = own * share;
+  return p + other_part(p);
+}
+
 // Four signed bytes as binary16: xor 0x80 makes them 0..255 (code + 128), which
 // over 0x6400 read as 1024 + u.
 __device__ __forceinline__ h2 bytes_h2(uint32_t u, uint32_t sel) {
@@ -286,12 +295,26 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
     for (int f = 0; f < kFrags; ++f) acc[n][f] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
+  // Per lane: what its part of a score counts for (softmax's scale in it), and
+  // how the second part of a weight is made.
+  float share[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) share[n] = second ? factor[n] * kPart : factor[n];
+  const float less = second ? -1.f : 0.f, times = second ? 0x1p11f : 1.f;
+
   const int32_t* row_pages = a.table + seq * a.width;
   const int32_t held = kv_pages_of(a, length);
   const int32_t page_mask = (1 << a.page_shift) - 1;
+  const int32_t first_tile = part * per + wave, last_tile = end - 1;
   int32_t ids[kPages];   // lane i: the pages of the wavefront's i-th tile from here
-  const int32_t first_tile = part * per + wave;
-  for (int32_t tile = first_tile; tile < end; tile += kAttnWaves) {
+
+  // Where a tile lies: rows of the layer's pools that its token 0 would have in
+  // the page of K's tokens (column col) and of V's (lane group g), by half.
+  struct Place {
+    int64_t k_row[2], v_row[2];
+    uint32_t there;   // bit t: token t of the tile is in the cache
+  };
+  auto locate = [&](int32_t tile) {
     const int step = (tile - first_tile) / kAttnWaves & 63;
     if (step == 0) {
 #pragma unroll
@@ -300,12 +323,9 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
         ids[j] = idx < held ? row_pages[idx] : -1;
       }
     }
-    // Pages, and which tokens of the tile there are.
+    Place w;
     const int32_t t0 = tile * kTile, left = length - t0;
-    uint32_t there = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1;
-    // Rows of the layer's pools that the tile's token 0 would have in the page
-    // of K's tokens (column col) and of V's (lane group g), by half.
-    int64_t k_row[2], v_row[2];
+    w.there = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1;
     auto row_in = [&](int32_t page, int first) {
       return page * a.page_rows + (static_cast<int64_t>(kvh) << a.page_shift) + ((t0 + first) & page_mask) - first;
     };
@@ -314,26 +334,28 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
     for (int j = 0; j < kPages; ++j) {
       page[j] = __builtin_amdgcn_readlane(ids[j], step);
       if (!kv_page_ok(a, page[j])) {
-        there &= SMALL ? ~(0xFFu << (8 * j)) : 0u;
+        w.there &= SMALL ? ~(0xFFu << (8 * j)) : 0u;
         page[j] = 0;   // read instead, and not used
       }
     }
-    if (there == 0) continue;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if constexpr (SMALL) {
-        k_row[h] = row_in(second ? page[2 * h + 1] : page[2 * h], 16 * h + (second ? 8 : 0));
-        v_row[h] = row_in(g >= 2 ? page[2 * h + 1] : page[2 * h], 16 * h + (g >= 2 ? 8 : 0));
+        w.k_row[h] = row_in(second ? page[2 * h + 1] : page[2 * h], 16 * h + (second ? 8 : 0));
+        w.v_row[h] = row_in(g >= 2 ? page[2 * h + 1] : page[2 * h], 16 * h + (g >= 2 ? 8 : 0));
       } else {
-        k_row[h] = v_row[h] = row_in(page[0], 0);
+        w.k_row[h] = w.v_row[h] = row_in(page[0], 0);
       }
     }
-
-    // K: token col of each half.
-    u32x4a kw[2][I8 ? (kSteps + 1) / 2 : kSteps];
+    return w;
+  };
+  // K: token col of each half.
+  u32x4a kw[2][I8 ? (kSteps + 1) / 2 : kSteps];
+  f32x4 ks[2], vs[2];
+  auto load_k = [&](const Place& w) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint8_t* r = a.k + k_row[h] * (D * kSize) + (16 * h + col) * (D * kSize);
+      const uint8_t* r = a.k + w.k_row[h] * (D * kSize) + (16 * h + col) * (D * kSize);
       if constexpr (!I8) {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) kw[h][s] = *reinterpret_cast<const u32x4a*>(r + (32 * s + 8 * g) * 2);
@@ -344,25 +366,32 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
           const u32x2a v = *reinterpret_cast<const u32x2a*>(r + 32 * (kSteps - 1) + 8 * g);
           kw[h][kSteps / 2] = u32x4a{v.x, v.y, 0u, 0u};
         }
+        ks[h] = *reinterpret_cast<const f32x4*>(a.k_scales + w.v_row[h] + 16 * h + 4 * g);
       }
     }
-    // V: tokens 4g..4g+3 of each half, in the lane's runs of dimensions.
-    VTile<I8, D> v;
-    f32x4 ks[2], vs[2];
+  };
+  // V: tokens 4g..4g+3 of each half, in the lane's runs of dimensions.
+  VTile<I8, D> vt;
+  auto load_v = [&](const Place& w) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint8_t* r = a.v + v_row[h] * (D * kSize) + (16 * h + 4 * g) * (D * kSize);
+      const uint8_t* r = a.v + w.v_row[h] * (D * kSize) + (16 * h + 4 * g) * (D * kSize);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v.load(4 * h + i, r + i * (D * kSize), col);
-      if constexpr (I8) {
-        ks[h] = *reinterpret_cast<const f32x4*>(a.k_scales + v_row[h] + 16 * h + 4 * g);
-        vs[h] = *reinterpret_cast<const f32x4*>(a.v_scales + v_row[h] + 16 * h + 4 * g);
-      }
+      for (int i = 0; i < 4; ++i) vt.load(4 * h + i, r + i * (D * kSize), col);
+      if constexpr (I8) vs[h] = *reinterpret_cast<const f32x4*>(a.v_scales + w.v_row[h] + 16 * h + 4 * g);
     }
-    const bool whole = there == 0xFFFFFFFFu;
-    uint32_t mine = 0xFFu;   // bit 4h + i: the lane's token is there
-    if (!whole) mine = (there >> (4 * g) & 15u) | (there >> (16 + 4 * g) & 15u) << 4;
+  };
 
+  // K of the next tile is asked for as soon as the scores have used this one's
+  // registers, V after the weighted sums: each is in flight under the other's
+  // half of a step, without a second set of registers.
+  Place at{};
+  if (first_tile <= last_tile) {
+    at = locate(first_tile);
+    load_k(at);
+    load_v(at);
+  }
+  for (int32_t tile = first_tile; tile <= last_tile; tile += kAttnWaves) {
     f32x4 s[NT][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -377,69 +406,78 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
           s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][t], s[n][h], 0, 0, 0);
         }
       }
-    if (!whole) {
+    const uint32_t there = at.there;
+    const bool whole = there == 0xFFFFFFFFu;
+    // bit 4h + i: the lane's token is there
+    const uint32_t mine = (there >> (4 * g) & 15u) | (there >> (16 + 4 * g) & 15u) << 4;
+    float kscale[8];
+    if constexpr (I8) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (!(mine >> j & 1)) v.clear(j);
+      for (int j = 0; j < 8; ++j) kscale[j] = ks[j / 4][j % 4];
     }
-
+    __builtin_amdgcn_sched_barrier(0);
+    at = locate(tile + kAttnWaves <= last_tile ? tile + kAttnWaves : tile);   // (the last one's are loaded again)
+    load_k(at);
+    __builtin_amdgcn_sched_barrier(0);
+    h8 pf[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float x[8], w[8];
-      float now, add;
-      auto weigh = [&](bool careful) {
-        float top = -INFINITY;
+      float x[8], e[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float own = s[n][j / 4][j % 4], oth = other_part(own);
-          float t;
-          if (careful) t = second ? both_parts(oth, own) : both_parts(own, oth);
-          else t = second ? fmaf(own, kPart, oth) : fmaf(oth, kPart, own);
-          t *= factor[n];
-          if constexpr (I8) t *= ks[j / 4][j % 4];
-          if (!whole) t = mine >> j & 1 ? t : -INFINITY;
-          x[j] = t;
-          top = fmaxf(top, t);
+      for (int j = 0; j < 8; ++j) {
+        x[j] = joined(s[n][j / 4][j % 4], share[n]);
+        if constexpr (I8) x[j] *= kscale[j];
+      }
+      float now, add;
+      auto weigh = [&]() {
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = mine >> j & 1 ? x[j] : -INFINITY;
         }
+        const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
         now = fmaxf(most[n], column_max(top));
         const float base = now == -INFINITY ? 0.f : now;
         add = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          w[j] = __builtin_amdgcn_exp2f(x[j] - base);
-          add += w[j];
+          e[j] = __builtin_amdgcn_exp2f(x[j] - base);
+          add += e[j];
         }
       };
-      weigh(false);
-      if (__any(add != add)) weigh(true);   // an infinity of K or q, or a NaN
-      sum[n] = now > most[n] ? sum[n] * __builtin_amdgcn_exp2f(most[n] - now) + add : sum[n] + add;
-      float old = 1.f;   // what y so far is to be scaled by
-      bool moved;
-      if constexpr (!I8) {
-        moved = now > most[n];
-        if (moved) old = __builtin_amdgcn_exp2f(most[n] - now);
+      weigh();
+      if (__any(add != add)) {   // an infinity of K or q, whose second parts' products are of any kind, or a NaN
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] *= 0x1p14f;
-      } else {
+        for (int j = 0; j < 8; ++j) {
+          const float own = s[n][j / 4][j % 4], oth = other_part(own);
+          x[j] = (second ? both_parts(oth, own) : both_parts(own, oth)) * factor[n];
+          if constexpr (I8) x[j] *= kscale[j];
+        }
+        weigh();
+      }
+      const bool higher = now > most[n];
+      const float down = higher ? __builtin_amdgcn_exp2f(most[n] - now) : 1.f;
+      sum[n] = fmaf(sum[n], down, add);
+      float old = down;   // what y so far is to be scaled by
+      float lift = 0x1p14f;
+      bool moved = higher;
+      if constexpr (I8) {
         // The weights of the codes are p times the token's scale: y is held
         // relative to the largest of them, 2^ref, as p is to the maximum.
         float top = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          w[j] *= vs[j / 4][j % 4];
-          if (!whole) w[j] = mine >> j & 1 ? w[j] : 0.f;
-          top = fmaxf(top, __builtin_fabsf(w[j]));
+          e[j] *= vs[j / 4][j % 4];
+          if (!whole) e[j] = mine >> j & 1 ? e[j] : 0.f;
+          top = fmaxf(top, __builtin_fabsf(e[j]));
         }
         top = column_max(top);
-        const float r = now > most[n] && most[n] > -INFINITY ? ref[n] + (most[n] - now) : ref[n];
+        const float r = higher && most[n] > -INFINITY ? ref[n] + (most[n] - now) : ref[n];
         const float need = static_cast<float>(static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 127 - 13);
         const float to = fmaxf(fmaxf(need, r), -126.f);
         moved = to > r;
-        if (moved) old = __builtin_amdgcn_exp2f(r - to);
+        old = moved ? __builtin_amdgcn_exp2f(r - to) : 1.f;
         ref[n] = to;
-        const float lift = __builtin_amdgcn_exp2f(-to);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] *= lift;
+        lift = __builtin_amdgcn_exp2f(-to);
       }
       most[n] = now;
       if (__any(moved)) {
@@ -448,13 +486,27 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[n][f][i] *= old;
       }
-      h8 pf;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) pf[j] = part_of(w[j], second);
-      // V's operands are formed again for a second head tile rather than held
-#pragma unroll
-      for (int f = 0; f < kFrags; ++f) acc[n][f] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v.frag(f), pf, acc[n][f], 0, 0, 0);
+      for (int j = 0; j < 8; ++j) {   // first part: the weight; second: what its rounding leaves
+        const float v = e[j] * lift;
+        const _Float16 hi = static_cast<_Float16>(v);
+        pf[n][j] = static_cast<_Float16>(fmaf(static_cast<float>(hi), less, v) * times);
+      }
     }
+    if (!whole) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!(mine >> j & 1)) vt.clear(j);
+    }
+    // V's operands are formed again for a second head tile rather than held
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f)
+        acc[n][f] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vt.frag(f), pf[n], acc[n][f], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_v(at);
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   // Join the wavefronts: y relative to the workgroup's maximum.
