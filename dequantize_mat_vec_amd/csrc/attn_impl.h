@@ -49,6 +49,7 @@ struct AttnArgs {
   int32_t group;           // query heads per KV head
   int32_t head_blocks;     // workgroups per KV head
   int32_t splits;
+  int32_t part_tiles;      // tiles of a part
   int32_t q_f32, y_f32;
 };
 
@@ -56,10 +57,13 @@ constexpr int kAttnWaves = 4;
 constexpr int kTile = 32;            // tokens of one step of a wavefront
 constexpr int kMinPartTiles = 8;     // a workgroup's part of a sequence is at least two steps of each wavefront
 
-// Tiles per part, and parts, of a sequence of `length` tokens.
-__device__ __forceinline__ int32_t attn_part_tiles(int32_t length, int32_t splits) {
+// Tiles per part, and parts, of a sequence of `length` tokens.  Parts of all
+// sequences have one size, so that workgroups of a batch of uneven lengths
+// finish together (48 sequences up to 8191 in 8 bits, the same number of parts
+// each: 107 us); only a sequence past the caller's bound has larger ones.
+__device__ __forceinline__ int32_t attn_part_tiles(int32_t length, int32_t splits, int32_t part_tiles) {
   const int32_t tiles = (length + kTile - 1) / kTile, per = (tiles + splits - 1) / splits;
-  return per > kMinPartTiles ? per : kMinPartTiles;
+  return per > part_tiles ? per : part_tiles;
 }
 __device__ __forceinline__ int32_t attn_parts(int32_t length, int32_t per) {
   return ((length + kTile - 1) / kTile + per - 1) / per;
@@ -216,11 +220,23 @@ __device__ __forceinline__ constexpr int k_dim(int s, int steps, int g) {
 
 #endif  // __HIP_DEVICE_COMPILE__
 
-// One workgroup: the NT * 8 query heads of block blockIdx.y of a KV head, part
-// blockIdx.x of row blockIdx.z's sequence.  SMALL: pages of 8 or 16 tokens, up
+// Wavefronts per SIMD that the registers are to leave room for.  Stated, since
+// the compiler left to itself adds accumulator registers up to two wavefronts'
+// share where three fit (8 bits, D 128: 113 -> 107 us).
+constexpr int attn_waves(bool i8, int d, int nt, bool small) {
+  return d * nt <= 64 ? 4 : (d * nt <= (i8 || !small ? 128 : 96) ? 3 : (d * nt <= 192 ? 2 : 1));
+}
+
+// One workgroup: the NT * 8 query heads of block blockIdx.x of a KV head, a part
+// of row blockIdx.z's sequence.  Workgroups go to the 8 XCDs in turn: heads, which
+// have equal work, lie next to each other, and a row's parts, of which short
+// sequences lack the last ones, start at another place in each row (48 sequences
+// up to 8191 in 8 parts, the part first and unrotated: 136 us, the last parts'
+// XCDs idle).  SMALL: pages of 8 or 16 tokens, up
 // to four in a tile; else a tile lies in one page.
 template <bool I8, int D, int NT, bool SMALL>
-__global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
+__global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu(attn_waves(I8, D, NT, SMALL))))
+void attn_kernel(AttnArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int kSteps = D / 32, kFrags = D / 16, kSize = I8 ? 1 : 2, kPages = SMALL ? 4 : 1;
   __shared__ float joint[kAttnWaves][8 * NT][D];
@@ -230,14 +246,14 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
   const int col = lane & 15, g = lane >> 4;
   const bool second = col >= 8;
   const int64_t row = blockIdx.z;
-  const int kvh = blockIdx.y / p.head_blocks, hb = blockIdx.y % p.head_blocks;
+  const int kvh = blockIdx.x / p.head_blocks, hb = blockIdx.x % p.head_blocks;
   const int head0 = hb * 8 * NT, heads_here = p.group - head0 < 8 * NT ? p.group - head0 : 8 * NT;
   const int64_t first_head = static_cast<int64_t>(kvh) * p.group + head0;
 
   int64_t seq;
   const int32_t length = attn_length(p, row, &seq);
-  const int32_t per = attn_part_tiles(length, p.splits), parts = attn_parts(length, per);
-  const int32_t part = blockIdx.x;
+  const int32_t per = attn_part_tiles(length, p.splits, p.part_tiles), parts = attn_parts(length, per);
+  const int32_t part = static_cast<int32_t>((blockIdx.y + blockIdx.z) % static_cast<uint32_t>(p.splits));
   if (part >= parts && part > 0) return;   // (a sequence without tokens: part 0 writes the zeros)
   const int32_t tiles = (length + kTile - 1) / kTile;
   const int32_t end = part * per + per < tiles ? part * per + per : tiles;
@@ -366,11 +382,11 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
           const u32x2a v = *reinterpret_cast<const u32x2a*>(r + 32 * (kSteps - 1) + 8 * g);
           kw[h][kSteps / 2] = u32x4a{v.x, v.y, 0u, 0u};
         }
-        ks[h] = *reinterpret_cast<const f32x4*>(a.k_scales + w.v_row[h] + 16 * h + 4 * g);
       }
     }
   };
-  // V: tokens 4g..4g+3 of each half, in the lane's runs of dimensions.
+  // V: tokens 4g..4g+3 of each half, in the lane's runs of dimensions, and both
+  // scales of those tokens.
   VTile<I8, D> vt;
   auto load_v = [&](const Place& w) {
 #pragma unroll
@@ -378,7 +394,10 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
       const uint8_t* r = a.v + w.v_row[h] * (D * kSize) + (16 * h + 4 * g) * (D * kSize);
 #pragma unroll
       for (int i = 0; i < 4; ++i) vt.load(4 * h + i, r + i * (D * kSize), col);
-      if constexpr (I8) vs[h] = *reinterpret_cast<const f32x4*>(a.v_scales + w.v_row[h] + 16 * h + 4 * g);
+      if constexpr (I8) {
+        ks[h] = *reinterpret_cast<const f32x4*>(a.k_scales + w.v_row[h] + 16 * h + 4 * g);
+        vs[h] = *reinterpret_cast<const f32x4*>(a.v_scales + w.v_row[h] + 16 * h + 4 * g);
+      }
     }
   };
 
@@ -410,11 +429,6 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
     const bool whole = there == 0xFFFFFFFFu;
     // bit 4h + i: the lane's token is there
     const uint32_t mine = (there >> (4 * g) & 15u) | (there >> (16 + 4 * g) & 15u) << 4;
-    float kscale[8];
-    if constexpr (I8) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) kscale[j] = ks[j / 4][j % 4];
-    }
     __builtin_amdgcn_sched_barrier(0);
     at = locate(tile + kAttnWaves <= last_tile ? tile + kAttnWaves : tile);   // (the last one's are loaded again)
     load_k(at);
@@ -426,7 +440,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         x[j] = joined(s[n][j / 4][j % 4], share[n]);
-        if constexpr (I8) x[j] *= kscale[j];
+        if constexpr (I8) x[j] *= ks[j / 4][j % 4];
       }
       float now, add;
       auto weigh = [&]() {
@@ -450,7 +464,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(AttnArgs p) {
         for (int j = 0; j < 8; ++j) {
           const float own = s[n][j / 4][j % 4], oth = other_part(own);
           x[j] = (second ? both_parts(oth, own) : both_parts(own, oth)) * factor[n];
-          if constexpr (I8) x[j] *= kscale[j];
+          if constexpr (I8) x[j] *= ks[j / 4][j % 4];
         }
         weigh();
       }
@@ -576,7 +590,7 @@ int launch(const pesti::AttnArgs& p, int64_t rows, hipStream_t st) {
   pesti::AttnArgs args = p;
   void* params[] = {&args};
   return pesti_kv::launch(reinterpret_cast<const void*>(&pesti::attn_kernel<I8, D, NT, SMALL>),
-                          dim3(static_cast<unsigned>(p.splits), static_cast<unsigned>(p.kv.kv_heads * p.head_blocks),
+                          dim3(static_cast<unsigned>(p.kv.kv_heads * p.head_blocks), static_cast<unsigned>(p.splits),
                                static_cast<unsigned>(rows)),
                           dim3(64 * pesti::kAttnWaves), params, 0, st);
 }

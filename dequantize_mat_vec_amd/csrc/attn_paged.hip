@@ -6,6 +6,7 @@
 namespace pesti {
 
 constexpr int kMaxParts = 256;
+constexpr int kManyRows = 16;
 
 // y of one row and head from its parts, in part order: part i counts 2^(max_i -
 // max) times.  D4: head_dim / 4 rounded up to a power of two; as many threads
@@ -18,7 +19,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
   const int64_t row = blockIdx.y, slot0 = (row * p.heads + blockIdx.x) * p.splits;
   int64_t seq;
   const int32_t length = attn_length(p, row, &seq);
-  const int32_t parts = attn_parts(length, attn_part_tiles(length, p.splits));
+  const int32_t parts = attn_parts(length, attn_part_tiles(length, p.splits, p.part_tiles));
   if (parts <= 1) return;   // written already
   float m = -INFINITY, l = 0.f;
   if (tid < parts) {
@@ -82,8 +83,11 @@ int check(const pesti_kv_cache* cache, int64_t rows, int64_t heads, int64_t max_
 }
 
 // Workgroups per KV head, and parts that a sequence of up to max_length tokens
-// is split into: as many as bring the launch to about four workgroups a compute
-// unit, none of under kMinPartTiles tiles.
+// is split into, none of under kMinPartTiles tiles.  Few rows: about four
+// workgroups a compute unit, all resident at once (one row of 131071 binary16
+// tokens, 8 KV heads of 128: 104 us so, 111 at nine).  Many rows, whose lengths
+// differ: about nine, so that what ends early makes room (48 rows up to 8191 in 8
+// bits: 102 us so, 106 at four).
 int64_t head_blocks(const pesti_kv_cache* cache, int64_t heads) {
   const int64_t group = heads / cache->kv_heads, each = 8 * pesti_attn::head_tiles(group, cache->head_dim);
   return (group + each - 1) / each;
@@ -91,7 +95,8 @@ int64_t head_blocks(const pesti_kv_cache* cache, int64_t heads) {
 int64_t splits_of(const pesti_kv_cache* cache, int64_t rows, int64_t heads, int64_t max_length) {
   const int64_t base = rows * cache->kv_heads * head_blocks(cache, heads);
   const int64_t most = (max_length + pesti::kTile * pesti::kMinPartTiles - 1) / (pesti::kTile * pesti::kMinPartTiles);
-  int64_t s = base > 0 ? (1024 + base - 1) / base : 1;
+  const int64_t target = rows >= pesti::kManyRows ? 2304 : 1024;
+  int64_t s = base > 0 ? (target + base - 1) / base : 1;
   s = s < most ? s : most;
   return s < pesti::kMaxParts ? s : pesti::kMaxParts;
 }
@@ -162,6 +167,8 @@ int pesti_attn_paged(const pesti_kv_cache* cache, const pesti_kv_table* table, i
   p.group = static_cast<int32_t>(heads / cache->kv_heads);
   p.head_blocks = static_cast<int32_t>(head_blocks(cache, heads));
   p.splits = static_cast<int32_t>(splits);
+  const int64_t tiles = (max_length + pesti::kTile - 1) / pesti::kTile, part = (tiles + splits - 1) / splits;
+  p.part_tiles = static_cast<int32_t>(part > pesti::kMinPartTiles ? part : pesti::kMinPartTiles);
   p.q_f32 = q_format == PESTI_FMT_F32;
   p.y_f32 = y_format == PESTI_FMT_F32;
   const hipStream_t sh = static_cast<hipStream_t>(stream);
