@@ -9,6 +9,9 @@ of the C ABI, so a step is 97 dependent launches (--grouping none: 169).  Weight
 is not available), resident in HBM; two copies of the step's weights are
 alternated so that the 256 MB last-level cache cannot hold a step's bytes.
 
+With --context the step also holds what stands between the mat-vecs: K and V
+appended to a paged cache and the attention over it, in every layer.
+
 Prints one JSON line: HBM GB/s over the step (nominal algorithmic bytes per
 step / time per step), microseconds per step, the roofline of the dominant
 kernel (the kernel with the most time per step, timed by replaying a graph
@@ -59,6 +62,12 @@ def parse_args(argv=None):
     p.add_argument("--ffn", choices=("separate", "swiglu"), default="separate",
                    help="gate and up as two mat-vecs (the 169-call step) or one fused launch "
                         "writing silu(gate) * up, which the down projection then reads")
+    p.add_argument("--context", type=int, default=None, metavar="TOKENS",
+                   help="put the attention between Q/K/V and O into the step: every layer appends its K and V "
+                        "to a paged cache that holds TOKENS tokens at the start and grows by one a step, and O "
+                        "reads the attention's result")
+    p.add_argument("--cache-format", choices=("f16", "i8row"), default="f16",
+                   help="values of the cache that --context asks for")
     p.add_argument("--kernel-steps", type=int, default=20,
                    help="replays of each per-kernel graph (per-kernel times)")
     p.add_argument("--no-cpu-baseline", action="store_true")
@@ -70,7 +79,7 @@ def parse_args(argv=None):
                    help="skip the oracle check of the step's sampled outputs before timing")
     p.add_argument("--suite", action="store_true",
                    help="instead of the decode step, time every other workload (int8, Q4_K FFN, "
-                        "f16 GEMM, LM-head sweep) and print one JSON line per case")
+                        "f16 GEMM, LM-head sweep, 4-bit with group scales) and print one JSON line per case")
     p.add_argument("--launch-floor", action="store_true",
                    help="instead of the decode step, time graphs of 96 dependent batch-1 Q4_K "
                         "mat-vec launches (896 columns, 1 to 4864 rows) and of 96 one-element "
@@ -157,13 +166,103 @@ def plan_launches(calls, grouping):
     return launches
 
 
-def make_step(lib, calls, launches, weights, xs, ys, biases, ffn="separate"):
+CACHE_PAGE_SIZE = 64
+
+
+def context_bytes(context, fmt):
+    """Bytes that one step's attention reads of a cache of `context` tokens, all layers: K and V, with their scales."""
+    from dequantize_mat_vec_amd import synth
+    per_head = synth.QWEN_HEAD_DIM * 2 if fmt == "f16" else synth.QWEN_HEAD_DIM + 4
+    return synth.QWEN_LAYERS * 2 * context * synth.QWEN_KV_HEADS * per_head
+
+
+class StepCache:
+    """The decode step's key-value cache: one sequence on pages in a shuffled order, filled with `context`
+    tokens of N(0, 1) values, with pages for `steps` more.  begin()
+    takes a place for the step's token; layer(i) appends what the layer's K and V calls wrote and attends with
+    what its Q call wrote, into the x of its O call.  Everything a call needs is on the device, so a captured
+    step grows the cache at each replay."""
+
+    def __init__(self, lib, context, fmt, steps, calls, xs, ys):
+        import math
+        import torch
+        import dequantize_mat_vec_amd as dmv
+        from dequantize_mat_vec_amd import synth
+        self.lib, self.heads = lib, synth.QWEN_HEADS
+        self.max_length = context + steps
+        layers, kvh, d = 1 + max(c[0] for c in calls if c[1] == "k"), synth.QWEN_KV_HEADS, synth.QWEN_HEAD_DIM
+        pages = max(1, -(-self.max_length // CACHE_PAGE_SIZE))
+        dev = torch.device("cuda:0")
+        shape = (layers, pages, kvh, CACHE_PAGE_SIZE, d)
+        self.k, self.v = (torch.zeros(shape, dtype=torch.float16 if fmt == "f16" else torch.int8, device=dev) for _ in range(2))
+        self.k_scales, self.v_scales = ((torch.zeros(shape[:-1], device=dev) for _ in range(2)) if fmt == "i8row" else (None, None))
+        self.cache = dmv.kv_cache(fmt, layers, pages, CACHE_PAGE_SIZE, kvh, d, self.k, self.v, self.k_scales, self.v_scales)
+        self.lengths = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        # the pages that the first tokens lie in, in an order such as sequences that came and went leave
+        order = torch.from_numpy(synth.rng_for(CONFIG_INDEX, 0, 300).permutation(pages)).to(dev)
+        self.pages = torch.full((1, pages), -1, dtype=torch.int32, device=dev)
+        refs = torch.zeros(pages, dtype=torch.int32, device=dev)
+        self.table = dmv.kv_table(self.pages, self.lengths, refs)
+        held = -(-context // CACHE_PAGE_SIZE)
+        self.pages[0, :held] = order[:held].to(torch.int32)
+        refs[order[:held]] = 1
+        self.lengths.fill_(context)
+        gen = torch.Generator(device=dev).manual_seed(CONFIG_INDEX)
+        for at in range(0, context, 65536):
+            n = min(65536, context - at)
+            positions = torch.arange(at, at + n, dtype=torch.int32, device=dev)
+            first = torch.zeros(n, dtype=torch.int32, device=dev)
+            for layer in range(layers):
+                kv = torch.randn(2, n, kvh * d, device=dev, generator=gen)
+                dmv.pesti_cache_append(self.cache, self.table, layer, n, kv[0], kv[1], seq_ids=first, positions=positions)
+        need = dmv.pesti_attn_paged_workspace_bytes(self.cache, 1, self.heads, self.max_length)
+        self.workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        index = {(c[0], c[1]): i for i, c in enumerate(calls)}
+        self.args = []
+        f32 = dmv.VALUE_FORMAT_IDS["f32"]
+        for i in range(layers):
+            q, k, v, x = (ys[index[i, "q"]], ys[index[i, "k"]], ys[index[i, "v"]], xs[index[i, "o"]])
+            self.args.append(((i, 1, f32, k.data_ptr(), v.data_ptr(), kvh * d, None, None),
+                              (i, 1, self.heads, None, f32, q.data_ptr(), self.heads * d, f32, x.data_ptr(), 1 / math.sqrt(d),
+                               self.max_length, self.workspace.data_ptr(), need)))
+
+    def _check(self, what, status):
+        if status != 0:
+            raise RuntimeError(f"{what} failed with status {status}")
+
+    def begin(self, sh):
+        self._check("cache extend", self.lib.pesti_cache_extend(self.cache.address, self.table.address, 1, None, None,
+                                                                self.status.data_ptr(), sh))
+
+    def layer(self, i, sh):
+        append, attend = self.args[i]
+        self._check("cache append", self.lib.pesti_cache_append(self.cache.address, self.table.address, *append, sh))
+        self._check("attention", self.lib.pesti_attn_paged(self.cache.address, self.table.address, *attend, sh))
+
+    def sample(self, layers, calls, xs, ys):
+        """What the parity check needs of the step just run: pools, table, length, q, k, v and the result of some layers."""
+        index = {(c[0], c[1]): i for i, c in enumerate(calls)}
+        out = {"cache_layers": [i for i in layers if i < len(self.args)], "cache_length": int(self.lengths.item()),
+               "cache_status": int(self.status.item()), "cache_table": self.pages[0].cpu().numpy()}
+        for i in out["cache_layers"]:
+            for name, t in (("k_pool", self.k[i]), ("v_pool", self.v[i]), ("q", ys[index[i, "q"]]), ("k", ys[index[i, "k"]]),
+                            ("v", ys[index[i, "v"]]), ("y", xs[index[i, "o"]])):
+                out[f"cache_{name}_{i}"] = t.cpu().numpy()
+            if self.k_scales is not None:
+                out[f"cache_k_scales_{i}"] = self.k_scales[i].cpu().numpy()
+                out[f"cache_v_scales_{i}"] = self.v_scales[i].cpu().numpy()
+        return out
+
+
+def make_step(lib, calls, launches, weights, xs, ys, biases, ffn="separate", cache=None):
     """A function issuing the step's launches on a stream handle; the op
     tables are built once so a step is only the C calls.  With ffn
     "swiglu" each layer's gate/up launch is the fused pesti_gemv_swiglu,
     writing h = silu(gate) * up into the gate call's output buffer, and the
     down projection reads h as its x (the step's data dependence in a
-    model)."""
+    model).  With a StepCache the step begins with it, and a layer's
+    attention follows the launch that writes its V."""
     import ctypes
     from dequantize_mat_vec_amd import _lib
     h_of_layer = {}
@@ -196,11 +295,18 @@ def make_step(lib, calls, launches, weights, xs, ys, biases, ffn="separate"):
         plans.append(plan)
     fn = lib.pesti_gemv_group
     fn_swiglu = lib.pesti_gemv_swiglu
+    attends = {} if cache is None else {li: calls[idx[-1]][0] for li, (_, idx) in enumerate(launches)
+                                        if calls[idx[-1]][1] == "v"}
 
     def step(copy, stream_handle, only=None):
-        """One step (or, with `only`, just the launches whose indices are in it)."""
+        """One step (or, with `only`, just the launches whose indices are in it; "cache": those of the cache)."""
+        caching = cache is not None and (only is None or "cache" in only)
+        if caching:
+            cache.begin(stream_handle)
         for idx, (kind, a) in enumerate(plans[copy]):
             if only is not None and idx not in only:
+                if caching and idx in attends:
+                    cache.layer(attends[idx], stream_handle)
                 continue
             if kind == "group":
                 st = fn(a[0], a[1], a[2], 1, stream_handle)
@@ -209,6 +315,8 @@ def make_step(lib, calls, launches, weights, xs, ys, biases, ffn="separate"):
                 st = fn_swiglu(fid, out, inf, wg, wu, None, None, x, h, 1, stream_handle)
             if st != 0:
                 raise RuntimeError(f"launch {idx} failed with status {st}")
+            if caching and idx in attends:
+                cache.layer(attends[idx], stream_handle)
     return step
 
 
@@ -284,6 +392,11 @@ def suite_cases():
     cases += [("q4_k_stream lm-head 151936x896 b1", "gemv", ("q4_k_stream", synth.QWEN_VOCAB, 896, 1)),
               ("q4_k_stream 4864x896 b1 (gate/up)", "gemv", ("q4_k_stream", 4864, 896, 1)),
               ("q4_k_stream 4864x896 b1 (gate/up) x8 grouped", "group", ("q4_k_stream", 4864, 896, 8))]
+    # 4-bit weights with a scale and a zero point per 128
+    for b in (1, 2, 4, 8):
+        cases.append((f"i4group128 lm-head 151936x896 b{b}", "gemv4", (128, synth.QWEN_VOCAB, 896, b)))
+    cases += [("i4group128 4864x896 b1 (gate/up)", "gemv4", (128, 4864, 896, 1)),
+              ("i4group128 896x4864 b1 (down)", "gemv4", (128, 896, 4864, 1))]
     return cases
 
 
@@ -310,6 +423,15 @@ def suite_case_inputs(idx, name, kind, prm, rows_limit=None):
         d.update(fmt=fmt, out=out, inf=inf, batch=batch, packed=packed, scales=scales,
                  x=synth.activations(rng, batch, inf), algo=call_bytes(fmt, out, inf, batch, False),
                  flops=2.0 * out * inf * batch)
+    elif kind == "gemv4":
+        group, out, inf, batch = prm
+        out = out if rows_limit is None else min(out, rows_limit)
+        packed, scales, zeros = synth.i4group(rng, out, inf, group)
+        # one buffer of codes, scales and zero points, so that a weight copy holds all three
+        d.update(group=group, out=out, inf=inf, batch=batch, codes=packed, scales=scales, zeros=zeros,
+                 packed=np.concatenate([packed.reshape(-1), scales.view(np.uint8).reshape(-1), zeros.reshape(-1)]),
+                 x=synth.activations(rng, batch, inf),
+                 algo=packed.size + 3 * scales.size + 4 * batch * (inf + out), flops=2.0 * out * inf * batch)
     elif kind == "qgemm":
         fmt, m, n, k = prm
         n = n if rows_limit is None else min(n, rows_limit)
@@ -363,6 +485,11 @@ def run_suite(lib, args):
             x = torch.from_numpy(inp["x"]).to(dev)
             y = torch.empty(batch * out, dtype=torch.float32, device=dev)
             sc = torch.from_numpy(inp["scales"]).to(dev) if inp["scales"] is not None else None
+        elif kind == "gemv4":
+            group, out, inf, batch = inp["group"], inp["out"], inp["inf"], inp["batch"]
+            at_scales, at_zeros = inp["codes"].size, inp["codes"].size + 2 * inp["scales"].size
+            x = torch.from_numpy(inp["x"]).to(dev)
+            y = torch.empty(batch * out, dtype=torch.float32, device=dev)
         else:
             if kind == "qgemm":
                 fmt = inp["fmt"]
@@ -400,6 +527,10 @@ def run_suite(lib, args):
                       if fmt in ("i8row", "i4row") else
                       getattr(lib, f"pesti_gemv_{fmt}")(out, inf, ws[i % copies].data_ptr(),
                                                        x.data_ptr(), y.data_ptr(), None, batch, sh))
+            elif kind == "gemv4":
+                w = ws[i % copies].data_ptr()
+                st = lib.pesti_gemv_i4group(out, inf, group, w, w + at_scales, w + at_zeros, x.data_ptr(), y.data_ptr(), None,
+                                            batch, sh)
             else:
                 st = lib.pesti_gemm_smallm_ws(gfid, m, n, k, ws[i % copies].data_ptr(), x16.data_ptr(),
                                               y.data_ptr(), b.data_ptr(), gws.data_ptr(), ws_bytes, sh)
@@ -480,9 +611,9 @@ def suite_oracle_leg(filt):
     for idx, (name, kind, prm) in enumerate(suite_cases()):
         if filt and not any(f in name for f in filt.split(",")):
             continue
-        full = {"group": prm[1], "gemv": prm[1], "qgemm": prm[2], "gemm": prm[2]}[kind]
+        full = {"group": prm[1], "gemv": prm[1], "gemv4": prm[1], "qgemm": prm[2], "gemm": prm[2]}[kind]
         inp = suite_case_inputs(idx, name, kind, prm, SUITE_ORACLE_ROWS)
-        rows = {"group": "out", "gemv": "out"}.get(kind, "n")
+        rows = {"group": "out", "gemv": "out", "gemv4": "out"}.get(kind, "n")
         timed_rows = inp[rows]
 
         def once():
@@ -493,6 +624,8 @@ def suite_oracle_leg(filt):
             elif kind == "gemv":
                 oracle.gemv_packed(inp["fmt"], inp["packed"], inp["out"], inp["inf"], inp["x"], None,
                                    inp["scales"])
+            elif kind == "gemv4":
+                oracle.gemv_i4group(inp["codes"], inp["out"], inp["inf"], inp["group"], inp["scales"], inp["zeros"], inp["x"])
             elif kind == "qgemm":
                 oracle.gemm_packed(inp["fmt"], inp["packed"], inp["n"], inp["k"], inp["x16"], inp["bias"])
             else:
@@ -772,20 +905,61 @@ def parity_leg(path):
         if np.any(bad):
             failures.append(f"{name}{layer} ({fmt} {out}x{inf}): {int(bad.sum())} rows, "
                             f"first row {int(rows[np.argmax(bad)])}")
+    if "cache_layers" in data.files:
+        n, bad, most = cache_parity(data)
+        n_out, worst, failures = n_out + n, max(worst, most), failures + bad
     return {"ok": not failures, "calls": int(len(data["calls"])), "outputs": n_out,
             "worst_err_over_bound": round(worst, 4), "failures": failures[:8]}
 
 
-def run_parity(calls, ys, skip_names=(), layout="rows"):
-    """parity_sample() in this process, the check in a child process (the
-    oracle runs only in the CPU leg)."""
+def cache_parity(data):
+    """The sampled layers' attention against the oracle over the pools as read back (1e-4 * sum p|v| + 1e-6), and
+    the step's own token there against what its K and V calls wrote, rounded to the cache's format.
+    (outputs, failures, worst error over its bound)"""
+    import numpy as np
+    from dequantize_mat_vec_amd import synth
+    import oracle
+    n_out, failures, worst = 0, [], 0.0
+    length, table, d = int(data["cache_length"]), data["cache_table"], synth.QWEN_HEAD_DIM
+    if int(data["cache_status"]) != 0 or length < 1:
+        return 0, [f"cache: status {int(data['cache_status'])}, {length} tokens"], np.inf
+    group = synth.QWEN_HEADS // synth.QWEN_KV_HEADS
+    for i in data["cache_layers"]:
+        q, y = data[f"cache_q_{i}"].reshape(-1, d), data[f"cache_y_{i}"].reshape(-1, d).astype(np.float64)
+        for g in range(synth.QWEN_KV_HEADS):
+            rows = {}
+            for name in ("k", "v"):
+                pool, scales = data[f"cache_{name}_pool_{i}"], data.get(f"cache_{name}_scales_{i}")
+                rows[name] = oracle.cached_rows(pool, scales, table, length, g)
+                new = data[f"cache_{name}_{i}"].reshape(-1, d)[g]
+                if scales is None:
+                    want = new.astype(np.float16).astype(np.float64)
+                else:
+                    codes, s = oracle.quantize_i8token(new[None])
+                    want = codes[0] * s.astype(np.float64)[0]
+                if not np.array_equal(rows[name][-1], want):
+                    failures.append(f"cache: layer {i}, KV head {g}: the step's {name.upper()} is not in its place")
+            for h in range(g * group, (g + 1) * group):
+                y_ref, size = oracle.attend(q[h], rows["k"], rows["v"], d ** -0.5)
+                ratio = np.abs(y[h] - y_ref) / (GEMV_REL * size + 1e-6)
+                n_out += d
+                worst = max(worst, float(np.max(np.where(np.isfinite(ratio), ratio, np.inf))))
+                if not np.all(ratio <= 1.0):
+                    failures.append(f"attention: layer {i}, head {h}")
+    return n_out, failures, worst
+
+
+def run_parity(calls, ys, skip_names=(), layout="rows", extra=None):
+    """parity_sample() in this process (and `extra`, what StepCache.sample
+    gave), the check in a child process (the oracle runs only in the CPU
+    leg)."""
     import tempfile
     import numpy as np
     sample = parity_sample(calls, ys, skip_names)
     fd, path = tempfile.mkstemp(suffix=".npz")
     os.close(fd)
     try:
-        arrays = {"calls": np.array(sorted(sample), dtype=np.int64), "layout": np.array(layout)}
+        arrays = {"calls": np.array(sorted(sample), dtype=np.int64), "layout": np.array(layout), **(extra or {})}
         for i, (rows, y) in sample.items():
             arrays[f"rows_{i}"] = rows
             arrays[f"y_{i}"] = y
@@ -903,6 +1077,9 @@ def main(argv=None):
         print(f"bench.py measures one GPU only: --gpus {args.gpus} is not supported "
               "(the decode-step mat-vec runs on a single MI355X)", file=sys.stderr)
         return 2
+    if args.context is not None and not 0 <= args.context <= 1 << 20:
+        print("--context takes 0 to 1048576 tokens", file=sys.stderr)
+        return 2
 
     import torch
     import dequantize_mat_vec_amd as dmv
@@ -921,8 +1098,15 @@ def main(argv=None):
     from dequantize_mat_vec_amd import synth
     calls, weights, xs, ys, biases = build_inputs(args.copies, synth.decode_step_calls(layout=args.layout))
     launches = plan_launches(calls, args.grouping)
-    step = make_step(lib, calls, launches, weights, xs, ys, biases, args.ffn)
+    cache = None
+    if args.context is not None:
+        # each run of a step takes one token's place: eager ones, the parity check's, warm-up and timed ones, and the
+        # cache's launches alone
+        cache = StepCache(lib, args.context, args.cache_format, args.steps + args.warmup + args.kernel_steps + 16, calls, xs, ys)
+    step = make_step(lib, calls, launches, weights, xs, ys, biases, args.ffn, cache)
     bytes_per_step = sum(call_bytes(fmt, out, inf, 1, hb) for _, _, fmt, out, inf, hb in calls)
+    if cache is not None:
+        bytes_per_step += context_bytes(args.context, args.cache_format)
     stream = torch.cuda.Stream()
     sh = stream.cuda_stream
 
@@ -969,7 +1153,11 @@ def main(argv=None):
             torch.cuda.synchronize()
             # with the fused SwiGLU the gate buffer holds h and the down
             # projection reads it: those calls are checked by the test suite
-            parity = run_parity(calls, ys, ("gate", "up", "down") if args.ffn == "swiglu" else (), args.layout)
+            skip = ("gate", "up", "down") if args.ffn == "swiglu" else ()
+            extra = None
+            if cache is not None:   # O reads the attention's result, which is checked instead
+                skip, extra = skip + ("o",), cache.sample(PARITY_LAYERS, calls, xs, ys)
+            parity = run_parity(calls, ys, skip, args.layout, extra)
         t0 = time.perf_counter()
         for i in range(args.steps):
             run(i)
@@ -988,8 +1176,8 @@ def main(argv=None):
                      if [calls[i][1] for i in idx] == ["gate", "up"] else n
                      for n, (_, idx) in zip(names, launches)]
         per_kernel = {}
-        for name in sorted(set(names)):
-            only = {i for i, n in enumerate(names) if n == name}
+        for name in sorted(set(names)) + (["cache"] if cache is not None else []):
+            only = {"cache"} if name == "cache" else {i for i, n in enumerate(names) if n == name}
             subs = []
             for c in range(args.copies):
                 g = torch.cuda.CUDAGraph()
@@ -1007,6 +1195,7 @@ def main(argv=None):
             torch.cuda.synchronize()
             per_kernel[name] = (e0.elapsed_time(e1), only)
 
+    cache_ms = per_kernel.pop("cache")[0] / args.kernel_steps if cache is not None else None
     per_name = {}
     for name, (ms, only) in per_kernel.items():
         per_name[name] = {
@@ -1055,6 +1244,14 @@ def main(argv=None):
                         "GB/s": round(v["bytes"] / (v["ms"] / 1e3) / 1e9, 1)}
                     for k, v in sorted(per_name.items(), key=lambda kv: -kv[1]["ms"])},
     }
+    if cache is not None:
+        nbytes = context_bytes(args.context, args.cache_format)
+        result["config"]["workload"] += (f", with attention of 14 heads of 64 over a paged {args.cache_format} cache of "
+                                         f"{args.context} tokens x 2 KV heads in each layer")
+        result["config"].update(context=args.context, cache_format=args.cache_format, cache_page_size=CACHE_PAGE_SIZE)
+        result["cache"] = {"us_per_step": round(cache_ms * 1e3, 2), "bytes_per_step": nbytes,
+                           "GB/s": round(nbytes / cache_ms / 1e6, 1), "tokens_at_the_end": int(cache.lengths.item()),
+                           "status": int(cache.status.item())}
     if not args.no_cpu_baseline:
         result["cpu_baseline"] = run_cpu_baseline(args.cpu_sample_seconds, args.layout)
     else:

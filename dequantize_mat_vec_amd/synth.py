@@ -140,6 +140,15 @@ def i4row(rng: np.random.Generator, rows: int, in_features: int):
     return rng.integers(0, 256, size=(rows, rb), dtype=np.uint8), scales
 
 
+def i4group(rng: np.random.Generator, rows: int, in_features: int, group: int):
+    """(packed uint8 [rows, in/2], binary16 scales [rows, groups], zero points uint8 [rows, groups]) for 4-bit weights
+    with group scales: random bytes, scales of a group of N(0, 0.02^2) weights in 15 steps, zero points 0..15."""
+    groups = -(-in_features // group)
+    scales = ((rng.random((rows, groups)) * 2 + 4) * 0.02 / 15).astype(np.float16)
+    return (rng.integers(0, 256, size=(rows, in_features // 2), dtype=np.uint8), scales,
+            rng.integers(0, 16, size=(rows, groups), dtype=np.uint8))
+
+
 def matrix(fmt: str, rng: np.random.Generator, rows: int, in_features: int):
     """(packed bytes, scales-or-None) for any format; i8row codes are returned
     as a uint8 view so every format travels as bytes."""
@@ -159,6 +168,7 @@ def matrix(fmt: str, rng: np.random.Generator, rows: int, in_features: int):
 QWEN_HIDDEN = 896
 QWEN_FFN = 4864
 QWEN_KV_OUT = 128          # 2 KV heads x 64
+QWEN_HEADS, QWEN_KV_HEADS, QWEN_HEAD_DIM = 14, 2, 64
 QWEN_LAYERS = 24
 QWEN_VOCAB = 151936
 GPT2_HIDDEN = 768

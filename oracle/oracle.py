@@ -614,3 +614,48 @@ def gemm_experts(offsets, w, x, rows: int, x_rows=None, bias=None, w_scales=None
             y[at] += b
             size[at] += np.abs(b)
     return y, size
+
+
+def dequant_i4group(packed, rows: int, in_features: int, group: int, scales, zeros=None) -> np.ndarray:
+    """4-bit codes 0..15 with a scale and a zero point (None: 8) per `group`
+    weights of a row: w[o][i] = scales[o][i / group] (q[o][i] - zeros[o][i /
+    group]), weight 2k the low nibble of byte k.  float64."""
+    b = np.asarray(packed, dtype=np.uint8).reshape(rows, in_features // 2)
+    q = np.stack([b & 15, b >> 4], axis=-1).reshape(rows, in_features).astype(np.float64)
+    groups = -(-in_features // group)
+    at = np.arange(in_features) // group
+    z = 8.0 if zeros is None else np.asarray(zeros, dtype=np.float64).reshape(rows, groups)[:, at]
+    return np.asarray(scales, dtype=np.float16).astype(np.float64).reshape(rows, groups)[:, at] * (q - z)
+
+
+def gemv_i4group(packed, rows: int, in_features: int, group: int, scales, zeros, x, bias=None, row_chunk: int = 8192):
+    """The mat-vec on such weights, a chunk of rows at a time: (y, error scale)."""
+    parts = []
+    for r0 in range(0, rows, row_chunk):
+        r1 = min(rows, r0 + row_chunk)
+        w = dequant_i4group(packed[r0:r1], r1 - r0, in_features, group, scales[r0:r1], None if zeros is None else zeros[r0:r1])
+        parts.append(gemv(w, x, None if bias is None else np.asarray(bias)[r0:r1]))
+    return tuple(np.concatenate(v, axis=1) for v in zip(*parts))
+
+
+def cached_rows(pool, scales, table, length: int, kv_head: int) -> np.ndarray:
+    """K or V of one sequence and KV head from one layer's pool [pages]
+    [kv_heads][page_size][head_dim] (scales None, or one per row of it), token
+    t being row t % page_size of page table[t / page_size].  float64."""
+    t = np.arange(length)
+    page_size = pool.shape[2]
+    at = (np.asarray(table)[t // page_size], kv_head, t % page_size)
+    x = pool[at].astype(np.float64)
+    return x if scales is None else x * scales[at].astype(np.float64)[:, None]
+
+
+def attend(q, k, v, scale: float):
+    """One query head over its tokens: softmax(scale k q) v, and the error
+    scale sum_t p_t |v_t| ("PESTI ..." README, "Conformance": grouped-query
+    attention).  No token: zeros.  float64."""
+    if len(k) == 0:
+        return np.zeros(len(q)), np.zeros(len(q))
+    score = k @ np.asarray(q, dtype=np.float64) * scale
+    p = np.exp(score - score.max())
+    p /= p.sum()
+    return p @ v, p @ np.abs(v)
