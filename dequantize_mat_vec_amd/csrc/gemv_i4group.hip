@@ -45,6 +45,7 @@ struct I4Args {
   int32_t k_waves;        // wavefronts that share a tile's row length
   int32_t phase_chunks;   // chunks of x staged at once
   int32_t batch_magic;    // ceil(2^16 / batch)
+  int32_t joints;         // buffers for the wavefronts' sums of a tile in LDS
 };
 
 // Sum over groups of L lanes, in every lane: rows of 16 by DPP, then exchanges
@@ -266,20 +267,24 @@ __device__ __forceinline__ void steps_of(const u32x4& q, uint32_t (&w)[4]) {
 constexpr int kScaleRow = 80, kZeroRow = 40;   // LDS bytes of a row's window, padded against bank conflicts
 constexpr int kWindowBytes = 16 * (kScaleRow + kZeroRow);
 
-// A wavefront takes tiles of 16 rows (PAIR: of both matrices), U chunks in
-// flight.  ROWS: each its own tiles, in turn; else the workgroup's wavefronts
-// share a tile's chunks and join their sums in LDS (two wavefronts at least: 128
-// threads store the tile).  GS: groups of a chunk (1 where a group is 128 weights
-// or more).
+// How the work is dealt out (cut_of): few columns on the vector ALUs (the kernel
+// above); or a wavefront takes tiles of 16 rows by itself; or a workgroup's
+// wavefronts share a tile's chunks and join their sums in LDS (two wavefronts at
+// least: 128 threads store the tile); or they do so with x staged in phases.
+enum Way { kFew, kRows, kDeal, kPhases };
+
+// Tiles of 16 rows (PAIR: of both matrices) in turn, U chunks in flight.  GS:
+// groups of a chunk (1 where a group is 128 weights or more).
 //
 // Loads are unconditional, from stand-in places where there is nothing to load:
 // the compiler then knows how many are younger than the one that it waits for.
-template <int GS, bool PAIR, bool ROWS, int U>
+template <int GS, bool PAIR, Way WAY, int U>
 __global__ __launch_bounds__(64 * kI4MaxWaves) __attribute__((amdgpu_waves_per_eu(PAIR ? 2 : 4)))
 void gemv_i4group_kernel(I4Args p) {
 #ifdef __HIP_DEVICE_COMPILE__
   extern __shared__ uint8_t lds[];
   constexpr int R = PAIR ? 2 : 1, kWindowChunks = kWindow / GS;
+  constexpr bool ROWS = WAY == kRows, PHASES = WAY == kPhases;
   static_assert(kWindowChunks % U == 0, "a window is whole rounds");
   const I4Op o = p.op[blockIdx.y];
   asm volatile("" ::"s"(o.a.packed), "s"(o.a.scales), "s"(o.a.zeros), "s"(o.x), "s"(o.y), "s"(o.bias), "s"(o.out), "s"(o.in),
@@ -289,7 +294,7 @@ void gemv_i4group_kernel(I4Args p) {
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int batch = p.batch, in = o.in, chunks = (in + kChunk - 1) / kChunk;
-  const int phase = p.phase_chunks < chunks ? p.phase_chunks : chunks;
+  const int phase = PHASES ? p.phase_chunks : chunks;
   const int64_t out = o.out;
   const int32_t tiles = static_cast<int32_t>((out + 15) / 16);
   int32_t tile = ROWS ? blockIdx.x * waves + wave : blockIdx.x;
@@ -507,12 +512,19 @@ void gemv_i4group_kernel(I4Args p) {
       if (b < batch) o.y[b * out + row] = PAIR ? y[0][i] / (1.f + expf(-y[0][i])) * y[R - 1][i] : (o.bias ? y[0][i] + bias : y[0][i]);
     }
   };
-  auto store_joint = [&](int32_t t, float* at, float bias) {   // at: one of two buffers, used in turn
+  auto keep = [&](float* at) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < 4; ++i) at[((wave * R + r) * 4 + i) * 64 + lane] = total[r][i];
-    __syncthreads();
+  };
+  auto resume = [&](const float* at) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total[r][i] = at[((wave * R + r) * 4 + i) * 64 + lane];
+  };
+  auto join = [&](int32_t t, const float* at, float bias) {
     const int64_t row = static_cast<int64_t>(t) * 16 + en;
     if (!mine || row >= out) return;
     float y[R];
@@ -531,30 +543,33 @@ void gemv_i4group_kernel(I4Args p) {
     o.y[eb * out + row] = PAIR ? y[0] / (1.f + expf(-y[0])) * y[R - 1] : (o.bias ? y[0] + bias : y[0]);
   };
 
-  // x is staged at once, and the workgroup takes tiles in turn; or in phases,
-  // and it has one.  A wavefront's chunks of a phase are first .. first + count - 1.
+  // The workgroup takes tiles in turn, for each phase of x again: between
+  // phases the tiles' sums wait in LDS.  A wavefront's chunks of a phase are
+  // first .. first + count - 1.
   const int32_t apart = ROWS ? gridDim.x * waves : gridDim.x;
+  const int slot_size = waves * R * 256;
   u32x4 w[U][R];
   if (tile >= tiles) tile = -1;   // no tiles for this wavefront: it stages x only
-  int32_t here_tile = tile < 0 ? 0 : tile;
-  int row = row_in(here_tile);
-  int turn = 0;
-  float bias = bias_of(here_tile);
-  clear();
+  float bias = bias_of(tile < 0 ? 0 : tile);
   for (int c0 = 0; c0 < chunks; c0 += phase) {
     const int here = chunks - c0 < phase ? chunks - c0 : phase;
     const int share = ROWS ? here : (here + waves - 1) / waves, first = ROWS ? 0 : wave * share;
     const int count = here - first < share ? (here - first > 0 ? here - first : 0) : share;
     const int g_first = (c0 + first) * kChunk >> p.shift;
+    int32_t here_tile = tile < 0 ? 0 : tile;
+    int row = row_in(here_tile), turn = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) load(here_tile, row * half, c0 + first + u, w[u]);
     fetch(here_tile, row, g_first);
-    if (c0 > 0) __syncthreads();   // x of the phase before has been read
+    if (PHASES && c0 > 0) __syncthreads();   // x of the phase before has been read
     stage(c0, here);
     if (tile < 0) break;
     while (true) {
       const int32_t next = here_tile + apart < tiles ? here_tile + apart : here_tile;
       const int next_row = row_in(next);
+      float* slot = joint + turn * slot_size;
+      if (PHASES && c0 > 0) resume(slot);
+      else clear();
       for (int w0 = 0; w0 < count; w0 += kWindowChunks) {
         const int gw0 = (c0 + first + w0) * kChunk >> p.shift;
         place(here_tile, row, gw0);
@@ -572,19 +587,27 @@ void gemv_i4group_kernel(I4Args p) {
           }
         }
       }
-      if (phase < chunks) break;   // the tile's next phase
-      if constexpr (ROWS) store_rows(here_tile, bias);
-      else store_joint(here_tile, joint + turn * waves * R * 256, bias);
-      turn ^= 1;
-      clear();
+      if constexpr (ROWS) {
+        store_rows(here_tile, bias);
+      } else if constexpr (PHASES) {
+        keep(slot);
+        ++turn;
+      } else {
+        if (p.joints == 1) __syncthreads();   // the tile before has been read
+        keep(slot);
+        __syncthreads();
+        join(here_tile, slot, bias);
+        if (p.joints > 1) turn ^= 1;
+      }
       if (here_tile + apart >= tiles) break;
       here_tile = next;
       row = next_row;
-      bias = bias_of(here_tile);
+      if constexpr (!PHASES) bias = bias_of(here_tile);
     }
   }
-  if constexpr (!ROWS) {
-    if (phase < chunks) store_joint(tile, joint, bias);
+  if constexpr (PHASES) {
+    __syncthreads();
+    for (const float* slot = joint; tile < tiles; tile += apart, slot += slot_size) join(tile, slot, bias_of(tile));
   }
 #endif
 }
@@ -662,26 +685,50 @@ int device() {
 }
 
 // How an op is computed: it depends on the op and the batch alone, so an op of a
-// group has the bits of its single call.
-enum Kind { kFew, kDeal, kRows };
+// group has the bits of its single call.  Measured with groups of 128, in us:
+//   few columns   896 x 896, one column 2.8 on the vector ALUs, 4.4 on the matrix
+//     cores; 4864 x 896, two: 4.2 and 5.4; 9728 x 896, two: 6.3 and 5.4; 4864 x
+//     4096, one: 8.1 and 8.2, two: 13.7 and 9.3
+//   short rows    4864 x 896, four columns: 6.0 a wavefront a tile, 6.4 dealt
+//     out; 2432 x 896: 6.0 and 4.8; 24576 x 896: 7.3 with four wavefronts a
+//     workgroup, 6.7 with eight; gate and up of 9728 x 896: 8.0 with four, 9.9
+//     with eight, 12.7 dealt out
+//   longer rows   16384 x 2048, four columns: 10.9 a wavefront a tile, 10.1 dealt
+//     out
+//   long rows     14336 x 8192, eight columns: 40 in phases with four tiles of a
+//     workgroup, 89 with one; 73 where the columns were split over three launches
+using pesti::kDeal;
+using pesti::kFew;
+using pesti::kPhases;
+using pesti::kRows;
 struct Cut {
-  int kind, waves, phase;
-  bool operator==(const Cut& c) const { return kind == c.kind && waves == c.waves && phase == c.phase; }
+  pesti::Way way;
+  int waves, phase, each;   // chunks staged at once (kFew: dwords of a pass); tiles of a workgroup, where x comes in phases
+  bool operator==(const Cut& c) const { return way == c.way && waves == c.waves && phase == c.phase && each == c.each; }
 };
-Cut cut_of(const I4Op& o, int batch) {
+constexpr int64_t kMost = 160 * 1024;   // LDS of a workgroup
+int64_t x_bytes(int chunks, int columns) { return int64_t{chunks} * (pesti::chunk_bytes(columns) + 32); }
+int64_t wave_bytes(int waves, bool pair, int joints) { return int64_t{waves} * (pair ? 2 : 1) * (pesti::kWindowBytes + 1024 * joints); }
+
+Cut cut_of(const I4Op& o, int batch, bool pair) {
   const int chunks = (o.in + pesti::kChunk - 1) / pesti::kChunk, dwords = o.in / 8;
-  const int64_t tiles = (o.out + 15) / 16;
+  const int64_t tiles = (o.out + 15) / 16, products = o.out * o.in * batch;
   // (the matrix kernel loads eight groups' scales at once)
-  if (batch <= 2 || o.out * o.groups < 8) {   // dwords per lane group and pass: 32 x 1, 2, 4 or 64 x 4, 8
-    int span = 32;
+  if ((batch <= 2 && products <= (chunks <= 8 ? 12 << 20 : 20 << 20)) || o.out * o.groups < 8) {
+    int span = 32;   // dwords per lane group and pass: 32 x 1, 2, 4 or 64 x 4, 8
     while (span < dwords && span < 512) span *= 2;
-    return Cut{kFew, 4, span};
+    return Cut{kFew, 4, span, 0};
   }
-  const int fits = 96 * 1024 / (pesti::chunk_bytes(batch) + 32);   // chunks of x in LDS, beside 62 KiB of windows and sums
-  if (tiles >= 2048 && chunks <= fits / 2) return Cut{kRows, 8, chunks};
+  if (tiles >= (chunks <= 8 ? 256 : 2048) && x_bytes(chunks, batch) <= 48 * 1024)
+    return Cut{kRows, pair || tiles < 1024 ? 4 : 8, chunks, 0};
   // 128 threads store a tile of eight columns
   const int waves = chunks < 2 ? 2 : (chunks < pesti::kI4MaxWaves ? chunks : pesti::kI4MaxWaves);
-  return Cut{kDeal, waves, chunks < fits ? chunks : fits};
+  if (x_bytes(chunks, batch) <= kMost - wave_bytes(waves, pair, 1)) return Cut{kDeal, waves, chunks, 0};
+  // Tiles whose sums wait in LDS for the next phase: the more a workgroup has,
+  // the fewer times x is staged, and the less of it at once.
+  const int64_t most = pair ? 4 : 8, per_unit = (tiles + 255) / 256;
+  const int each = static_cast<int>(per_unit < most ? per_unit : most);
+  return Cut{kPhases, waves, static_cast<int>((kMost - wave_bytes(waves, pair, each)) / x_bytes(1, batch)), each};
 }
 
 int64_t most_rows(const I4Args& p, int n_ops) {
@@ -725,31 +772,30 @@ int launch_few_span(I4Args& p, int n_ops, int span, hipStream_t st) {
 
 template <int GS, bool PAIR>
 int launch_many(I4Args& p, int n_ops, const Cut& c, hipStream_t st) {
-  constexpr int R = PAIR ? 2 : 1;
   const int64_t tiles = (most_rows(p, n_ops) + 15) / 16;
   p.phase_chunks = c.phase;
   p.batch_magic = (65536 + p.batch - 1) / p.batch;
-  const size_t x = static_cast<size_t>(c.phase) * (pesti::chunk_bytes(p.batch) + 32) + static_cast<size_t>(c.waves) * R * pesti::kWindowBytes;
-  if (c.kind == kRows) {
+  const int64_t x = x_bytes(c.phase, p.batch);
+  if (c.way == kRows) {
     const int64_t blocks = (tiles + c.waves - 1) / c.waves;
-    return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel<GS, PAIR, true, 2>), p, blocks < 512 ? blocks : 512,
-                  n_ops, 64 * c.waves, x, st);
+    return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel<GS, PAIR, kRows, 2>), p, blocks < 512 ? blocks : 512,
+                  n_ops, 64 * c.waves, x + wave_bytes(c.waves, PAIR, 0), st);
   }
-  // Workgroups that are resident together stage x once and take tiles in turn;
-  // where x comes in phases each has one tile.
-  const size_t lds = x + 2 * static_cast<size_t>(c.waves) * R * 1024;
-  int64_t blocks = tiles;
-  bool phased = false;
-  for (int i = 0; i < n_ops; ++i) phased = phased || (p.op[i].in + pesti::kChunk - 1) / pesti::kChunk > c.phase;
-  const int64_t resident = 256 * (lds > 80 * 1024 ? 1 : 2);
-  if (!phased && blocks > resident) blocks = resident;
-  return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel<GS, PAIR, false, 2>), p, blocks, n_ops, 64 * c.waves,
-                lds, st);
+  if (c.way == kPhases) {
+    p.joints = c.each;
+    return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel<GS, PAIR, kPhases, 2>), p, (tiles + c.each - 1) / c.each,
+                  n_ops, 64 * c.waves, x + wave_bytes(c.waves, PAIR, c.each), st);
+  }
+  // Workgroups that are resident together stage x once and take tiles in turn.
+  p.joints = x + wave_bytes(c.waves, PAIR, 2) > kMost ? 1 : 2;
+  const int64_t lds = x + wave_bytes(c.waves, PAIR, p.joints), resident = 256 * (lds > kMost / 2 ? 1 : 2);
+  return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_kernel<GS, PAIR, kDeal, 2>), p, tiles < resident ? tiles : resident,
+                n_ops, 64 * c.waves, lds, st);
 }
 
 template <bool PAIR>
 int launch_cut(I4Args& p, int n_ops, const Cut& c, hipStream_t st) {
-  if (c.kind == kFew) {
+  if (c.way == kFew) {
     for (int b = 0; b < p.batch; b += 2) {   // two columns a launch
       I4Args q = p;
       q.batch = p.batch - b < 2 ? 1 : 2;
@@ -775,10 +821,10 @@ int launch(const I4Args& all, int n_ops, bool pair, hipStream_t st) {
     I4Args p = all;
     int n = 0;
     const bool empty = all.op[i].in == 0;
-    const Cut c = empty ? Cut{} : cut_of(all.op[i], all.batch);
+    const Cut c = empty ? Cut{} : cut_of(all.op[i], all.batch, pair);
     for (int j = i; j < n_ops; ++j) {
       if (taken[j] || (all.op[j].in == 0) != empty) continue;
-      if (!empty && !(cut_of(all.op[j], all.batch) == c)) continue;
+      if (!empty && !(cut_of(all.op[j], all.batch, pair) == c)) continue;
       taken[j] = true;
       p.op[n++] = all.op[j];
     }

@@ -274,3 +274,66 @@ def test_other_stream_and_captured_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, eager[i])
+
+
+# how the work is dealt out by size: x whole in LDS with one or two buffers of sums, in phases with one to eight tiles
+# of a workgroup (the last with fewer, and more workgroups than compute units), few rows by single wavefronts
+WAYS = [(8, 5003, 4096, 128), (8, 4115, 8192, 64), (5, 9001, 8192, 128), (8, 33003, 8224, 256), (7, 4801, 16384, 32),
+        (3, 4115, 28704, 128), (1, 4115, 5152, 64), (2, 4200, 800, 32), (4, 4099, 1024, 128), (6, 16500, 1024, 64),
+        (1, 12345, 1088, 32), (2, 32771, 640, 128)]
+
+
+@pytest.mark.parametrize("batch,out,inf,group", WAYS)
+def test_ways(batch, out, inf, group):
+    announce(f"i4group way of {batch}x{out}x{inf} group {group}")
+    rng = case_rng(13, out, inf)
+    m = i4_matrix(rng, out, inf, group)
+    x, bias = rng.standard_normal((batch, inf)).astype(np.float32), rng.standard_normal(out).astype(np.float32)
+    y = run(m, out, inf, group, x, bias)
+    for rows in np.array_split(np.arange(out), -(-out * inf // (1 << 24))):
+        w = i4_weights(*(v[rows] for v in m), inf, group)
+        exact = x.astype(np.float64) @ w.T
+        tol = i4_tolerance(w, x.astype(np.float64)) + 2.0 ** -23 * np.abs(bias[rows])
+        exact = exact + bias[rows].astype(np.float64)
+        err = np.abs(y[:, rows] - exact)
+        assert np.all(err <= tol + 2.0 ** -24 * np.abs(exact)), (float((err / tol).max()), int(rows[np.argmax(err / tol) % len(rows)]))
+
+
+@pytest.mark.parametrize("batch,out,inf,group", [(8, 4115, 4096, 128), (6, 2500, 8192, 64), (4, 9003, 8192, 32), (2, 12000, 1056, 64),
+                                                 (4, 17001, 896, 128), (5, 16400, 6176, 128)])
+def test_ways_of_swiglu(batch, out, inf, group):
+    announce(f"i4group swiglu way of {batch}x{out}x{inf} group {group}")
+    import torch
+    rng = case_rng(14, out, inf)
+    gate, up = (i4_matrix(rng, out, inf, group) for _ in range(2))
+    x = rng.standard_normal((batch, inf)).astype(np.float32)
+    buf, h = guarded_y(batch * out)
+    dmv.pesti_gemv_i4group_swiglu(out, inf, group, *put(gate), *put(up), to_dev(x), h, batch)
+    torch.cuda.synchronize()
+    assert guards_intact(buf, batch * out)
+    h, x = h.cpu().numpy().reshape(batch, out).astype(np.float64), x.astype(np.float64)
+    for rows in np.array_split(np.arange(out), -(-out * inf // (1 << 24))):
+        wg, wu = (i4_weights(*(v[rows] for v in m), inf, group) for m in (gate, up))
+        g, u, eg, eu = x @ wg.T, x @ wu.T, i4_tolerance(wg, x), i4_tolerance(wu, x)
+        tol = 1.1 * eg * (np.abs(u) + eu) + np.abs(silu(g)) * eu + 2.0 ** -20 * np.abs(silu(g) * u) + 1e-30
+        err = np.abs(h[:, rows] - silu(g) * u)
+        assert np.all(err <= tol), float((err / tol).max())
+
+
+def test_a_group_of_all_ways():
+    """Ops that are dealt out differently share a call, and keep the bits of their single calls."""
+    announce("i4group group of all ways")
+    import torch
+    rng = case_rng(15)
+    ops, singles = [], []
+    for out, inf in ((4115, 8192), (40, 8192), (4800, 896), (17000, 896), (600, 4096), (9000, 8192), (3, 32)):
+        p, s, z = put(i4_matrix(rng, out, inf, 128))
+        x = to_dev(rng.standard_normal((8, inf)).astype(np.float32))
+        y, y1 = (torch.full((8, out), 7.0, device="cuda") for _ in range(2))
+        ops.append((out, inf, p, s, z, x, y, None))
+        dmv.pesti_gemv_i4group(out, inf, 128, p, s, z, x, y1, None, 8)
+        singles.append(y1)
+    dmv.pesti_gemv_group_i4group(ops, 128, 8)
+    torch.cuda.synchronize()
+    for op, y1 in zip(ops, singles):
+        assert torch.equal(op[6], y1), op[:2]
