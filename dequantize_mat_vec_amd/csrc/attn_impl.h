@@ -23,7 +23,7 @@
 //     the same run of up to 8 dimensions of each, and the transposition is the
 //     choice of which 16-bit halves form a register (v_perm), with the
 //     dimensions of a run spread over as many matrix instructions.  No LDS.
-// LDS is used once, to join the four wavefronts of a workgroup, which take the
+// LDS is used once, to join the wavefronts of a workgroup, which take the
 // tiles of its part of the sequence in turn.  Parts are joined by a second
 // kernel (attn_paged.hip) where a sequence has more than one.
 #pragma once
@@ -50,12 +50,13 @@ struct AttnArgs {
   int32_t head_blocks;     // workgroups per KV head
   int32_t splits;
   int32_t part_tiles;      // tiles of a part
+  int32_t waves;           // wavefronts of a workgroup
   int32_t q_f32, y_f32;
 };
 
-constexpr int kAttnWaves = 4;
+// Wavefronts of a workgroup: four, or eight where a sequence is one part.
+constexpr int attn_most_waves(int d, int nt) { return d * nt <= 128 ? 8 : 4; }
 constexpr int kTile = 32;            // tokens of one step of a wavefront
-constexpr int kMinPartTiles = 8;     // a workgroup's part of a sequence is at least two steps of each wavefront
 
 // Tiles per part, and parts, of a sequence of `length` tokens.  Parts of all
 // sequences have one size, so that workgroups of a batch of uneven lengths
@@ -69,10 +70,15 @@ __device__ __forceinline__ int32_t attn_parts(int32_t length, int32_t per) {
   return ((length + kTile - 1) / kTile + per - 1) / per;
 }
 
-__device__ __forceinline__ int32_t attn_length(const AttnArgs& p, int64_t row, int64_t* seq) {
-  *seq = p.seq_ids ? p.seq_ids[row] : row;
-  if (*seq < 0 || *seq >= p.kv.seqs || p.kv.pages == 0) return 0;
-  return kv_length(p.kv, static_cast<int32_t>(*seq));
+// Four values of y, at a multiple of four.
+__device__ __forceinline__ void store_y(const AttnArgs& p, int64_t at, const f32x4& y) {
+  if (p.y_f32) {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + at) = y;
+  } else {
+    typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<h4*>(static_cast<_Float16*>(p.y) + at) =
+        h4{static_cast<_Float16>(y[0]), static_cast<_Float16>(y[1]), static_cast<_Float16>(y[2]), static_cast<_Float16>(y[3])};
+  }
 }
 
 #ifdef __HIP_DEVICE_COMPILE__
@@ -235,13 +241,19 @@ constexpr int attn_waves(bool i8, int d, int nt, bool small) {
 // XCDs idle).  SMALL: pages of 8 or 16 tokens, up
 // to four in a tile; else a tile lies in one page.
 template <bool I8, int D, int NT, bool SMALL>
-__global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu(attn_waves(I8, D, NT, SMALL))))
+__global__ __launch_bounds__(64 * attn_most_waves(D, NT)) __attribute__((amdgpu_waves_per_eu(attn_waves(I8, D, NT, SMALL))))
 void attn_kernel(AttnArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int kSteps = D / 32, kFrags = D / 16, kSize = I8 ? 1 : 2, kPages = SMALL ? 4 : 1;
-  __shared__ float joint[kAttnWaves][8 * NT][D];
-  __shared__ float wave_max[kAttnWaves][8 * NT], wave_sum[kAttnWaves][8 * NT];
+  constexpr int kMostWaves = attn_most_waves(D, NT), kRow = D + 4;   // (padded against bank conflicts)
+  extern __shared__ float lds[];   // per wavefront: y of 8 NT heads, their maxima, their sums
   const KvArgs& a = p.kv;
+  const int waves = p.waves;
+  float* joint = lds;
+  float* wave_max = lds + waves * 8 * NT * kRow;
+  float* wave_sum = wave_max + waves * 8 * NT;
+  float* joint_max = wave_sum + waves * 8 * NT;   // and the workgroup's
+  float* joint_sum = joint_max + 8 * NT;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
   const bool second = col >= 8;
@@ -249,80 +261,57 @@ void attn_kernel(AttnArgs p) {
   const int kvh = blockIdx.x / p.head_blocks, hb = blockIdx.x % p.head_blocks;
   const int head0 = hb * 8 * NT, heads_here = p.group - head0 < 8 * NT ? p.group - head0 : 8 * NT;
   const int64_t first_head = static_cast<int64_t>(kvh) * p.group + head0;
-
-  int64_t seq;
-  const int32_t length = attn_length(p, row, &seq);
-  const int32_t per = attn_part_tiles(length, p.splits, p.part_tiles), parts = attn_parts(length, per);
   const int32_t part = static_cast<int32_t>((blockIdx.y + blockIdx.z) % static_cast<uint32_t>(p.splits));
-  if (part >= parts && part > 0) return;   // (a sequence without tokens: part 0 writes the zeros)
-  const int32_t tiles = (length + kTile - 1) / kTile;
-  const int32_t end = part * per + per < tiles ? part * per + per : tiles;
 
-  // Q: columns 0-7 the first parts, 8-15 the second ones, of heads that exist;
-  // scaled so that a head's largest finite value lies in [2^14, 2^15).
-  h8 qf[NT][kSteps];
-  float factor[NT];
+  // A short sequence's time is the way from one load to the next: q, the length
+  // and the pages of the first tiles, where they lie unless the sequence is
+  // longer than the caller's bound, are asked for together.
+  const int64_t seq = p.seq_ids ? p.seq_ids[row] : row;
+  const bool known = seq >= 0 && seq < a.seqs && a.pages > 0 && a.width > 0;
+  const int32_t* row_pages = a.table + (known ? seq : 0) * a.width;
+  auto page_index = [&](int32_t tile, int j) {
+    return ((static_cast<int64_t>(tile) + lane * waves) * kTile + 8 * j) >> a.page_shift;
+  };
+  int32_t ids[kPages];   // lane i: the pages of the wavefront's i-th tile from here
+#pragma unroll
+  for (int j = 0; j < kPages; ++j) {
+    const int64_t idx = page_index(part * p.part_tiles + wave, j);
+    ids[j] = known ? row_pages[idx < a.width ? idx : a.width - 1] : -1;
+  }
+  const int32_t length = known ? kv_length(a, static_cast<int32_t>(seq)) : 0;
+  f32x4 q32[NT][kSteps][2];
+  h8 q16[NT][kSteps];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int h = 8 * n + (col & 7);
-    const bool there = h < heads_here;
-    const int64_t at = row * p.q_stride + (first_head + (there ? h : 0)) * D;
-    float v[kSteps][8];
-    uint32_t most = 0;
+    const int64_t q0 = row * p.q_stride + (first_head + (h < heads_here ? h : 0)) * D;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const int64_t e0 = at + k_dim<I8>(s, kSteps, g);
+      const int64_t e0 = q0 + k_dim<I8>(s, kSteps, g);
       if (p.q_f32) {
         const f32x4* src = reinterpret_cast<const f32x4*>(static_cast<const float*>(p.q) + e0);
-        const f32x4 lo = src[0], hi = src[1];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) { v[s][e] = lo[e]; v[s][e + 4] = hi[e]; }
+        q32[n][s][0] = src[0];
+        q32[n][s][1] = src[1];
       } else {
-        const h8 x = *reinterpret_cast<const h8*>(static_cast<const _Float16*>(p.q) + e0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[s][e] = static_cast<float>(x[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t u = __builtin_bit_cast(uint32_t, v[s][e]) & 0x7FFFFFFFu;
-        most = u < 0x7F800000u && u > most ? u : most;
+        q16[n][s] = *reinterpret_cast<const h8*>(static_cast<const _Float16*>(p.q) + e0);
       }
     }
-    // magnitudes are ordered as floats too
-    const uint32_t big = __builtin_bit_cast(uint32_t, column_max(__builtin_bit_cast(float, most)));
-    int up = 14 + 127 - static_cast<int>(big >> 23);   // the exponent to add
-    up = big == 0 ? 0 : (up > 126 ? 126 : up);
-    const float lift = __builtin_bit_cast(float, static_cast<uint32_t>(up + 127) << 23);
-    factor[n] = p.scale * __builtin_bit_cast(float, static_cast<uint32_t>(127 - up) << 23);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) qf[n][s][e] = there ? part_of(v[s][e] * lift, second) : static_cast<_Float16>(0.f);
+  }
+  const int32_t per = attn_part_tiles(length, p.splits, p.part_tiles), parts = attn_parts(length, per);
+  const int32_t tiles = (length + kTile - 1) / kTile;
+  const int32_t end = part * per + per < tiles ? part * per + per : tiles;
+  if (p.splits > 1 && part >= parts) {   // nothing there: the join is told so
+    if (tid < heads_here) {
+      float* stats = p.stats + 2 * ((row * p.heads + first_head + tid) * p.splits + part);
+      stats[0] = -INFINITY;
+      stats[1] = 0.f;
+    }
+    return;
   }
 
-  f32x4 acc[NT][kFrags];
-  float most[NT], sum[NT], ref[NT];   // ref: y is held as acc * 2^ref (8 bits; else the maximum alone scales it)
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    most[n] = -INFINITY;
-    sum[n] = 0.f;
-    ref[n] = -126.f;
-#pragma unroll
-    for (int f = 0; f < kFrags; ++f) acc[n][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
-  // Per lane: what its part of a score counts for (softmax's scale in it), and
-  // how the second part of a weight is made.
-  float share[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) share[n] = second ? factor[n] * kPart : factor[n];
-  const float less = second ? -1.f : 0.f, times = second ? 0x1p11f : 1.f;
-
-  const int32_t* row_pages = a.table + seq * a.width;
   const int32_t held = kv_pages_of(a, length);
   const int32_t page_mask = (1 << a.page_shift) - 1;
   const int32_t first_tile = part * per + wave, last_tile = end - 1;
-  int32_t ids[kPages];   // lane i: the pages of the wavefront's i-th tile from here
 
   // Where a tile lies: rows of the layer's pools that its token 0 would have in
   // the page of K's tokens (column col) and of V's (lane group g), by half.
@@ -330,12 +319,12 @@ void attn_kernel(AttnArgs p) {
     int64_t k_row[2], v_row[2];
     uint32_t there;   // bit t: token t of the tile is in the cache
   };
-  auto locate = [&](int32_t tile) {
-    const int step = (tile - first_tile) / kAttnWaves & 63;
-    if (step == 0) {
+  auto locate = [&](int32_t tile, int step) {   // step: of the wavefront
+    step &= 63;
+    if (step == 0 && (tile != first_tile || per != p.part_tiles)) {
 #pragma unroll
       for (int j = 0; j < kPages; ++j) {
-        const int64_t idx = ((static_cast<int64_t>(tile) + lane * kAttnWaves) * kTile + 8 * j) >> a.page_shift;
+        const int64_t idx = page_index(tile, j);
         ids[j] = idx < held ? row_pages[idx] : -1;
       }
     }
@@ -406,11 +395,64 @@ void attn_kernel(AttnArgs p) {
   // half of a step, without a second set of registers.
   Place at{};
   if (first_tile <= last_tile) {
-    at = locate(first_tile);
+    at = locate(first_tile, 0);
     load_k(at);
     load_v(at);
   }
-  for (int32_t tile = first_tile; tile <= last_tile; tile += kAttnWaves) {
+  __builtin_amdgcn_sched_barrier(0);
+
+  // Q: columns 0-7 the first parts, 8-15 the second ones, of heads that exist;
+  // scaled so that a head's largest finite value lies in [2^14, 2^15).
+  h8 qf[NT][kSteps];
+  float factor[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int h = 8 * n + (col & 7);
+    const bool there = h < heads_here;
+    float v[kSteps][8];
+    uint32_t most = 0;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[s][e] = p.q_f32 ? q32[n][s][e / 4][e % 4] : static_cast<float>(q16[n][s][e]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v[s][e]) & 0x7FFFFFFFu;
+        most = u < 0x7F800000u && u > most ? u : most;
+      }
+    }
+    // magnitudes are ordered as floats too
+    const uint32_t big = __builtin_bit_cast(uint32_t, column_max(__builtin_bit_cast(float, most)));
+    int up = 14 + 127 - static_cast<int>(big >> 23);   // the exponent to add
+    up = big == 0 ? 0 : (up > 126 ? 126 : up);
+    const float lift = __builtin_bit_cast(float, static_cast<uint32_t>(up + 127) << 23);
+    factor[n] = p.scale * __builtin_bit_cast(float, static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) qf[n][s][e] = there ? part_of(v[s][e] * lift, second) : static_cast<_Float16>(0.f);
+  }
+
+  f32x4 acc[NT][kFrags];
+  float most[NT], sum[NT], ref[NT];   // ref: y is held as acc * 2^ref (8 bits; else the maximum alone scales it)
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    most[n] = -INFINITY;
+    sum[n] = 0.f;
+    ref[n] = -126.f;
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) acc[n][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // Per lane: what its part of a score counts for (softmax's scale in it), and
+  // how the second part of a weight is made.
+  float share[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) share[n] = second ? factor[n] * kPart : factor[n];
+  const float less = second ? -1.f : 0.f, times = second ? 0x1p11f : 1.f;
+
+  int step = 0;
+  for (int32_t tile = first_tile; tile <= last_tile; tile += waves) {
     f32x4 s[NT][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -430,7 +472,8 @@ void attn_kernel(AttnArgs p) {
     // bit 4h + i: the lane's token is there
     const uint32_t mine = (there >> (4 * g) & 15u) | (there >> (16 + 4 * g) & 15u) << 4;
     __builtin_amdgcn_sched_barrier(0);
-    at = locate(tile + kAttnWaves <= last_tile ? tile + kAttnWaves : tile);   // (the last one's are loaded again)
+    // (the last one's are loaded again)
+    if (tile + waves <= last_tile) at = locate(tile + waves, ++step);
     load_k(at);
     __builtin_amdgcn_sched_barrier(0);
     h8 pf[NT];
@@ -528,48 +571,65 @@ void attn_kernel(AttnArgs p) {
   for (int n = 0; n < NT; ++n) {
     const float all = column_sum(sum[n]);
     if (lane < 8) {
-      wave_max[wave][8 * n + lane] = most[n];
-      wave_sum[wave][8 * n + lane] = all;
+      wave_max[wave * 8 * NT + 8 * n + lane] = most[n];
+      wave_sum[wave * 8 * NT + 8 * n + lane] = all;
     }
   }
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    float top = -INFINITY;
+    const int h = 8 * n + (col & 7);
+    float top = -INFINITY, total = 0.f, m[kMostWaves], l[kMostWaves];
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, wave_max[w][8 * n + (col & 7)]);
+    for (int w = 0; w < kMostWaves; ++w) {
+      m[w] = wave_max[(w < waves ? w : 0) * 8 * NT + h];
+      l[w] = wave_sum[(w < waves ? w : 0) * 8 * NT + h];
+      top = fmaxf(top, m[w]);
+    }
+    if (wave == 0) {
+#pragma unroll
+      for (int w = 0; w < kMostWaves; ++w)
+        total += w < waves ? (m[w] == -INFINITY ? l[w] : l[w] * __builtin_amdgcn_exp2f(m[w] - top)) : 0.f;   // l is 0 there, or NaN
+      if (lane < 8) {
+        joint_max[h] = top;
+        joint_sum[h] = total;
+      }
+    }
     float scale = most[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(most[n] - top + (I8 ? ref[n] : -14.f));
     if (sum[n] != sum[n]) scale = 1.f;   // NaN without a maximum: y is NaN already
+    float* to = joint + (wave * 8 * NT + h) * kRow;
+    // both columns of a head have its sums: each writes half of them
 #pragma unroll
-    for (int f = 0; f < kFrags; ++f)
+    for (int f = 0; f < kFrags / 2; ++f)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float own = acc[n][f][i], oth = other_part(own);
-        if (!second) joint[wave][8 * n + col][VTile<I8, D>::dim(f, 4 * g + i)] = both_parts(own, oth) * scale;
+        const float a0 = acc[n][f][i], a1 = acc[n][f + kFrags / 2][i], o0 = other_part(a0), o1 = other_part(a1);
+        const float y = both_parts(second ? o1 : a0, second ? a1 : o0) * scale;
+        to[second ? VTile<I8, D>::dim(f + kFrags / 2, 4 * g + i) : VTile<I8, D>::dim(f, 4 * g + i)] = y;
       }
   }
   __syncthreads();
-  for (int e = tid; e < heads_here * D; e += 64 * kAttnWaves) {
-    const int h = e / D, d = e % D;
-    float top = -INFINITY, total = 0.f, y = 0.f;
+  for (int e = tid; e < heads_here * (D / 4); e += 64 * waves) {
+    const int h = e / (D / 4), d = e % (D / 4) * 4;
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, wave_max[w][h]);
+    for (int w = 0; w < kMostWaves; ++w) {
+      if (w >= waves) break;
+      const f32x4 v = *reinterpret_cast<const f32x4*>(joint + (w * 8 * NT + h) * kRow + d);
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
-      const float m = wave_max[w][h], l = wave_sum[w][h];
-      total += m == -INFINITY ? l : l * __builtin_amdgcn_exp2f(m - top);   // l is 0 there, or NaN
-      y += joint[w][h][d];
+      for (int j = 0; j < 4; ++j) y[j] += v[j];
     }
+    const float total = joint_sum[h];
     const int64_t at = row * p.heads + first_head + h;
-    if (parts <= 1) {
-      const float r = total == 0.f ? 0.f : y / total;
-      if (p.y_f32) static_cast<float*>(p.y)[at * D + d] = r;
-      else static_cast<_Float16*>(p.y)[at * D + d] = static_cast<_Float16>(r);
+    if (p.splits <= 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = total == 0.f ? 0.f : y[j] / total;
+      store_y(p, at * D + d, y);
     } else {
       const int64_t slot = at * p.splits + part;
-      p.parts[slot * D + d] = y;
+      *reinterpret_cast<f32x4*>(p.parts + slot * D + d) = y;
       if (d == 0) {
-        p.stats[2 * slot] = top;
+        p.stats[2 * slot] = joint_max[h];
         p.stats[2 * slot + 1] = total;
       }
     }
@@ -582,8 +642,10 @@ void attn_kernel(AttnArgs p) {
 namespace pesti_attn {
 
 // Head tiles of 8 that a workgroup takes: two where a KV head has more than 8
-// query heads and the registers hold them.
-inline int head_tiles(int64_t group, int64_t head_dim) { return group > 8 && head_dim <= 128 ? 2 : 1; }
+// query heads and the registers leave three wavefronts on a SIMD (16 rows up to
+// 2000, 16 query heads to a KV head of 128, where they leave one: 22.5 us with
+// one tile, 29.3 with two).
+inline int head_tiles(int64_t group, int64_t head_dim) { return group > 8 && head_dim <= 64 ? 2 : 1; }
 
 template <bool I8, int D, int NT, bool SMALL>
 int launch(const pesti::AttnArgs& p, int64_t rows, hipStream_t st) {
@@ -592,13 +654,13 @@ int launch(const pesti::AttnArgs& p, int64_t rows, hipStream_t st) {
   return pesti_kv::launch(reinterpret_cast<const void*>(&pesti::attn_kernel<I8, D, NT, SMALL>),
                           dim3(static_cast<unsigned>(p.kv.kv_heads * p.head_blocks), static_cast<unsigned>(p.splits),
                                static_cast<unsigned>(rows)),
-                          dim3(64 * pesti::kAttnWaves), params, 0, st);
+                          dim3(64 * p.waves), params, static_cast<size_t>(p.waves * (D + 6) + 2) * 8 * NT * 4, st);
 }
 
 template <bool I8, int D>
 int launch_d(const pesti::AttnArgs& p, int64_t rows, hipStream_t st) {
   const bool small = p.kv.page_shift < 5;
-  if constexpr (D <= 128) {
+  if constexpr (D <= 64) {
     if (head_tiles(p.group, D) == 2) return small ? launch<I8, D, 2, true>(p, rows, st) : launch<I8, D, 2, false>(p, rows, st);
   }
   return small ? launch<I8, D, 1, true>(p, rows, st) : launch<I8, D, 1, false>(p, rows, st);

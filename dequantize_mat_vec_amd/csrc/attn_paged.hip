@@ -6,25 +6,71 @@
 namespace pesti {
 
 constexpr int kMaxParts = 256;
-constexpr int kManyRows = 16;
+constexpr int kFewParts = 8;
+constexpr int kManyRows = 32;
+constexpr int kWholeTiles = 4;   // a sequence of that many tiles a wavefront is one part
 
-// y of one row and head from its parts, in part order: part i counts 2^(max_i -
-// max) times.  D4: head_dim / 4 rounded up to a power of two; as many threads
-// take a part, so several parts are in flight.
-template <int D4>
+// y of one row and head from its parts: part i counts 2^(max_i - max) times, one
+// without tokens (maximum -infinity, sum 0) not at all.  The parts are added in
+// an order that the launch fixes.
+//
+// Few parts: a thread takes four dimensions of all of them.
+__global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs p, int64_t threads) {
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= threads) return;
+  const int quads = p.kv.head_dim / 4, parts = p.splits;
+  const int64_t head = at / quads, slot0 = head * parts;
+  const int e = static_cast<int>(at - head * quads);
+  const float* src = p.parts + slot0 * p.kv.head_dim + 4 * e;
+  float m[kFewParts], l[kFewParts], top = -INFINITY, total = 0.f;
+  f32x4 v[kFewParts], y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kFewParts; ++i) {
+    if (i >= parts) break;
+    m[i] = p.stats[2 * (slot0 + i)];
+    l[i] = p.stats[2 * (slot0 + i) + 1];
+    v[i] = *reinterpret_cast<const f32x4*>(src + static_cast<int64_t>(i) * p.kv.head_dim);
+  }
+#pragma unroll
+  for (int i = 0; i < kFewParts; ++i) top = i < parts ? fmaxf(top, m[i]) : top;
+#pragma unroll
+  for (int i = 0; i < kFewParts; ++i) {
+    if (i >= parts) break;
+    const float w = m[i] == -INFINITY ? (l[i] == l[i] ? 0.f : 1.f) : exp2f(m[i] - top);   // a NaN without a maximum stays
+    total = fmaf(w, l[i], total);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = w == 0.f ? y[j] : fmaf(w, v[i][j], y[j]);   // (a part without tokens wrote nothing)
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = total == 0.f ? 0.f : y[j] / total;
+  store_y(p, 4 * at, y);
+}
+
+// More: a workgroup has 4 * LANES dimensions of a row and head.  LANES threads
+// take a part, all parts are in flight while the maxima are: with that many
+// LANES at most that eight parts a thread are enough (256 parts of heads of 128
+// with one workgroup a head: 28.5 us with the attention, with four: 17.6).
+template <int LANES>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
+  constexpr int kGroups = 256 / LANES, kAhead = 8;
   __shared__ float weight[kMaxParts], sums[4], tops[4];
-  __shared__ f32x4 joint[256 / D4][D4];
-  const int tid = threadIdx.x, d = p.kv.head_dim;
-  const int64_t row = blockIdx.y, slot0 = (row * p.heads + blockIdx.x) * p.splits;
-  int64_t seq;
-  const int32_t length = attn_length(p, row, &seq);
-  const int32_t parts = attn_parts(length, attn_part_tiles(length, p.splits, p.part_tiles));
-  if (parts <= 1) return;   // written already
-  float m = -INFINITY, l = 0.f;
-  if (tid < parts) {
-    m = p.stats[2 * (slot0 + tid)];
-    l = p.stats[2 * (slot0 + tid) + 1];
+  __shared__ f32x4 joint[kGroups][LANES];
+  const int tid = threadIdx.x, d = p.kv.head_dim, parts = p.splits;
+  const int64_t row = blockIdx.z, head = row * p.heads + blockIdx.y, slot0 = head * parts;
+  const int e = tid % LANES, first = tid / LANES, at = blockIdx.x * 4 * LANES + 4 * e;
+  const bool live = at < d;
+  const float* src = p.parts + slot0 * d + (live ? at : 0);
+  const int has = tid < parts ? tid : 0;
+  float m = p.stats[2 * (slot0 + has)], l = p.stats[2 * (slot0 + has) + 1];
+  f32x4 v[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = first + k * kGroups;
+    v[k] = *reinterpret_cast<const f32x4*>(src + static_cast<int64_t>(i < parts ? i : 0) * d);
+  }
+  if (tid >= parts) {
+    m = -INFINITY;
+    l = 0.f;
   }
   float top = m;
 #pragma unroll
@@ -40,33 +86,23 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
   if ((tid & 63) == 0) sums[tid >> 6] = total;
   __syncthreads();
   total = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-  constexpr int kGroups = 256 / D4;
-  const int e = tid % D4, first = tid / D4;
-  const bool live = 4 * e < d;
   f32x4 y = {0.f, 0.f, 0.f, 0.f};
-  if (live) {
-    const f32x4* src = reinterpret_cast<const f32x4*>(p.parts + slot0 * d) + e;
-#pragma unroll 8
-    for (int i = first; i < parts; i += kGroups) {
-      const f32x4 v = src[static_cast<int64_t>(i) * (d / 4)];
-      const float f = weight[i];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = fmaf(f, v[j], y[j]);
-    }
+  for (int k = 0; k < kAhead; ++k) {
+    const float f = weight[first + k * kGroups];   // (0 past the last part)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = f == 0.f ? y[j] : fmaf(f, v[k][j], y[j]);   // (a part without tokens wrote nothing)
   }
   joint[first][e] = y;
   __syncthreads();
-  if (first > 0 || !live) return;
+  if (tid >= LANES || !live) return;
+#pragma unroll
   for (int k = 1; k < kGroups; ++k)
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] += joint[k][e][j];
-  const int64_t at = (row * p.heads + blockIdx.x) * d + 4 * e;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float r = total == 0.f ? 0.f : y[j] / total;
-    if (p.y_f32) static_cast<float*>(p.y)[at + j] = r;
-    else static_cast<_Float16*>(p.y)[at + j] = static_cast<_Float16>(r);
-  }
+  for (int j = 0; j < 4; ++j) y[j] = total == 0.f ? 0.f : y[j] / total;
+  store_y(p, head * d + at, y);
 }
 
 }  // namespace pesti
@@ -82,34 +118,60 @@ int check(const pesti_kv_cache* cache, int64_t rows, int64_t heads, int64_t max_
   return PESTI_OK;
 }
 
-// Workgroups per KV head, and parts that a sequence of up to max_length tokens
-// is split into, none of under kMinPartTiles tiles.  Few rows: about four
-// workgroups a compute unit, all resident at once (one row of 131071 binary16
-// tokens, 8 KV heads of 128: 104 us so, 111 at nine).  Many rows, whose lengths
-// differ: about nine, so that what ends early makes room (48 rows up to 8191 in 8
-// bits: 102 us so, 106 at four).
+// Workgroups per KV head.
 int64_t head_blocks(const pesti_kv_cache* cache, int64_t heads) {
   const int64_t group = heads / cache->kv_heads, each = 8 * pesti_attn::head_tiles(group, cache->head_dim);
   return (group + each - 1) / each;
 }
-int64_t splits_of(const pesti_kv_cache* cache, int64_t rows, int64_t heads, int64_t max_length) {
-  const int64_t base = rows * cache->kv_heads * head_blocks(cache, heads);
-  const int64_t most = (max_length + pesti::kTile * pesti::kMinPartTiles - 1) / (pesti::kTile * pesti::kMinPartTiles);
-  const int64_t target = rows >= pesti::kManyRows ? 2304 : 1024;
+// Parts that a sequence of up to max_length tokens is split into, and wavefronts
+// of a workgroup.  All binary16 and 8 KV heads of 128 unless said, joining
+// included:
+//   short   one part of up to four tiles for each of eight wavefronts: no joining
+//     (32 rows up to 512: 13.4 us, 19.0 in parts; 512 tokens of 2 heads of 64: 8.1
+//     and 9.9)
+//   longer  parts of eight tiles, two of each of four wavefronts; of four tiles
+//     where the launch has no more workgroups than compute units that way (2048
+//     tokens: 11.3 us, 12.4 with eight)
+//   long    as many parts as bring the launch to two workgroups a compute unit, all
+//     resident at once (131071 tokens: 98 us, 104 at four; 32768: 31.5 and 39.7);
+//     three for some rows of different lengths (8 rows up to 4096: 22 us, 24.5 at
+//     two and 27 at four), nine for many, so that what ends early makes room (48 rows
+//     up to 8191 in 8 bits: 98 us, 106 at four, 117 at three)
+struct Split {
+  int64_t parts, part_tiles;
+  int waves;
+};
+Split split_of(const pesti_kv_cache* cache, int64_t rows, int64_t heads, int64_t max_length) {
+  const int64_t base = rows * cache->kv_heads * head_blocks(cache, heads), tiles = (max_length + pesti::kTile - 1) / pesti::kTile;
+  const int64_t nt = pesti_attn::head_tiles(heads / cache->kv_heads, cache->head_dim);
+  const int most_waves = pesti::attn_most_waves(static_cast<int>(cache->head_dim), static_cast<int>(nt));
+  if (tiles <= pesti::kWholeTiles * most_waves) return Split{1, tiles, tiles > 4 ? most_waves : 4};
+  const int64_t least = base * ((tiles + 3) / 4) <= 256 ? 4 : 8, most = (tiles + least - 1) / least;
+  const int64_t target = rows <= 2 ? 512 : (rows < pesti::kManyRows ? 768 : 2304);
   int64_t s = base > 0 ? (target + base - 1) / base : 1;
   s = s < most ? s : most;
-  return s < pesti::kMaxParts ? s : pesti::kMaxParts;
+  s = s < pesti::kMaxParts ? s : pesti::kMaxParts;
+  const int64_t part = (tiles + s - 1) / s;
+  return Split{s, part > least ? part : least, 4};
 }
 int64_t workspace_of(const pesti_kv_cache* cache, int64_t rows, int64_t heads, int64_t splits) {
   return splits <= 1 ? 0 : rows * heads * splits * (cache->head_dim + 2) * 4;
 }
 
-template <int D4>
 int join(const pesti::AttnArgs& p, int64_t rows, hipStream_t st) {
   pesti::AttnArgs args = p;
-  void* params[] = {&args};
-  return pesti_kv::launch(reinterpret_cast<const void*>(&pesti::attn_join_kernel<D4>),
-                          dim3(static_cast<unsigned>(p.heads), static_cast<unsigned>(rows)), dim3(256), params, 0, st);
+  int64_t threads = rows * p.heads * (p.kv.head_dim / 4);
+  void* params[] = {&args, &threads};
+  if (p.splits <= pesti::kFewParts)
+    return pesti_kv::launch(reinterpret_cast<const void*>(&pesti::attn_join_few_kernel), dim3(static_cast<unsigned>((threads + 255) / 256)),
+                            dim3(256), params, 0, st);
+  const int d = p.kv.head_dim, lanes = d > 64 && p.splits <= 64 ? 32 : (d > 32 && p.splits <= 128 ? 16 : 8);
+  const void* kernel = lanes == 32 ? reinterpret_cast<const void*>(&pesti::attn_join_kernel<32>)
+                                   : (lanes == 16 ? reinterpret_cast<const void*>(&pesti::attn_join_kernel<16>)
+                                                  : reinterpret_cast<const void*>(&pesti::attn_join_kernel<8>));
+  return pesti_kv::launch(kernel, dim3(static_cast<unsigned>((d + 4 * lanes - 1) / (4 * lanes)), static_cast<unsigned>(p.heads),
+                                       static_cast<unsigned>(rows)),
+                          dim3(256), params, 0, st);
 }
 
 }  // namespace
@@ -118,7 +180,7 @@ extern "C" {
 
 int64_t pesti_attn_paged_workspace_bytes(const pesti_kv_cache* cache, int64_t rows, int64_t heads, int64_t max_length) {
   const int st = check(cache, rows, heads, max_length);
-  return st != PESTI_OK ? st : workspace_of(cache, rows, heads, splits_of(cache, rows, heads, max_length));
+  return st != PESTI_OK ? st : workspace_of(cache, rows, heads, split_of(cache, rows, heads, max_length).parts);
 }
 
 int pesti_attn_paged(const pesti_kv_cache* cache, const pesti_kv_table* table, int64_t layer, int64_t rows, int64_t heads,
@@ -138,7 +200,8 @@ int pesti_attn_paged(const pesti_kv_cache* cache, const pesti_kv_table* table, i
   if (!pesti_host::aligned(q, 16) || !pesti_host::aligned(y, 16) ||
       (q_stride * (q_format == PESTI_FMT_F32 ? 4 : 2)) % 16 != 0 || !pesti_host::aligned(seq_ids, 4))
     return PESTI_ERR_ALIGN;
-  const int64_t splits = splits_of(cache, rows, heads, max_length), need = workspace_of(cache, rows, heads, splits);
+  const Split split = split_of(cache, rows, heads, max_length);
+  const int64_t splits = split.parts, need = workspace_of(cache, rows, heads, splits);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return PESTI_ERR_WORKSPACE;
     if (!pesti_host::aligned(workspace, 16)) return PESTI_ERR_ALIGN;
@@ -167,16 +230,13 @@ int pesti_attn_paged(const pesti_kv_cache* cache, const pesti_kv_table* table, i
   p.group = static_cast<int32_t>(heads / cache->kv_heads);
   p.head_blocks = static_cast<int32_t>(head_blocks(cache, heads));
   p.splits = static_cast<int32_t>(splits);
-  const int64_t tiles = (max_length + pesti::kTile - 1) / pesti::kTile, part = (tiles + splits - 1) / splits;
-  p.part_tiles = static_cast<int32_t>(part > pesti::kMinPartTiles ? part : pesti::kMinPartTiles);
+  p.part_tiles = static_cast<int32_t>(split.part_tiles);
+  p.waves = split.waves;
   p.q_f32 = q_format == PESTI_FMT_F32;
   p.y_f32 = y_format == PESTI_FMT_F32;
   const hipStream_t sh = static_cast<hipStream_t>(stream);
   st = i8 ? pesti_attn::launch_i8(p, rows, sh) : pesti_attn::launch_f16(p, rows, sh);
-  if (st != PESTI_OK || splits <= 1) return st;
-  if (cache->head_dim <= 32) return join<8>(p, rows, sh);
-  if (cache->head_dim <= 64) return join<16>(p, rows, sh);
-  return cache->head_dim <= 128 ? join<32>(p, rows, sh) : join<64>(p, rows, sh);
+  return st != PESTI_OK || splits <= 1 ? st : join(p, rows, sh);
 }
 
 }  // extern "C"

@@ -509,7 +509,7 @@ int pesti_dequant_i4group(int64_t rows, int64_t in_features, int64_t group, cons
  *   lengths    int32 [seqs]: tokens of each sequence (below 0 counts as 0,
  *              above width * page_size as that)
  *   refs       int32 [pages]: how many sequences hold the page; 0: it is free
- * Only entries of a sequence's ceil(length / page_size) pages are read.  A page
+ * Only entries of a sequence's ceil(length / page_size) pages count.  A page
  * number outside 0..pages-1 names no page: attention leaves its tokens out,
  * rows for it are not written, and page upkeep passes over it.
  *

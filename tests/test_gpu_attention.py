@@ -383,3 +383,44 @@ def test_a_decode_step():
         assert np.allclose(o.cpu().numpy(), oa, rtol=0, atol=1e-4)
         ha = o.cpu().numpy().astype(np.float64)
         assert np.allclose(h.cpu().numpy(), silu(ha @ w["gate"].T) * (ha @ w["up"].T), rtol=1e-4, atol=1e-4)
+
+
+# how a sequence is cut and its parts are joined: one part of eight wavefronts, up to 8 parts by threads, more by
+# workgroups of 128, 64 or 32 dimensions; parts of 4 tiles and of 8; rows that lack most of the parts
+CUTS = [(32, 1, 3, 16, 200), (64, 2, 7, 16, 1000), (64, 8, 2, 32, 5000), (128, 8, 4, 64, 900), (128, 4, 2, 64, 9000), (96, 1, 4, 32, 3000),
+        (256, 1, 8, 64, 6000), (160, 2, 3, 128, 40000), (32, 1, 20, 64, 60000), (192, 12, 1, 16, 1100)]
+
+
+@pytest.mark.parametrize("d,kv,group,page,longest", CUTS)
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_cuts(d, kv, group, page, longest, rows):
+    announce(f"attend cut d {d} kv {kv} group {group} page {page} longest {longest} rows {rows}")
+    rng = rng_of(17, d, longest, rows)
+    longest = longest // (1 if rows == 1 else (3 if rows == 5 else 20))
+    lengths = [longest] + [int(n) for n in rng.integers(0, longest // 2 + 1, rows - 1)]
+    if rows > 2:
+        lengths[1:3] = [0, 1]
+    width = -(-longest // page)
+    c = Cache(rng, "i8row" if kv == 8 else "f16", 1, sum(-(-n // page) for n in lengths) + 1, page, kv, d, rows, width, lengths)
+    g = OnGpu(c)
+    q = queries(rng, rows, kv * group, d)
+    for bound in (longest, 3 * longest + 7, max(1, longest // 5)):
+        check(g, q, d ** -0.5, max_length=bound)
+
+
+@pytest.mark.parametrize("longest", [300, 2000, 9000, 50000])
+def test_a_nan_in_one_part_reaches_its_heads_alone(longest):
+    announce(f"attend NaN in a part, {longest} tokens")
+    rng = rng_of(18, longest)
+    c = Cache(rng, "f16", 1, -(-longest // 64) * 2, 64, 2, 64, 2, -(-longest // 64), [longest, longest - 5])
+    at = c.table[0, (longest // 3) // 64]
+    c.k[0, at, 1, (longest // 3) % 64, 5] = np.nan
+    g = OnGpu(c)
+    q = queries(rng, 2, 6, 64)
+    y = attend(g, 0, q, 0.125)
+    assert np.isnan(y[0, 3:]).all() and not np.isnan(y[0, :3]).any() and not np.isnan(y[1]).any()
+    c.k[0, at, 1, (longest // 3) % 64, 5] = -np.inf   # scores of +inf or -inf by the sign of q
+    g = OnGpu(c)
+    y = attend(g, 0, q, 0.125)
+    for h in range(3, 6):
+        assert np.isnan(y[0, h]).all() if q[0, h, 5] < 0 else not np.isnan(y[0, h]).any()
