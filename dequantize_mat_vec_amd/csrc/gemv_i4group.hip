@@ -6,16 +6,16 @@
 // packed addition of -(1024 + z): q - z exactly, 9 vector instructions for 8
 // weights.  Two kernels multiply them:
 //
-//   one or two columns of x   on the vector ALUs, with one fma of a binary16 and
-//     a float32 factor per weight and column.  x stays in registers as it is: a
-//     lane holds the same 32 (or 64) elements for every row it serves, so
-//     nothing is staged and a short launch is one memory round trip.
-//   more columns              on the matrix cores, v_mfma_f32_16x16x32_f16, with
-//     x as the 16-row operand and 16 rows of W as the columns.  Rows 0-7 of x
-//     are the first binary16 parts of up to eight columns, rows 8-15 what these
-//     leave, 2^11 times as large.  A column of the result is one row of W in all
-//     lanes that hold it, so the lane that unpacks a row's codes also has the
-//     scales that its sums take.
+//   few products (one column, or a small matrix)   on the vector ALUs, with one
+//     fma of a binary16 and a float32 factor per weight and column.  x stays in
+//     registers as it is: a lane holds the same 32 (or 64) elements of one or two
+//     columns for every row it serves, so nothing is staged and a short launch is
+//     one memory round trip.
+//   more   on the matrix cores, v_mfma_f32_16x16x32_f16, with x as the 16-row
+//     operand and 16 rows of W as the columns.  Rows 0-7 of x are the first
+//     binary16 parts of up to eight columns, rows 8-15 what these leave, 2^11 times
+//     as large.  A column of the result is one row of W in all lanes that hold it,
+//     so the lane that unpacks a row's codes also has the scales that its sums take.
 //
 // In both a group's sum is finished in float32 and takes its scale in one fma.
 #include <type_traits>
@@ -118,8 +118,8 @@ __device__ __forceinline__ uint32_t i4_magic() {
 #endif
 
 // ---------------------------------------------------------------------------
-// One or two columns: L lanes per row, J dwords (8 weights) a lane, R rows a
-// lane group (PAIR: a row of each matrix).  A lane's dwords lie L apart, so a
+// Few products: L lanes per row, J dwords (8 weights) a lane, R rows a lane group
+// (PAIR: a row of each matrix), B columns, other workgroups for the next ones.  A lane's dwords lie L apart, so a
 // load of codes, and of the 32 bytes of x behind each, is one run of memory.
 // Rows longer than 8 J L weights (L = 64) are walked in passes.  A workgroup
 // takes slabs of rows in turn; the next slab's codes are in flight under the
@@ -131,6 +131,7 @@ __global__ __launch_bounds__(256) void gemv_i4group_few_kernel(I4Args p) {
   static_assert(!PAIR || R == 2, "a pair is two rows");
   constexpr int kGroups = 4 * 64 / L, kRows = PAIR ? kGroups : kGroups * R;   // lane groups, rows of y per slab
   const I4Op o = p.op[blockIdx.y];
+  const int col0 = blockIdx.z * B, cols = p.batch - col0;   // the last workgroups of an odd batch have one column twice
   const int sub = threadIdx.x & (L - 1), mine = static_cast<int>(threadIdx.x / L);
   const int64_t slabs = (o.out + kRows - 1) / kRows;
   if (blockIdx.x >= slabs) return;
@@ -171,7 +172,7 @@ __global__ __launch_bounds__(256) void gemv_i4group_few_kernel(I4Args p) {
         const int d = (pass * J + j) * L + sub;
         x[b][j][0] = x[b][j][1] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (d < dwords) {
-          const f32x4* src = reinterpret_cast<const f32x4*>(o.x + static_cast<int64_t>(b) * o.in + 8 * d);
+          const f32x4* src = reinterpret_cast<const f32x4*>(o.x + static_cast<int64_t>(col0 + (b < cols ? b : 0)) * o.in + 8 * d);
           x[b][j][0] = src[0];
           x[b][j][1] = src[1];
         }
@@ -221,14 +222,16 @@ __global__ __launch_bounds__(256) void gemv_i4group_few_kernel(I4Args p) {
         const int64_t row = slab * kRows + mine;
         if (row < o.out)
 #pragma unroll
-          for (int b = 0; b < B; ++b) o.y[b * o.out + row] = acc[0][b] / (1.f + expf(-acc[0][b])) * acc[R - 1][b];
+          for (int b = 0; b < B; ++b)
+            if (b < cols) o.y[(col0 + b) * o.out + row] = acc[0][b] / (1.f + expf(-acc[0][b])) * acc[R - 1][b];
       } else {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const int64_t row = slab * kRows + mine + kGroups * r;
           if (row < o.out)
 #pragma unroll
-            for (int b = 0; b < B; ++b) o.y[b * o.out + row] = acc[r][b] + bias[r];
+            for (int b = 0; b < B; ++b)
+              if (b < cols) o.y[(col0 + b) * o.out + row] = acc[r][b] + bias[r];
         }
       }
     }
@@ -311,7 +314,7 @@ void gemv_i4group_kernel(I4Args p) {
 
   // Chunks c0 .. c0 + count - 1 of x: 16 lanes take a chunk of a column.
   auto stage = [&](int c0, int count) {
-    constexpr int kAhead = 2;
+    constexpr int kAhead = 4;
     const int items = count * batch;
     for (int base = wave * 4 + g; base - g < items; base += waves * 4 * kAhead) {
       f32x4 v[kAhead][2];
@@ -686,9 +689,11 @@ int device() {
 
 // How an op is computed: it depends on the op and the batch alone, so an op of a
 // group has the bits of its single call.  Measured with groups of 128, in us:
-//   few columns   896 x 896, one column 2.8 on the vector ALUs, 4.4 on the matrix
-//     cores; 4864 x 896, two: 4.2 and 5.4; 9728 x 896, two: 6.3 and 5.4; 4864 x
-//     4096, one: 8.1 and 8.2, two: 13.7 and 9.3
+//   few products  (columns in pairs on the vector ALUs) 896 x 896, one column 2.8,
+//     4.4 on the matrix cores, eight: 3.7 and 5.3; 2432 x 896, four: 4.2 and 4.7,
+//     eight: 6.0 and 5.4; 4864 x 896, four: 6.1 and 5.7; 2048 x 4096, two: 5.3 and
+//     6.5, three: 8.6 and 7.0; 512 x 16384, eight, few workgroups on the matrix
+//     cores: 15 and 35
 //   short rows    4864 x 896, four columns: 6.0 a wavefront a tile, 6.4 dealt
 //     out; 2432 x 896: 6.0 and 4.8; 24576 x 896: 7.3 with four wavefronts a
 //     workgroup, 6.7 with eight; gate and up of 9728 x 896: 8.0 with four, 9.9
@@ -712,9 +717,10 @@ int64_t wave_bytes(int waves, bool pair, int joints) { return int64_t{waves} * (
 
 Cut cut_of(const I4Op& o, int batch, bool pair) {
   const int chunks = (o.in + pesti::kChunk - 1) / pesti::kChunk, dwords = o.in / 8;
-  const int64_t tiles = (o.out + 15) / 16, products = o.out * o.in * batch;
+  const int64_t tiles = (o.out + 15) / 16, products = o.out * o.in * batch * (pair ? 2 : 1);
+  const int64_t few = (chunks <= 8 ? 12 : (tiles > 64 ? 20 : (tiles > 32 ? 32 : 64))) << 20;
   // (the matrix kernel loads eight groups' scales at once)
-  if ((batch <= 2 && products <= (chunks <= 8 ? 12 << 20 : 20 << 20)) || o.out * o.groups < 8) {
+  if (products <= few || o.out * o.groups < 8) {
     int span = 32;   // dwords per lane group and pass: 32 x 1, 2, 4 or 64 x 4, 8
     while (span < dwords && span < 512) span *= 2;
     return Cut{kFew, 4, span, 0};
@@ -737,10 +743,10 @@ int64_t most_rows(const I4Args& p, int n_ops) {
   return rows;
 }
 
-int submit(const void* kernel, I4Args& p, int64_t blocks, int n_ops, int threads, size_t lds, hipStream_t st) {
+int submit(const void* kernel, I4Args& p, int64_t blocks, int n_ops, int threads, size_t lds, hipStream_t st, int columns = 1) {
   void* params[] = {&p};
-  const hipError_t e = hipLaunchKernel(kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(n_ops)), dim3(threads),
-                                       params, lds, st);
+  const hipError_t e = hipLaunchKernel(kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(n_ops), static_cast<unsigned>(columns)),
+                                       dim3(threads), params, lds, st);
   return e == hipSuccess ? PESTI_OK : PESTI_ERR_LAUNCH;
 }
 
@@ -751,7 +757,7 @@ int launch_few(I4Args& p, int n_ops, hipStream_t st) {
     constexpr int R = decltype(r)::value;
     const int64_t slabs = (rows + groups * (PAIR ? 1 : R) - 1) / (groups * (PAIR ? 1 : R));
     return submit(reinterpret_cast<const void*>(&pesti::gemv_i4group_few_kernel<B, L, J, R, PAIR>), p, slabs < 2048 ? slabs : 2048,
-                  n_ops, 256, 0, st);
+                  n_ops, 256, 0, st, (p.batch + B - 1) / B);
   };
   if constexpr (PAIR) {
     return run(std::integral_constant<int, 2>{});
@@ -795,19 +801,8 @@ int launch_many(I4Args& p, int n_ops, const Cut& c, hipStream_t st) {
 
 template <bool PAIR>
 int launch_cut(I4Args& p, int n_ops, const Cut& c, hipStream_t st) {
-  if (c.way == kFew) {
-    for (int b = 0; b < p.batch; b += 2) {   // two columns a launch
-      I4Args q = p;
-      q.batch = p.batch - b < 2 ? 1 : 2;
-      for (int i = 0; i < n_ops; ++i) {
-        q.op[i].x += static_cast<int64_t>(b) * q.op[i].in;
-        q.op[i].y += b * q.op[i].out;
-      }
-      const int r = q.batch == 1 ? launch_few_span<1, PAIR>(q, n_ops, c.phase, st) : launch_few_span<2, PAIR>(q, n_ops, c.phase, st);
-      if (r != PESTI_OK) return r;
-    }
-    return PESTI_OK;
-  }
+  if (c.way == kFew)
+    return p.batch == 1 ? launch_few_span<1, PAIR>(p, n_ops, c.phase, st) : launch_few_span<2, PAIR>(p, n_ops, c.phase, st);
   if (p.shift == 5) return launch_many<4, PAIR>(p, n_ops, c, st);
   if (p.shift == 6) return launch_many<2, PAIR>(p, n_ops, c, st);
   return launch_many<1, PAIR>(p, n_ops, c, st);

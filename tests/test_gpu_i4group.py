@@ -337,3 +337,74 @@ def test_a_group_of_all_ways():
     torch.cuda.synchronize()
     for op, y1 in zip(ops, singles):
         assert torch.equal(op[6], y1), op[:2]
+
+
+# large enough for the matrix cores: a wavefront a tile, dealt out, in phases, rows of less than a chunk
+LARGE = [(5, 4801, 800, 32), (5, 2101, 2080, 64), (8, 1045, 8224, 128), (8, 50003, 64, 32), (7, 60005, 32, 64)]
+
+
+@pytest.mark.parametrize("batch,out,inf,group", LARGE)
+@pytest.mark.parametrize("size", [1e-38, 1e-20, 1.0, 3e4, 1e30])
+def test_magnitudes_on_the_matrix_cores(batch, out, inf, group, size):
+    announce(f"i4group {batch}x{out}x{inf} x of {size}")
+    rng = case_rng(16, out)
+    x = (rng.standard_normal((batch, inf)) * size).astype(np.float32)
+    x[1] *= 1e-6   # columns of their own sizes
+    x[2, :32] *= 1e4
+    check(i4_matrix(rng, out, inf, group), out, inf, group, x)
+
+
+@pytest.mark.parametrize("batch,out,inf,group", LARGE)
+def test_values_on_the_matrix_cores(batch, out, inf, group):
+    """Zero points of any value, scales of every kind, a row of zero weights, an element 2^27 times the others on a zero
+    weight, infinities and NaN in columns of their own."""
+    announce(f"i4group {batch}x{out}x{inf} values")
+    rng = case_rng(17, out)
+    packed, scales, zeros = m = i4_matrix(rng, out, inf, group)
+    zeros[:50] = rng.integers(0, 256, zeros[:50].shape, dtype=np.uint8)
+    scales[60], scales[61], scales[62], scales[63] = 0, -0.5, 6e-8, 65504
+    packed[70:90], zeros[70:90] = 0x99, 9
+    packed[:, 8], zeros[100:, 0] = (packed[:, 8] & 0xF0) | 7, 7   # weight 16 of rows from 100 on
+    x = rng.standard_normal((batch, inf)).astype(np.float32)
+    x[1, 16] = 2.0 ** 27
+    x[2, 21], x[3, 5], x[3, 6], x[4, 30] = np.inf, np.inf, -np.inf, np.nan
+    bias = rng.standard_normal(out).astype(np.float32)
+    y = run(m, out, inf, group, x, bias)
+    w = i4_weights(*m, inf, group)
+    none = (w == 0).all(1)
+    assert none[60] and np.array_equal(y[:2, none].astype(np.float32), np.broadcast_to(bias[none], (2, none.sum())))
+    fine = [b for b in range(batch) if b not in (2, 3, 4)]
+    xs = x[fine].astype(np.float64)
+    exact, tol = xs @ w.T, i4_tolerance(w, xs) + 2.0 ** -23 * np.abs(bias)
+    exact = exact + bias.astype(np.float64)
+    err = np.abs(y[fine] - exact)
+    assert np.all(err <= tol + 2.0 ** -24 * np.abs(exact)), float((err / tol).max())
+    # an infinity times a weight is one of the weight's sign, times a zero weight NaN
+    hit = w[:, 21]
+    assert np.all(y[2][hit > 0] == np.inf) and np.all(y[2][hit < 0] == -np.inf) and np.isnan(y[2][hit == 0]).all()
+    one, two = w[:, 5], w[:, 6]
+    assert np.isnan(y[3][one * two >= 0]).all() and np.all(y[3][(one > 0) & (two < 0)] == np.inf)
+    assert np.isnan(y[4]).all()
+
+
+@pytest.mark.parametrize("batch,out,inf,group", LARGE)
+def test_surroundings_on_the_matrix_cores(batch, out, inf, group):
+    announce(f"i4group {batch}x{out}x{inf} surroundings")
+    import torch
+    rng = case_rng(18, out)
+    m = i4_matrix(rng, out, inf, group)
+    x = to_dev(rng.standard_normal((batch, inf)).astype(np.float32))
+    ys = []
+    for fill in (0, 255):
+        dev = []
+        for a in m:
+            a = np.ascontiguousarray(a)
+            whole = torch.full((a.nbytes + 512,), fill, dtype=torch.uint8, device="cuda")
+            whole[256:256 + a.nbytes] = torch.from_numpy(a.reshape(-1).view(np.uint8)).cuda()
+            dev.append(whole[256:256 + a.nbytes])
+        buf, y = guarded_y(batch * out)
+        dmv.pesti_gemv_i4group(out, inf, group, dev[0], dev[1].view(torch.float16), dev[2], x, y, None, batch)
+        torch.cuda.synchronize()
+        assert guards_intact(buf, batch * out)
+        ys.append(y.cpu())
+    assert torch.equal(*ys)
