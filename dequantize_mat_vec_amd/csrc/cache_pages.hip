@@ -19,16 +19,28 @@ namespace pesti {
 constexpr int kPlanThreads = 1024;
 constexpr int kRun = 32;   // pages per thread and round of a plan
 
+// v plus what DPP brings of it: the lanes whose bit is in ROWS from the place that
+// CTRL names, the others 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t plus_dpp(int64_t v) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CTRL, ROWS, 0xF, false);
+  v += static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+#endif
+  return v;
+}
+
 // Exclusive sum over a plan's threads; *total gets the sum.
-template <typename T>
-__device__ __forceinline__ T plan_scan(T v, T* total, T* wave_sums) {
+__device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* total, int64_t* wave_sums) {
+  typedef int64_t T;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  T s = v;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const T o = __shfl_up(s, d, 64);
-    if (lane >= d) s += o;
-  }
+  T s = plus_dpp<0x111, 0xF>(v);   // rows of 16 lanes: one, two, four, eight lanes up
+  s = plus_dpp<0x112, 0xF>(s);
+  s = plus_dpp<0x114, 0xF>(s);
+  s = plus_dpp<0x118, 0xF>(s);
+  s = plus_dpp<0x142, 0xA>(s);     // rows 1 and 3: the last lane of the row before
+  s = plus_dpp<0x143, 0xC>(s);     // rows 2 and 3: lane 31
   __syncthreads();   // the sums of the call before have been read
   if (lane == 63) wave_sums[wave] = s;
   __syncthreads();

@@ -329,3 +329,23 @@ def test_a_captured_beam_step():
         plain(new)
         assert int(g.status[0]) == 0
         g.same()
+
+
+@pytest.mark.parametrize("power", [0, -100, -127, -138, 90])
+def test_ties_into_8_bits(power):
+    """Halves of a scale that is a power of two: exactly between two codes, away from zero, also where the scale is a
+    subnormal; a last row of values a rounding beside them."""
+    announce(f"append ties, scale 2^{power}")
+    rng = rng_of(31, power + 200)
+    g = OnGpu(Cache(rng, "i8row", 1, 8, 16, 2, 64, 1, 4, (50,)))
+    x = (rng.integers(-253, 254, (40, 2, 64)) / 2).astype(np.float64)
+    x[..., 0] = 127
+    x = np.ldexp(x, power).astype(np.float32)
+    beside = np.nextafter(x, np.float32(0))
+    beside[..., 0] = x[..., 0]
+    for v in (x, beside):
+        seq, pos = np.zeros(40, np.int32), np.arange(5, 45, dtype=np.int32)
+        dmv.pesti_cache_append(g.cache, g.table, 0, 40, to_dev(v.reshape(40, -1)), to_dev(-v.reshape(40, -1)), seq_ids=to_dev(seq),
+                               positions=to_dev(pos))
+        g.c.append(0, v, -v, seq, pos)
+        g.same()
