@@ -312,18 +312,20 @@ void gemv_i4group_kernel(I4Args p) {
   float* joint = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lower + 8 * phase) + waves * R * kWindowBytes);
   const int slot = n < 8 ? (n < batch ? n : batch - 1) : batch + (n - 8 < batch ? n - 8 : batch - 1);
 
-  // Chunks c0 .. c0 + count - 1 of x: 16 lanes take a chunk of a column.
-  auto stage = [&](int c0, int count) {
+  // count chunks of x from c0 on, into the places from pos on: 16 lanes take a chunk
+  // of a column.  Where chunks are dealt out a wavefront stages those that it
+  // multiplies itself, into places of its own, and waits for no other.
+  auto stage = [&](int c0, int pos, int count) {
     constexpr int kAhead = 4;
-    const int items = count * batch;
-    for (int base = wave * 4 + g; base - g < items; base += waves * 4 * kAhead) {
+    const int items = count * batch, start = ROWS ? wave * 4 + g : g, apart = ROWS ? waves * 4 : 4;
+    for (int base = start; base - g < items; base += apart * kAhead) {
       f32x4 v[kAhead][2];
       int at[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int item = base + k * waves * 4;
+        const int item = base + k * apart;
         const int c = item * p.batch_magic >> 16, b = item - c * batch, i = (c0 + c) * kChunk + 8 * n;
-        at[k] = item < items ? c * 16 + n : -1;
+        at[k] = item < items ? (pos + c) * 16 + n : -1;
         v[k][0] = v[k][1] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (item < items && i < in) {
           const f32x4* src = reinterpret_cast<const f32x4*>(o.x + static_cast<int64_t>(b) * in + i);
@@ -333,42 +335,61 @@ void gemv_i4group_kernel(I4Args p) {
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        if (wave * 4 + (base - g - wave * 4) + k * waves * 4 >= items) break;   // the same for the wavefront
-        const int item = base + k * waves * 4;
+        if (base - g + k * apart >= items) break;   // the same for the wavefront
+        const int item = base + k * apart;
         const int c = item * p.batch_magic >> 16, b = item - c * batch;
+        auto chunk_max = [](float m) {   // over the 16 lanes
+          m = fmaxf(m, dpp<0xB1>(m));
+          m = fmaxf(m, dpp<0x4E>(m));
+          m = fmaxf(m, dpp<0x141>(m));
+          return fmaxf(m, dpp<0x140>(m));
+        };
         float top = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float m = __builtin_fabsf(v[k][j / 4][j % 4]);
-          top = m < INFINITY && m > top ? m : top;
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(v[k][j / 4][j % 4]));
+        top = chunk_max(top);
+        const bool endless = __any(top == INFINITY);
+        if (endless) {   // the largest finite one
+          top = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float m = __builtin_fabsf(v[k][j / 4][j % 4]);
+            top = m < INFINITY && m > top ? m : top;
+          }
+          top = chunk_max(top);
         }
-        top = fmaxf(top, dpp<0xB1>(top));    // over the 16 lanes
-        top = fmaxf(top, dpp<0x4E>(top));
-        top = fmaxf(top, dpp<0x141>(top));
-        top = fmaxf(top, dpp<0x140>(top));
         const uint32_t bits = __builtin_bit_cast(uint32_t, top);
         int up = 14 + 127 - static_cast<int>(bits >> 23);   // brings the largest to [2^14, 2^15)
         up = bits == 0 ? 0 : (up > 126 ? 126 : up);
         const float lift = __builtin_bit_cast(float, static_cast<uint32_t>(up + 127) << 23);
         h8 hi, lo;
+        // The first part towards zero, two at once; the second then to nearest, of
+        // what is left: below 2^-10 of the value, so that its 11 bits are within
+        // 2^-22 too.
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x = v[k][j / 4][j % 4] * lift;
-          const _Float16 h = static_cast<_Float16>(x);
-          const float rest = (x - static_cast<float>(h)) * 0x1p11f;
-          const int e = 2 * (j % 4) + j / 4;   // codes j and j + 4 share a register
-          hi[e] = h;
-          lo[e] = static_cast<_Float16>(rest - rest == 0.f ? rest : 0.f);   // an infinity is all in the first part
+        for (int j = 0; j < 4; ++j) {   // codes j and j + 4 share a register
+          const float x0 = v[k][0][j] * lift, x1 = v[k][1][j] * lift;
+          const h2 h = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_pkrtz(x0, x1));
+          float r0 = (x0 - static_cast<float>(h[0])) * 0x1p11f, r1 = (x1 - static_cast<float>(h[1])) * 0x1p11f;
+          if (endless) {   // an infinity is all in the first part
+            r0 = r0 - r0 == 0.f ? r0 : 0.f;
+            r1 = r1 - r1 == 0.f ? r1 : 0.f;
+          }
+          hi[2 * j] = h[0];
+          hi[2 * j + 1] = h[1];
+          lo[2 * j] = static_cast<_Float16>(r0);
+          lo[2 * j + 1] = static_cast<_Float16>(r1);
         }
         if (at[k] >= 0) {
           h8* x = reinterpret_cast<h8*>(lds) + at[k] * stride + b;
           x[0] = hi;
           x[batch] = lo;
-          if (n == 0) lower[8 * c + b] = __builtin_bit_cast(float, static_cast<uint32_t>(127 - up) << 23);
+          if (n == 0) lower[8 * (pos + c) + b] = __builtin_bit_cast(float, static_cast<uint32_t>(127 - up) << 23);
         }
       }
     }
-    __syncthreads();
+    if constexpr (ROWS) __syncthreads();
+    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
 
   const int64_t all_groups = out * o.groups;   // 8 at least
@@ -445,7 +466,7 @@ void gemv_i4group_kernel(I4Args p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) total[r][i] = 0.f;
   };
-  // c: chunk within the phase; gw: its first group within the window
+  // c: place of the chunk; gw: its first group within the window
   auto multiply = [&](int c, int gw, const u32x4 (&d)[R]) {
     const h8* x = reinterpret_cast<const h8*>(lds) + (c * 16 + g) * stride + slot;
     h8 xf[4];
@@ -558,14 +579,14 @@ void gemv_i4group_kernel(I4Args p) {
     const int here = chunks - c0 < phase ? chunks - c0 : phase;
     const int share = ROWS ? here : (here + waves - 1) / waves, first = ROWS ? 0 : wave * share;
     const int count = here - first < share ? (here - first > 0 ? here - first : 0) : share;
+    const int pos = PHASES ? wave * (phase / waves) : first;
     const int g_first = (c0 + first) * kChunk >> p.shift;
     int32_t here_tile = tile < 0 ? 0 : tile;
     int row = row_in(here_tile), turn = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) load(here_tile, row * half, c0 + first + u, w[u]);
     fetch(here_tile, row, g_first);
-    if (PHASES && c0 > 0) __syncthreads();   // x of the phase before has been read
-    stage(c0, here);
+    stage(c0 + first, pos, count);
     if (tile < 0) break;
     while (true) {
       const int32_t next = here_tile + apart < tiles ? here_tile + apart : here_tile;
@@ -583,7 +604,7 @@ void gemv_i4group_kernel(I4Args p) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             if (i + u >= end) break;
-            multiply(first + i + u, ((c0 + first + i + u) * kChunk >> p.shift) - gw0, w[u]);
+            multiply(pos + i + u, ((c0 + first + i + u) * kChunk >> p.shift) - gw0, w[u]);
             const bool same = i + u + U < count;
             load(same ? here_tile : next, (same ? row : next_row) * half, c0 + first + (same ? i + u + U : u), w[u]);
             __builtin_amdgcn_sched_barrier(0);   // (steps side by side cost registers, and wavefronts)
@@ -734,7 +755,8 @@ Cut cut_of(const I4Op& o, int batch, bool pair) {
   // the fewer times x is staged, and the less of it at once.
   const int64_t most = pair ? 4 : 8, per_unit = (tiles + 255) / 256;
   const int each = static_cast<int>(per_unit < most ? per_unit : most);
-  return Cut{kPhases, waves, static_cast<int>((kMost - wave_bytes(waves, pair, each)) / x_bytes(1, batch)), each};
+  const int phase = static_cast<int>((kMost - wave_bytes(waves, pair, each)) / x_bytes(1, batch));
+  return Cut{kPhases, waves, phase / waves * waves, each};   // (8 chunks of 8 columns are 35 KiB of the 64 that are left at least)
 }
 
 int64_t most_rows(const I4Args& p, int n_ops) {
