@@ -446,13 +446,14 @@ int pesti_gemm_experts_swiglu(int32_t format, int64_t rows, int64_t experts,
  *           last group of a row may be short), else PESTI_ERR_SHAPE
  *
  * x, y, bias, batch, stream and errors as for pesti_gemv_q8_0; packed 16-byte
- * aligned, scales 2.  The codes less their zero points are exact binary16
- * integers and are multiplied on the matrix cores with x in two binary16
- * parts: x is scaled by a power of two that brings the largest finite |x| of a
- * column (of each 128-weight multiple of it that is staged at once) to
- * [2^14, 2^15), and what the first part leaves is held 2^11 times as large in
- * the second, which adds at most 2^-22 |x_i| + 2^-50 max|x| per element to the
- * float32 error.  Group sums are float32 and take their scale once.
+ * aligned, scales 2.  The codes less their zero points are exact integers.  Ops
+ * of few products (a single column, or a small matrix; by sizes and batch
+ * alone) multiply them with float32 x on the vector ALUs, the others on the
+ * matrix cores with x in two binary16 parts: each run of 128 weights of a column
+ * is scaled by a power of two that brings its largest finite |x| to [2^14,
+ * 2^15), and what the first part leaves is held 2^11 times as large in the
+ * second, which adds at most 2^-22 |x_i| + 2^-50 max|x| (of the run) per element
+ * to the float32 error.  Group sums are float32 and take their scale once.
  *
  * pesti_gemv_group_i4group: up to PESTI_MAX_GROUP such mat-vecs of one group
  * size and batch in one launch, as pesti_gemv_group; every op's y has the bits
@@ -583,7 +584,7 @@ int pesti_cache_append(const pesti_kv_cache* cache, const pesti_kv_table* table,
  * y 16-byte aligned, q_stride >= heads * head_dim and its bytes a multiple of
  * 16.  A row without tokens (length 0, or no valid page) is zeros, as is one
  * whose every score is -infinity; a NaN of q, K or V makes NaN of the heads
- * that it enters.
+ * that it enters, an infinity of V infinities or NaN of its dimension.
  *
  * Scores, maximum, sum and result are float32.  q times scale and the softmax's
  * weights enter the matrix cores in two binary16 parts each (22 bits), K and V
