@@ -8,7 +8,6 @@ namespace pesti {
 constexpr int kMaxParts = 256;
 constexpr int kFewParts = 8;
 constexpr int kManyRows = 32;
-constexpr int kWholeTiles = 4;   // a sequence of that many tiles a wavefront is one part
 
 // y of one row and head from its parts: part i counts 2^(max_i - max) times, one
 // without tokens (maximum -infinity, sum 0) not at all.  The parts are added in
@@ -124,19 +123,21 @@ int64_t head_blocks(const pesti_kv_cache* cache, int64_t heads) {
   return (group + each - 1) / each;
 }
 // Parts that a sequence of up to max_length tokens is split into, and wavefronts
-// of a workgroup.  All binary16 and 8 KV heads of 128 unless said, joining
-// included:
-//   short   one part of up to four tiles for each of eight wavefronts: no joining
-//     (32 rows up to 512: 13.4 us, 19.0 in parts; 512 tokens of 2 heads of 64: 8.1
-//     and 9.9)
-//   longer  parts of eight tiles, two of each of four wavefronts; of four tiles
-//     where the launch has no more workgroups than compute units that way (2048
-//     tokens: 11.3 us, 12.4 with eight)
-//   long    as many parts as bring the launch to two workgroups a compute unit, all
-//     resident at once (131071 tokens: 98 us, 104 at four; 32768: 31.5 and 39.7);
-//     three for some rows of different lengths (8 rows up to 4096: 22 us, 24.5 at
-//     two and 27 at four), nine for many, so that what ends early makes room (48 rows
-//     up to 8191 in 8 bits: 98 us, 106 at four, 117 at three)
+// of a workgroup.  In us, joining included, 8 KV heads of 128 in binary16 unless
+// said:
+//   whole   short sequences are one part and need no joining: longer ones the more
+//     workgroups there are (512 tokens of 2 heads of 64: 8.1, 8.3 in parts, 700: 9.5
+//     and 8.5; 64 rows up to 512: 20.0 and 29.3, up to 1500: 48 and 58, up to 5000:
+//     143 and 134), in eight wavefronts where each has a compute unit to itself
+//     (64 rows up to 300, two to a unit: 20.5 with eight, 14.3 with four; 40 rows
+//     up to 600 of 4 heads of 96: 10.4 and 10.8)
+//   parts   of eight tiles, two of each of four wavefronts; of four tiles where the
+//     launch has no more workgroups than compute units that way (2048 tokens: 11.3,
+//     12.4 with eight); else as many parts as bring the launch to two workgroups a
+//     compute unit, all resident at once (131071 tokens: 98, 104 at four; 32768:
+//     31.5 and 39.7); three for some rows of different lengths (8 rows up to 4096: 22,
+//     24.5 at two and 27 at four), nine for many, so that what ends early makes room
+//     (48 rows up to 8191 in 8 bits: 98, 106 at four, 117 at three)
 struct Split {
   int64_t parts, part_tiles;
   int waves;
@@ -145,7 +146,8 @@ Split split_of(const pesti_kv_cache* cache, int64_t rows, int64_t heads, int64_t
   const int64_t base = rows * cache->kv_heads * head_blocks(cache, heads), tiles = (max_length + pesti::kTile - 1) / pesti::kTile;
   const int64_t nt = pesti_attn::head_tiles(heads / cache->kv_heads, cache->head_dim);
   const int most_waves = pesti::attn_most_waves(static_cast<int>(cache->head_dim), static_cast<int>(nt));
-  if (tiles <= pesti::kWholeTiles * most_waves) return Split{1, tiles, tiles > 4 ? most_waves : 4};
+  const int64_t whole = base <= 64 ? 1024 / cache->head_dim : (base < 256 ? 24 : 64);
+  if (tiles <= whole) return Split{1, tiles, tiles > 4 && base <= 256 ? most_waves : 4};
   const int64_t least = base * ((tiles + 3) / 4) <= 256 ? 4 : 8, most = (tiles + least - 1) / least;
   const int64_t target = rows <= 2 ? 512 : (rows < pesti::kManyRows ? 768 : 2304);
   int64_t s = base > 0 ? (target + base - 1) / base : 1;
