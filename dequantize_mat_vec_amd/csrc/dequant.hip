@@ -170,22 +170,29 @@ __global__ __launch_bounds__(256) void dequant_q6_k_kernel(DequantArgs a) {
 }
 
 // i8row: a workgroup writes 8192 values in a row of memory, a dword of codes and
-// a 16-byte store per thread and step (4.5 M values: 5 us; 32 values in a row
-// of memory per thread took 20).
+// a 16-byte store per thread and step, all loads ahead of the stores (2.2 M values:
+// 4.4 us; with each step's loads behind the last one's store 6.6, with 32 values in
+// a row of memory per thread four times as long).
 __global__ __launch_bounds__(256) void dequant_i8row_kernel(DequantArgs a) {
   const uint32_t per_row = static_cast<uint32_t>(a.in / 4);   // dwords
   const int64_t first = static_cast<int64_t>(blockIdx.x) * 2048, all = a.rows * per_row;
-  const int64_t row0 = first / per_row;
-  const uint32_t skip = static_cast<uint32_t>(first - row0 * per_row);
+  const int64_t row0 = first / per_row, left = all - first;
+  const uint32_t skip = static_cast<uint32_t>(first - row0 * per_row), last = static_cast<uint32_t>(left < 2048 ? left : 2048) - 1;
   const uint32_t* q = reinterpret_cast<const uint32_t*>(a.w) + first;
+  const float* scales = a.scales + row0;
   f32x4* o = reinterpret_cast<f32x4*>(a.out) + first;
+  uint32_t v[8];
+  float s[8];
+#pragma unroll
+  for (uint32_t k = 0; k < 8; ++k) {
+    const uint32_t d = k * 256 + threadIdx.x, at = d < last ? d : last;
+    v[k] = q[at];
+    s[k] = scales[(skip + at) / per_row];
+  }
 #pragma unroll
   for (uint32_t k = 0; k < 8; ++k) {
     const uint32_t d = k * 256 + threadIdx.x;
-    if (first + d >= all) return;
-    const uint32_t v = q[d];
-    const float s = a.scales[row0 + (skip + d) / per_row];
-    o[d] = f32x4{s * sbyte<0>(v), s * sbyte<1>(v), s * sbyte<2>(v), s * sbyte<3>(v)};
+    if (d <= last) o[d] = f32x4{s[k] * sbyte<0>(v[k]), s[k] * sbyte<1>(v[k]), s[k] * sbyte<2>(v[k]), s[k] * sbyte<3>(v[k])};
   }
 }
 
