@@ -720,7 +720,9 @@ int device() {
 //     workgroup, 6.7 with eight; gate and up of 9728 x 896: 8.0 with four, 9.9
 //     with eight, 12.7 dealt out
 //   longer rows   16384 x 2048, four columns: 10.9 a wavefront a tile, 10.1 dealt
-//     out
+//     out; 32768 x 2048, eight: 12.4 and 17.8; 100000 x 1536: 26 and 46; where x
+//     leaves room for one workgroup a compute unit only if its wavefronts' rounds
+//     are full (40000 x 3200, 1.2 rounds: 34.4 and 32.5)
 //   long rows     14336 x 8192, eight columns: 40 in phases with four tiles of a
 //     workgroup, 89 with one; 73 where the columns were split over three launches
 using pesti::kDeal;
@@ -746,8 +748,11 @@ Cut cut_of(const I4Op& o, int batch, bool pair) {
     while (span < dwords && span < 512) span *= 2;
     return Cut{kFew, 4, span, 0};
   }
-  if (tiles >= (chunks <= 8 ? 256 : 2048) && x_bytes(chunks, batch) <= 48 * 1024)
-    return Cut{kRows, pair || tiles < 1024 ? 4 : 8, chunks, 0};
+  if (tiles >= (chunks <= 8 ? 256 : 2048)) {
+    const int64_t x = x_bytes(chunks, batch), rounds = (tiles + 2047) / 2048;   // of one workgroup a compute unit
+    if (x <= 64 * 1024) return Cut{kRows, pair || tiles < 1024 ? 4 : 8, chunks, 0};
+    if (x <= kMost - wave_bytes(8, pair, 0) && 4 * tiles >= 3 * 2048 * rounds) return Cut{kRows, 8, chunks, 0};
+  }
   // 128 threads store a tile of eight columns
   const int waves = chunks < 2 ? 2 : (chunks < pesti::kI4MaxWaves ? chunks : pesti::kI4MaxWaves);
   if (x_bytes(chunks, batch) <= kMost - wave_bytes(waves, pair, 1)) return Cut{kDeal, waves, chunks, 0};

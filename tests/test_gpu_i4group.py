@@ -280,7 +280,7 @@ def test_other_stream_and_captured_graph():
 # of a workgroup (the last with fewer, and more workgroups than compute units), few rows by single wavefronts
 WAYS = [(8, 5003, 4096, 128), (8, 4115, 8192, 64), (5, 9001, 8192, 128), (8, 33003, 8224, 256), (7, 4801, 16384, 32),
         (3, 4115, 28704, 128), (1, 4115, 5152, 64), (2, 4200, 800, 32), (4, 4099, 1024, 128), (6, 16500, 1024, 64),
-        (1, 12345, 1088, 32), (2, 32771, 640, 128)]
+        (1, 12345, 1088, 32), (2, 32771, 640, 128), (5, 32763, 4128, 128), (8, 57001, 1312, 32)]
 
 
 @pytest.mark.parametrize("batch,out,inf,group", WAYS)
@@ -300,7 +300,7 @@ def test_ways(batch, out, inf, group):
 
 
 @pytest.mark.parametrize("batch,out,inf,group", [(8, 4115, 4096, 128), (6, 2500, 8192, 64), (4, 9003, 8192, 32), (2, 12000, 1056, 64),
-                                                 (4, 17001, 896, 128), (5, 16400, 6176, 128)])
+                                                 (4, 17001, 896, 128), (5, 16400, 6176, 128), (8, 32760, 2080, 64), (3, 32755, 2592, 128)])
 def test_ways_of_swiglu(batch, out, inf, group):
     announce(f"i4group swiglu way of {batch}x{out}x{inf} group {group}")
     import torch
