@@ -160,6 +160,7 @@ def load(path: os.PathLike | None = None) -> ctypes.CDLL:
         fn.argtypes = args
     if path is None:
         _lib = lib
+        _link_fast_calls(lib)
     return lib
 
 
@@ -174,6 +175,27 @@ def _bind_fast_args():
     if _sized is not _tensor_args.sized:
         _tensor_args.bind(_sized, _rows)
         _sized, _rows, _current = _tensor_args.sized, _tensor_args.rows, _tensor_args.place
+
+
+def _not_made(*args):
+    """A call that is left to its function below."""
+    return None
+
+
+_call_gemv_i4group = _call_gemv_i4group_swiglu = _call_cache_append = _call_attn_paged = _not_made
+
+
+def _link_fast_calls(lib):
+    """A decode step's calls on the current stream, made by the compiled checks as a whole."""
+    global _call_gemv_i4group, _call_gemv_i4group_swiglu, _call_cache_append, _call_attn_paged
+    try:
+        from . import _tensor_args as fast
+    except ImportError:
+        return
+    fast.link(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.pesti_gemv_i4group, lib.pesti_gemv_i4group_swiglu, lib.pesti_cache_append, lib.pesti_attn_paged)))
+    _call_gemv_i4group, _call_gemv_i4group_swiglu = fast.gemv_i4group, fast.gemv_i4group_swiglu
+    _call_cache_append, _call_attn_paged = fast.cache_append, fast.attn_paged
 
 
 def _ptr(obj):
@@ -487,6 +509,10 @@ def _groups(in_features, group):
 
 def pesti_gemv_i4group(out_features, in_features, group, packed, scales, zeros, x, y, bias=None, batch=1, stream=None):
     """y = W x + bias, W in 4-bit codes with a binary16 scale per `group` weights of a row and a zero point (None: 8)."""
+    if stream is None:
+        status = _call_gemv_i4group(out_features, in_features, group, packed, scales, zeros, x, y, bias, batch)
+        if status is not None:
+            return _check("pesti_gemv_i4group", status)
     torch, dev, st = _place(stream)
     fn, n, f32 = load().pesti_gemv_i4group, out_features * _groups(in_features, group), torch.float32
     return _check("pesti_gemv_i4group", fn(
@@ -527,6 +553,11 @@ def pesti_gemv_group_i4group(ops, group, batch=1, stream=None):
 def pesti_gemv_i4group_swiglu(out_features, in_features, group, gate_packed, gate_scales, gate_zeros, up_packed, up_scales,
                               up_zeros, x, h, batch=1, stream=None):
     """h = silu(W_gate x) * (W_up x) in one launch."""
+    if stream is None:
+        status = _call_gemv_i4group_swiglu(out_features, in_features, group, gate_packed, gate_scales, gate_zeros, up_packed,
+                                           up_scales, up_zeros, x, h, batch)
+        if status is not None:
+            return _check("pesti_gemv_i4group_swiglu", status)
     torch, dev, st = _place(stream)
     fn, codes, n = load().pesti_gemv_i4group_swiglu, out_features * (in_features // 2), out_features * _groups(in_features, group)
     u8, f16 = torch.uint8, torch.float16
@@ -629,6 +660,11 @@ def pesti_cache_extend(cache, table, n, seq_ids=None, counts=None, status=None, 
 def pesti_cache_append(cache, table, layer, rows, k, v, stride=None, seq_ids=None, positions=None, x_format=None,
                        stream=None):
     """K and V of `rows` new tokens into layer `layer`; stride: values from row to row (by default the tensors')."""
+    if stream is None and x_format is None and getattr(table, "address", None) and getattr(cache, "address", None):
+        status = _call_cache_append(cache.address, table.address, cache.device, table.device, table.refs_held, layer, rows, k, v,
+                                    stride, seq_ids, positions)
+        if status is not None:
+            return _check("pesti_cache_append", status)
     fid, size = _value_format(x_format, k, "k")
     torch, dev, st = _place(stream)
     values, width = _type_of(torch, fid), cache.kv_heads * cache.head_dim
@@ -650,13 +686,18 @@ def pesti_attn_paged(cache, table, layer, rows, heads, q, y, scale, q_stride=Non
                      workspace=None, workspace_bytes=None, q_format=None, y_format=None, stream=None):
     """Attention of one new token per row over its sequence's cache; max_length: the bound that the workspace was
     sized for (by default the table's width)."""
+    if max_length is None:
+        max_length = max(1, table.width * cache.page_size)
+    if stream is None and q_format is None and y_format is None and getattr(table, "address", None) and getattr(cache, "address", None):
+        status = _call_attn_paged(cache.address, table.address, cache.device, table.device, table.refs_held, layer, rows, heads, q, y,
+                                  scale, q_stride, max_length, seq_ids, workspace, workspace_bytes)
+        if status is not None:
+            return _check("pesti_attn_paged", status)
     qid, qsize = _value_format(q_format, q, "q")
     yid, ysize = _value_format(y_format, y, "y")
     torch, dev, st = _place(stream)
     width = heads * cache.head_dim
     qp, qs = _rows(dev, q, rows, width, q_stride, qsize, "q", _type_of(torch, qid))
-    if max_length is None:
-        max_length = max(1, table.width * cache.page_size)
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     return _check("pesti_attn_paged", load().pesti_attn_paged(

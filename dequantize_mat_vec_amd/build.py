@@ -48,7 +48,7 @@ def args_command(out: Path):
     lib = Path(torch.__file__).resolve().parent / "lib"
     return [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__",
-            *[f"-isystem{p}" for p in (*include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"])],
+            f"-I{INCLUDE_DIR}", *[f"-isystem{p}" for p in (*include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"])],
             str(SRC_DIR / "tensor_args.cpp"), "-o", str(out), f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
 
 

@@ -3,12 +3,20 @@
 // kernel takes, and 0.6 us on these.  sized() and rows() return what the
 // functions of the same names in _lib.py return where every check passes, and
 // call those for all else (other kinds of arguments, and the errors).
+//
+// gemv_i4group() and its like make a whole call of a decode step on the current
+// stream: every argument checked as in _lib.py, the library's function called, its
+// status returned.  None, and nothing done, where a check does not pass or an
+// argument is of another kind: the function in _lib.py then looks at it (a 4-bit
+// mat-vec 4.2 -> 3.3 us of the host, 3.1 of them the launch, attention 5.0 -> 3.4).
 #include <Python.h>
 
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include "pesti.h"
 
 namespace {
 
@@ -71,6 +79,221 @@ PyObject* place(PyObject*, PyObject* const*, Py_ssize_t) {
   }
 }
 
+struct Library {
+  decltype(&pesti_gemv_i4group) gemv_i4group;
+  decltype(&pesti_gemv_i4group_swiglu) gemv_i4group_swiglu;
+  decltype(&pesti_cache_append) cache_append;
+  decltype(&pesti_attn_paged) attn_paged;
+} library{};
+
+// The arguments of a call, read in turn; `ok` falls where one is of another kind or
+// does not pass.
+struct Reader {
+  PyObject* const* a;
+  bool ok = true;
+  int dev = -1;
+  void* stream = nullptr;
+
+  explicit Reader(PyObject* const* args) : a(args) {
+    try {
+      dev = c10::hip::current_device();
+      stream = c10::hip::getCurrentHIPStream(static_cast<c10::DeviceIndex>(dev)).stream();
+    } catch (...) {
+      ok = false;
+    }
+  }
+  bool none(int i) const { return a[i] == Py_None; }
+  // An integer of 0 .. most.
+  int64_t integer(int i, int64_t most = int64_t{1} << 31) {
+    if (!PyLong_CheckExact(a[i])) return fail();
+    int overflow = 0;
+    const long long v = PyLong_AsLongLongAndOverflow(a[i], &overflow);
+    return overflow || v < 0 || v > most ? fail() : v;
+  }
+  float number(int i) {
+    if (PyFloat_CheckExact(a[i])) return static_cast<float>(PyFloat_AS_DOUBLE(a[i]));
+    return static_cast<float>(fail());
+  }
+  void* address(int i) {
+    void* p = PyLong_CheckExact(a[i]) ? PyLong_AsVoidPtr(a[i]) : nullptr;
+    if (!p) {
+      PyErr_Clear();
+      fail();
+    }
+    return p;
+  }
+  const at::Tensor* tensor(int i) {
+    if (ok && THPVariable_CheckExact(a[i])) {
+      const at::Tensor& t = THPVariable_Unpack(a[i]);
+      if (t.is_cuda() && t.get_device() == dev) return &t;
+    }
+    fail();
+    return nullptr;
+  }
+  // A contiguous tensor of at least `bytes` bytes; type: any where not given.  None is NULL.
+  template <typename T>
+  T* array(int i, int64_t bytes, c10::optional<at::ScalarType> type) {
+    if (!ok || none(i)) return nullptr;
+    const at::Tensor* t = tensor(i);
+    if (!t || (type && t->scalar_type() != *type) || static_cast<int64_t>(t->nbytes()) < bytes || !t->is_contiguous()) {
+      fail();
+      return nullptr;
+    }
+    return static_cast<T*>(t->data_ptr());
+  }
+  // [count][width] values whose rows may lie apart, of a value format; *stride: given, or to be read off the tensor (-1).
+  void* values(int i, int64_t count, int64_t width, int64_t* stride, int32_t* format) {
+    const at::Tensor* t = tensor(i);
+    if (!t || t->dim() != 2 || (t->size(1) != 1 && t->stride(1) != 1)) {
+      fail();
+      return nullptr;
+    }
+    const bool f32 = t->scalar_type() == at::kFloat;
+    if (!f32 && t->scalar_type() != at::kHalf) fail();
+    *format = f32 ? PESTI_FMT_F32 : PESTI_FMT_F16;
+    if (*stride < 0) *stride = t->size(0) > 1 ? t->stride(0) : width;
+    const int64_t held = static_cast<int64_t>(t->storage().nbytes()) / (f32 ? 4 : 2) - t->storage_offset();
+    if (*stride < 0 || *stride > int64_t{1} << 31 || (count > 0 && (count - 1) * *stride + width > held)) fail();
+    return t->data_ptr();
+  }
+  int64_t fail() {
+    ok = false;
+    return 0;
+  }
+};
+
+template <typename F>
+PyObject* make(Reader& r, F call) {
+  if (!r.ok) Py_RETURN_NONE;
+  int status;
+  Py_BEGIN_ALLOW_THREADS;
+  status = call();
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(status);
+}
+
+// gemv_i4group(out, in, group, packed, scales, zeros, x, y, bias, batch)
+PyObject* gemv_i4group(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 10 || !library.gemv_i4group) Py_RETURN_NONE;
+  Reader r(a);
+  const int64_t out = r.integer(0), in = r.integer(1), group = r.integer(2), batch = r.integer(9, 1 << 20);
+  if (!r.ok || group == 0) Py_RETURN_NONE;
+  const int64_t groups = out * ((in + group - 1) / group);
+  const void* packed = r.array<void>(3, out * (in / 2), at::kByte);
+  const uint16_t* scales = r.array<uint16_t>(4, 2 * groups, at::kHalf);
+  const uint8_t* zeros = r.array<uint8_t>(5, groups, at::kByte);
+  const float* x = r.array<float>(6, 4 * batch * in, at::kFloat);
+  float* y = r.array<float>(7, 4 * batch * out, at::kFloat);
+  const float* bias = r.array<float>(8, 4 * out, at::kFloat);
+  return make(r, [&] {
+    return library.gemv_i4group(out, in, group, packed, scales, zeros, x, y, bias, static_cast<int32_t>(batch), r.stream);
+  });
+}
+
+// gemv_i4group_swiglu(out, in, group, gate and up: packed, scales, zeros, x, h, batch)
+PyObject* gemv_i4group_swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 12 || !library.gemv_i4group_swiglu) Py_RETURN_NONE;
+  Reader r(a);
+  const int64_t out = r.integer(0), in = r.integer(1), group = r.integer(2), batch = r.integer(11, 1 << 20);
+  if (!r.ok || group == 0) Py_RETURN_NONE;
+  const int64_t groups = out * ((in + group - 1) / group);
+  const void* packed[2];
+  const uint16_t* scales[2];
+  const uint8_t* zeros[2];
+  for (int m = 0; m < 2; ++m) {
+    packed[m] = r.array<void>(3 + 3 * m, out * (in / 2), at::kByte);
+    scales[m] = r.array<uint16_t>(4 + 3 * m, 2 * groups, at::kHalf);
+    zeros[m] = r.array<uint8_t>(5 + 3 * m, groups, at::kByte);
+  }
+  const float* x = r.array<float>(9, 4 * batch * in, at::kFloat);
+  float* h = r.array<float>(10, 4 * batch * out, at::kFloat);
+  return make(r, [&] {
+    return library.gemv_i4group_swiglu(out, in, group, packed[0], scales[0], zeros[0], packed[1], scales[1], zeros[1], x, h,
+                                       static_cast<int32_t>(batch), r.stream);
+  });
+}
+
+// The structs of a cache call, built for the current device and each other: their
+// addresses, the devices that they were built on, the pages that refs holds (or None).
+bool structs(Reader& r, const pesti_kv_cache** cache, const pesti_kv_table** table) {
+  *cache = static_cast<const pesti_kv_cache*>(r.address(0));
+  *table = static_cast<const pesti_kv_table*>(r.address(1));
+  if (r.integer(2) != r.dev || r.integer(3) != r.dev) r.fail();
+  if (r.ok && !r.none(4) && r.integer(4, INT64_MAX) < (*cache)->pages) r.fail();
+  const int64_t most = int64_t{1} << 20;   // (the library looks at the sizes themselves)
+  return r.ok && (*cache)->kv_heads >= 0 && (*cache)->kv_heads < most && (*cache)->head_dim >= 0 && (*cache)->head_dim < most;
+}
+
+// cache_append(cache, table, their devices, refs held, layer, rows, k, v, stride, seq_ids, positions)
+PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 12 || !library.cache_append) Py_RETURN_NONE;
+  Reader r(a);
+  const pesti_kv_cache* cache;
+  const pesti_kv_table* table;
+  if (!structs(r, &cache, &table)) Py_RETURN_NONE;
+  const int64_t layer = r.integer(5), rows = r.integer(6), width = cache->kv_heads * cache->head_dim;
+  int64_t k_stride = r.none(9) ? -1 : r.integer(9), v_stride = k_stride;
+  int32_t format = 0, v_format = 0;
+  const void* k = r.values(7, rows, width, &k_stride, &format);
+  const void* v = r.values(8, rows, width, &v_stride, &v_format);
+  if (format != v_format || k_stride != v_stride) r.fail();
+  const int32_t* seq_ids = r.array<int32_t>(10, 4 * rows, at::kInt);
+  const int32_t* positions = r.array<int32_t>(11, 4 * rows, at::kInt);
+  return make(r, [&] { return library.cache_append(cache, table, layer, rows, format, k, v, k_stride, seq_ids, positions, r.stream); });
+}
+
+// attn_paged(cache, table, their devices, refs held, layer, rows, heads, q, y, scale, q_stride, max_length, seq_ids,
+//            workspace, workspace_bytes)
+PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 16 || !library.attn_paged) Py_RETURN_NONE;
+  Reader r(a);
+  const pesti_kv_cache* cache;
+  const pesti_kv_table* table;
+  if (!structs(r, &cache, &table)) Py_RETURN_NONE;
+  const int64_t layer = r.integer(5), rows = r.integer(6), heads = r.integer(7, 1 << 20), width = heads * cache->head_dim;
+  int64_t stride = r.none(11) ? -1 : r.integer(11);
+  int32_t q_format = 0;
+  const void* q = r.values(8, rows, width, &stride, &q_format);
+  const at::Tensor* y = r.tensor(9);
+  const bool f32 = y && y->scalar_type() == at::kFloat;
+  if (y && !f32 && y->scalar_type() != at::kHalf) r.fail();
+  void* out = r.array<void>(9, rows * width * (f32 ? 4 : 2), c10::nullopt);
+  const float scale = r.number(10);
+  const int64_t longest = r.integer(12);
+  const int32_t* seq_ids = r.array<int32_t>(13, 4 * rows, at::kInt);
+  int64_t bytes = 0;
+  void* workspace = nullptr;
+  if (!r.none(14)) {
+    const at::Tensor* w = r.tensor(14);
+    bytes = w && r.none(15) ? static_cast<int64_t>(w->nbytes()) : r.integer(15, INT64_MAX);
+    workspace = r.array<void>(14, bytes, c10::nullopt);
+  } else if (!r.none(15)) {
+    bytes = r.integer(15, INT64_MAX);
+  }
+  return make(r, [&] {
+    return library.attn_paged(cache, table, layer, rows, heads, seq_ids, q_format, q, stride, f32 ? PESTI_FMT_F32 : PESTI_FMT_F16, out,
+                              scale, longest, workspace, bytes, r.stream);
+  });
+}
+
+// link(addresses of the library's functions, in Library's order)
+PyObject* link(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  void* f[4];
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "link takes four addresses");
+    return nullptr;
+  }
+  for (int i = 0; i < 4; ++i) {
+    f[i] = PyLong_AsVoidPtr(a[i]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  library.gemv_i4group = reinterpret_cast<decltype(library.gemv_i4group)>(f[0]);
+  library.gemv_i4group_swiglu = reinterpret_cast<decltype(library.gemv_i4group_swiglu)>(f[1]);
+  library.cache_append = reinterpret_cast<decltype(library.cache_append)>(f[2]);
+  library.attn_paged = reinterpret_cast<decltype(library.attn_paged)>(f[3]);
+  Py_RETURN_NONE;
+}
+
 // bind(sized, rows): the Python functions behind the fast ones
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 2) {
@@ -88,6 +311,11 @@ PyMethodDef methods[] = {
     {"sized", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(sized)), METH_FASTCALL, nullptr},
     {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rows)), METH_FASTCALL, nullptr},
     {"place", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(place)), METH_FASTCALL, nullptr},
+    {"gemv_i4group", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemv_i4group)), METH_FASTCALL, nullptr},
+    {"gemv_i4group_swiglu", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemv_i4group_swiglu)), METH_FASTCALL, nullptr},
+    {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
+    {"attn_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn_paged)), METH_FASTCALL, nullptr},
+    {"link", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(link)), METH_FASTCALL, nullptr},
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
