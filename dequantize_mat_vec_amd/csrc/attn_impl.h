@@ -401,6 +401,9 @@ void attn_kernel(AttnArgs p) {
   }
   __builtin_amdgcn_sched_barrier(0);
 
+  // How the second part of a value is made, per lane.
+  const float less = second ? -1.f : 0.f, times = second ? 0x1p11f : 1.f;
+
   // Q: columns 0-7 the first parts, 8-15 the second ones, of heads that exist;
   // scaled so that a head's largest finite value lies in [2^14, 2^15).
   h8 qf[NT][kSteps];
@@ -410,7 +413,7 @@ void attn_kernel(AttnArgs p) {
     const int h = 8 * n + (col & 7);
     const bool there = h < heads_here;
     float v[kSteps][8];
-    uint32_t most = 0;
+    uint32_t top = 0;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
 #pragma unroll
@@ -418,19 +421,41 @@ void attn_kernel(AttnArgs p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t u = __builtin_bit_cast(uint32_t, v[s][e]) & 0x7FFFFFFFu;
-        most = u < 0x7F800000u && u > most ? u : most;
+        top = u > top ? u : top;
       }
     }
+    const bool finite = !__any(top >= 0x7F800000u);
+    if (!finite) {   // the largest finite value
+      top = 0;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t u = __builtin_bit_cast(uint32_t, v[s][e]) & 0x7FFFFFFFu;
+          top = u < 0x7F800000u && u > top ? u : top;
+        }
+    }
     // magnitudes are ordered as floats too
-    const uint32_t big = __builtin_bit_cast(uint32_t, column_max(__builtin_bit_cast(float, most)));
+    const uint32_t big = __builtin_bit_cast(uint32_t, column_max(__builtin_bit_cast(float, top)));
     int up = 14 + 127 - static_cast<int>(big >> 23);   // the exponent to add
     up = big == 0 ? 0 : (up > 126 ? 126 : up);
-    const float lift = __builtin_bit_cast(float, static_cast<uint32_t>(up + 127) << 23);
+    const float lift = there ? __builtin_bit_cast(float, static_cast<uint32_t>(up + 127) << 23) : 0.f;
     factor[n] = p.scale * __builtin_bit_cast(float, static_cast<uint32_t>(127 - up) << 23);
+    // first part: the value; second: what its rounding leaves
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) qf[n][s][e] = there ? part_of(v[s][e] * lift, second) : static_cast<_Float16>(0.f);
+      for (int e = 0; e < 8; ++e) {
+        const float x = v[s][e] * lift;
+        const _Float16 hi = static_cast<_Float16>(x);
+        qf[n][s][e] = static_cast<_Float16>(fmaf(static_cast<float>(hi), less, x) * times);
+      }
+    if (!finite) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) qf[n][s][e] = there ? part_of(v[s][e] * lift, second) : static_cast<_Float16>(0.f);
+    }
   }
 
   f32x4 acc[NT][kFrags];
@@ -449,7 +474,6 @@ void attn_kernel(AttnArgs p) {
   float share[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) share[n] = second ? factor[n] * kPart : factor[n];
-  const float less = second ? -1.f : 0.f, times = second ? 0x1p11f : 1.f;
 
   int step = 0;
   for (int32_t tile = first_tile; tile <= last_tile; tile += waves) {
