@@ -102,6 +102,12 @@ __device__ __forceinline__ float column_sum(float v) {
 }
 __device__ __forceinline__ float other_part(float v) { return dpp<0x128>(v); }   // row_ror:8, column c ^ 8
 
+// Both to binary16, to nearest even (v_cvt_pk_f16_f32).
+__device__ __forceinline__ h2 pair_of(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  return __builtin_convertvector((f2{a, b}), h2);
+}
+
 constexpr float kPart = 0x1p-11f;   // the second part is held 2^11 times as large
 
 // First and second binary16 part of x (|x| < 2^15); an infinity or NaN is all in the first.
@@ -445,10 +451,12 @@ void attn_kernel(AttnArgs p) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = v[s][e] * lift;
-        const _Float16 hi = static_cast<_Float16>(x);
-        qf[n][s][e] = static_cast<_Float16>(fmaf(static_cast<float>(hi), less, x) * times);
+      for (int e = 0; e < 8; e += 2) {
+        const float x0 = v[s][e] * lift, x1 = v[s][e + 1] * lift;
+        const h2 hi = pair_of(x0, x1);
+        const h2 part = pair_of(fmaf(static_cast<float>(hi[0]), less, x0) * times, fmaf(static_cast<float>(hi[1]), less, x1) * times);
+        qf[n][s][e] = part[0];
+        qf[n][s][e + 1] = part[1];
       }
     if (!finite) {
 #pragma unroll
@@ -459,7 +467,11 @@ void attn_kernel(AttnArgs p) {
   }
 
   f32x4 acc[NT][kFrags];
-  float most[NT], sum[NT], ref[NT];   // ref: y is held as acc * 2^ref (8 bits; else the maximum alone scales it)
+  // Weights and their sum are 2^kLift times as large, so that the second part of a
+  // weight reaches further down.  ref: y is held as acc * 2^ref (8 bits, whose
+  // weights are scaled by their tokens' scales; else the maximum alone scales it).
+  constexpr float kLift = I8 ? 0.f : 14.f;
+  float most[NT], sum[NT], ref[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     most[n] = -INFINITY;
@@ -469,8 +481,7 @@ void attn_kernel(AttnArgs p) {
     for (int f = 0; f < kFrags; ++f) acc[n][f] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // Per lane: what its part of a score counts for (softmax's scale in it), and
-  // how the second part of a weight is made.
+  // Per lane: what its part of a score counts for (softmax's scale in it).
   float share[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) share[n] = second ? factor[n] * kPart : factor[n];
@@ -517,7 +528,7 @@ void attn_kernel(AttnArgs p) {
         }
         const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
         now = fmaxf(most[n], column_max(top));
-        const float base = now == -INFINITY ? 0.f : now;
+        const float base = now == -INFINITY ? 0.f : now - kLift;
         add = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -539,7 +550,7 @@ void attn_kernel(AttnArgs p) {
       const float down = higher ? __builtin_amdgcn_exp2f(most[n] - now) : 1.f;
       sum[n] = fmaf(sum[n], down, add);
       float old = down;   // what y so far is to be scaled by
-      float lift = 0x1p14f;
+      float lift = 1.f;
       bool moved = higher;
       if constexpr (I8) {
         // The weights of the codes are p times the token's scale: y is held
@@ -568,10 +579,12 @@ void attn_kernel(AttnArgs p) {
           for (int i = 0; i < 4; ++i) acc[n][f][i] *= old;
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {   // first part: the weight; second: what its rounding leaves
-        const float v = e[j] * lift;
-        const _Float16 hi = static_cast<_Float16>(v);
-        pf[n][j] = static_cast<_Float16>(fmaf(static_cast<float>(hi), less, v) * times);
+      for (int j = 0; j < 8; j += 2) {   // first part: the weight; second: what its rounding leaves
+        const float v0 = I8 ? e[j] * lift : e[j], v1 = I8 ? e[j + 1] * lift : e[j + 1];
+        const h2 hi = pair_of(v0, v1);
+        const h2 part = pair_of(fmaf(static_cast<float>(hi[0]), less, v0) * times, fmaf(static_cast<float>(hi[1]), less, v1) * times);
+        pf[n][j] = part[0];
+        pf[n][j + 1] = part[1];
       }
     }
     if (!whole) {
@@ -619,7 +632,7 @@ void attn_kernel(AttnArgs p) {
         joint_sum[h] = total;
       }
     }
-    float scale = most[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(most[n] - top + (I8 ? ref[n] : -14.f));
+    float scale = most[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(most[n] - top + (I8 ? ref[n] : 0.f));
     if (sum[n] != sum[n]) scale = 1.f;   // NaN without a maximum: y is NaN already
     float* to = joint + (wave * 8 * NT + h) * kRow;
     // both columns of a head have its sums: each writes half of them

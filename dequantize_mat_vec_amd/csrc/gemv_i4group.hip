@@ -363,13 +363,12 @@ void gemv_i4group_kernel(I4Args p) {
         up = bits == 0 ? 0 : (up > 126 ? 126 : up);
         const float lift = __builtin_bit_cast(float, static_cast<uint32_t>(up + 127) << 23);
         h8 hi, lo;
-        // The first part towards zero, two at once; the second then to nearest, of
-        // what is left: below 2^-10 of the value, so that its 11 bits are within
-        // 2^-22 too.
+        // Two at once (v_cvt_pk_f16_f32, to nearest even).
+        typedef float f2 __attribute__((ext_vector_type(2)));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {   // codes j and j + 4 share a register
           const float x0 = v[k][0][j] * lift, x1 = v[k][1][j] * lift;
-          const h2 h = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_pkrtz(x0, x1));
+          const h2 h = __builtin_convertvector((f2{x0, x1}), h2);
           float r0 = (x0 - static_cast<float>(h[0])) * 0x1p11f, r1 = (x1 - static_cast<float>(h[1])) * 0x1p11f;
           if (endless) {   // an infinity is all in the first part
             r0 = r0 - r0 == 0.f ? r0 : 0.f;
@@ -377,8 +376,9 @@ void gemv_i4group_kernel(I4Args p) {
           }
           hi[2 * j] = h[0];
           hi[2 * j + 1] = h[1];
-          lo[2 * j] = static_cast<_Float16>(r0);
-          lo[2 * j + 1] = static_cast<_Float16>(r1);
+          const h2 l = __builtin_convertvector((f2{r0, r1}), h2);
+          lo[2 * j] = l[0];
+          lo[2 * j + 1] = l[1];
         }
         if (at[k] >= 0) {
           h8* x = reinterpret_cast<h8*>(lds) + at[k] * stride + b;
