@@ -28,6 +28,8 @@
 // kernel (attn_paged.hip) where a sequence has more than one.
 #pragma once
 
+#include <type_traits>
+
 #include "kv_cache.h"
 
 namespace pesti {
@@ -215,12 +217,6 @@ struct VTile {
     if (f < 8 * kA + 4 * kB) return b[0].frag(f - 8 * kA);
     return c[0].frag(f - 8 * kA - 4 * kB);
   }
-  // The dimension that row `row` of operand f is.
-  __device__ __forceinline__ static int dim(int f, int row) {
-    if (f < 8 * kA) return 128 * (f / 8) + 8 * row + f % 8;
-    if (f < 8 * kA + 4 * kB) return 128 * kA + 4 * row + (f - 8 * kA);
-    return 128 * kA + 64 * kB + 2 * row + (f - 8 * kA - 4 * kB);
-  }
 };
 
 // The first of the 8 dimensions that lane group g holds in step s of the
@@ -252,7 +248,7 @@ void attn_kernel(AttnArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int kSteps = D / 32, kFrags = D / 16, kSize = I8 ? 1 : 2, kPages = SMALL ? 4 : 1;
   constexpr int kMostWaves = attn_most_waves(D, NT), kRow = D + 4;   // (padded against bank conflicts)
-  extern __shared__ float lds[];   // per wavefront: y of 8 NT heads, their maxima, their sums
+  extern __shared__ __attribute__((aligned(16))) float lds[];   // per wavefront: y of 8 NT heads, their maxima, their sums
   const KvArgs& a = p.kv;
   const int waves = p.waves;
   float* joint = lds;
@@ -634,16 +630,34 @@ void attn_kernel(AttnArgs p) {
     }
     float scale = most[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(most[n] - top + (I8 ? ref[n] : 0.f));
     if (sum[n] != sum[n]) scale = 1.f;   // NaN without a maximum: y is NaN already
+    // Both columns of a head have its sums: the first writes rows 4g and 4g + 1 of each
+    // operand, the second the other two, a run of E neighbouring dimensions at once.
     float* to = joint + (wave * 8 * NT + h) * kRow;
-    // both columns of a head have its sums: each writes half of them
+    auto put = [&](auto run, int f0, int dim0) {
+      constexpr int E = decltype(run)::value;
+      typedef float fE __attribute__((ext_vector_type(E < 4 ? 2 : 4)));
 #pragma unroll
-    for (int f = 0; f < kFrags / 2; ++f)
+      for (int i = 0; i < 2; ++i) {
+        float y[E];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a0 = acc[n][f][i], a1 = acc[n][f + kFrags / 2][i], o0 = other_part(a0), o1 = other_part(a1);
-        const float y = both_parts(second ? o1 : a0, second ? a1 : o0) * scale;
-        to[second ? VTile<I8, D>::dim(f + kFrags / 2, 4 * g + i) : VTile<I8, D>::dim(f, 4 * g + i)] = y;
+        for (int k = 0; k < E; ++k) {
+          const float a0 = acc[n][f0 + k][i], a1 = acc[n][f0 + k][i + 2], o0 = other_part(a0), o1 = other_part(a1);
+          y[k] = both_parts(second ? o1 : a0, second ? a1 : o0) * scale;
+        }
+        float* at = to + dim0 + E * (4 * g + i + (second ? 2 : 0));
+        if constexpr (E == 2) {
+          *reinterpret_cast<fE*>(at) = fE{y[0], y[1]};
+        } else {
+#pragma unroll
+          for (int k = 0; k < E; k += 4) *reinterpret_cast<fE*>(at + k) = fE{y[k], y[k + 1], y[k + 2], y[k + 3]};
+        }
       }
+    };
+    constexpr int kA = VTile<I8, D>::kA, kB = VTile<I8, D>::kB, kC = VTile<I8, D>::kC;
+#pragma unroll
+    for (int f = 0; f < kA; ++f) put(std::integral_constant<int, 8>{}, 8 * f, 128 * f);
+    if constexpr (kB) put(std::integral_constant<int, 4>{}, 8 * kA, 128 * kA);
+    if constexpr (kC) put(std::integral_constant<int, 2>{}, 8 * kA + 4 * kB, 128 * kA + 64 * kB);
   }
   __syncthreads();
   for (int e = tid; e < heads_here * (D / 4); e += 64 * waves) {
