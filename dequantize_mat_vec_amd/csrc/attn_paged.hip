@@ -126,18 +126,18 @@ int64_t head_blocks(const pesti_kv_cache* cache, int64_t heads) {
 // of a workgroup.  In us, joining included, 8 KV heads of 128 in binary16 unless
 // said:
 //   whole   short sequences are one part and need no joining: longer ones the more
-//     workgroups there are (512 tokens of 2 heads of 64: 8.1, 8.3 in parts, 700: 9.5
-//     and 8.5; 64 rows up to 512: 20.0 and 29.3, up to 1500: 48 and 58, up to 5000:
-//     143 and 134), in eight wavefronts where each has a compute unit to itself
-//     (64 rows up to 300, two to a unit: 20.5 with eight, 14.3 with four; 40 rows
-//     up to 600 of 4 heads of 96: 10.4 and 10.8)
+//     workgroups there are (512 tokens of 2 heads of 64: 7.5, 7.8 in parts, 700: 8.9
+//     and 8.0; 64 rows up to 512: 19.4 and 28, up to 1500: 48 and 57, up to 5000: 143
+//     and 133), in eight wavefronts where each has a compute unit to itself (64 rows
+//     up to 300, two to a unit: 18.3 with eight, 13.3 with four; 40 rows up to 600 of
+//     4 heads of 96: 9.4 and 9.8)
 //   parts   of eight tiles, two of each of four wavefronts; of four tiles where the
-//     launch has no more workgroups than compute units that way (2048 tokens: 11.3,
-//     12.4 with eight); else as many parts as bring the launch to two workgroups a
-//     compute unit, all resident at once (131071 tokens: 98, 104 at four; 32768:
-//     31.5 and 39.7); three for some rows of different lengths (8 rows up to 4096: 22,
-//     24.5 at two and 27 at four), nine for many, so that what ends early makes room
-//     (48 rows up to 8191 in 8 bits: 98, 106 at four, 117 at three)
+//     launch has no more workgroups than compute units that way (2048 tokens: 10.2,
+//     11.9 with eight); else as many parts as bring the launch to two workgroups a
+//     compute unit, all resident at once (131071 tokens: 98, 101 at four; 32768: 31.5
+//     and 36); three for some rows of different lengths (8 rows up to 4096: 22, 24 at
+//     two and 26 at four), nine for many, so that what ends early makes room (48 rows
+//     up to 8191 in 8 bits: 97, 98.5 at four, 114 at three)
 struct Split {
   int64_t parts, part_tiles;
   int waves;
