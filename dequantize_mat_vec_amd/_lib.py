@@ -183,19 +183,28 @@ def _not_made(*args):
 
 
 _call_gemv_i4group = _call_gemv_i4group_swiglu = _call_cache_append = _call_attn_paged = _not_made
+_call_cache_extend = _call_cache_free = _call_cache_fork = _call_cache_compact = _not_made
 
 
 def _link_fast_calls(lib):
     """A decode step's calls on the current stream, made by the compiled checks as a whole."""
     global _call_gemv_i4group, _call_gemv_i4group_swiglu, _call_cache_append, _call_attn_paged
+    global _call_cache_extend, _call_cache_free, _call_cache_fork, _call_cache_compact
     try:
         from . import _tensor_args as fast
     except ImportError:
         return
     fast.link(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        lib.pesti_gemv_i4group, lib.pesti_gemv_i4group_swiglu, lib.pesti_cache_append, lib.pesti_attn_paged)))
+        lib.pesti_gemv_i4group, lib.pesti_gemv_i4group_swiglu, lib.pesti_cache_append, lib.pesti_attn_paged,
+        lib.pesti_cache_extend, lib.pesti_cache_free, lib.pesti_cache_fork, lib.pesti_cache_compact)))
     _call_gemv_i4group, _call_gemv_i4group_swiglu = fast.gemv_i4group, fast.gemv_i4group_swiglu
-    _call_cache_append, _call_attn_paged = fast.cache_append, fast.attn_paged
+    _call_cache_append, _call_attn_paged, _call_cache_extend = fast.cache_append, fast.attn_paged, fast.cache_extend
+    _call_cache_free, _call_cache_fork, _call_cache_compact = fast.cache_free, fast.cache_fork, fast.cache_compact
+
+
+def _built(cache, table):
+    """Were the structs built by kv_cache() and kv_table()?  (Others are filled in by hand.)"""
+    return getattr(cache, "address", None) and getattr(table, "address", None)
 
 
 def _ptr(obj):
@@ -651,6 +660,10 @@ def _rows(dev, obj, rows, width, stride, size, what, dtype):
 
 def pesti_cache_extend(cache, table, n, seq_ids=None, counts=None, status=None, stream=None):
     """Pages for counts[i] (None: 1) more tokens of sequence seq_ids[i] (None: i)."""
+    if stream is None and _built(cache, table):
+        made = _call_cache_extend(cache.address, table.address, cache.device, table.device, table.refs_held, n, seq_ids, counts, status)
+        if made is not None:
+            return _check("pesti_cache_extend", made)
     torch, dev, st = _place(stream)
     return _check("pesti_cache_extend", load().pesti_cache_extend(
         *_kv(dev, cache, table), n, _sized(dev, seq_ids, 4 * n, "seq_ids", torch.int32),
@@ -660,7 +673,7 @@ def pesti_cache_extend(cache, table, n, seq_ids=None, counts=None, status=None, 
 def pesti_cache_append(cache, table, layer, rows, k, v, stride=None, seq_ids=None, positions=None, x_format=None,
                        stream=None):
     """K and V of `rows` new tokens into layer `layer`; stride: values from row to row (by default the tensors')."""
-    if stream is None and x_format is None and getattr(table, "address", None) and getattr(cache, "address", None):
+    if stream is None and x_format is None and _built(cache, table):
         status = _call_cache_append(cache.address, table.address, cache.device, table.device, table.refs_held, layer, rows, k, v,
                                     stride, seq_ids, positions)
         if status is not None:
@@ -688,7 +701,7 @@ def pesti_attn_paged(cache, table, layer, rows, heads, q, y, scale, q_stride=Non
     sized for (by default the table's width)."""
     if max_length is None:
         max_length = max(1, table.width * cache.page_size)
-    if stream is None and q_format is None and y_format is None and getattr(table, "address", None) and getattr(cache, "address", None):
+    if stream is None and q_format is None and y_format is None and _built(cache, table):
         status = _call_attn_paged(cache.address, table.address, cache.device, table.device, table.refs_held, layer, rows, heads, q, y,
                                   scale, q_stride, max_length, seq_ids, workspace, workspace_bytes)
         if status is not None:
@@ -713,6 +726,11 @@ def pesti_cache_workspace_bytes(cache, table):
 
 def pesti_cache_fork(cache, table, n, parents, children, status, workspace, workspace_bytes=None, stream=None):
     """Sequence children[i] becomes a copy of parents[i]: whole pages shared, a last one that is not full copied."""
+    if stream is None and _built(cache, table):
+        made = _call_cache_fork(cache.address, table.address, cache.device, table.device, table.refs_held, n, parents, children, status, workspace,
+                                   workspace_bytes)
+        if made is not None:
+            return _check("pesti_cache_fork", made)
     torch, dev, st = _place(stream)
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
@@ -724,6 +742,10 @@ def pesti_cache_fork(cache, table, n, parents, children, status, workspace, work
 
 def pesti_cache_free(cache, table, n, seq_ids=None, stream=None):
     """The listed sequences (None: 0..n-1) become empty, their pages free."""
+    if stream is None and _built(cache, table):
+        made = _call_cache_free(cache.address, table.address, cache.device, table.device, table.refs_held, n, seq_ids)
+        if made is not None:
+            return _check("pesti_cache_free", made)
     torch, dev, st = _place(stream)
     return _check("pesti_cache_free", load().pesti_cache_free(
         *_kv(dev, cache, table), n, _sized(dev, seq_ids, 4 * n, "seq_ids", torch.int32), st))
@@ -731,6 +753,11 @@ def pesti_cache_free(cache, table, n, seq_ids=None, stream=None):
 
 def pesti_cache_compact(cache, table, live, workspace, workspace_bytes=None, stream=None):
     """Live pages move to the front of the pool; live[0] gets their number."""
+    if stream is None and _built(cache, table):
+        made = _call_cache_compact(cache.address, table.address, cache.device, table.device, table.refs_held, live, workspace,
+                                      workspace_bytes)
+        if made is not None:
+            return _check("pesti_cache_compact", made)
     torch, dev, st = _place(stream)
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0

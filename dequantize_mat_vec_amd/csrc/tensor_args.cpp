@@ -84,7 +84,12 @@ struct Library {
   decltype(&pesti_gemv_i4group_swiglu) gemv_i4group_swiglu;
   decltype(&pesti_cache_append) cache_append;
   decltype(&pesti_attn_paged) attn_paged;
+  decltype(&pesti_cache_extend) cache_extend;
+  decltype(&pesti_cache_free) cache_free;
+  decltype(&pesti_cache_fork) cache_fork;
+  decltype(&pesti_cache_compact) cache_compact;
 } library{};
+constexpr int kCalls = 8;
 
 // The arguments of a call, read in turn; `ok` falls where one is of another kind or
 // does not pass.
@@ -155,6 +160,16 @@ struct Reader {
     const int64_t held = static_cast<int64_t>(t->storage().nbytes()) / (f32 ? 4 : 2) - t->storage_offset();
     if (*stride < 0 || *stride > int64_t{1} << 31 || (count > 0 && (count - 1) * *stride + width > held)) fail();
     return t->data_ptr();
+  }
+  // A workspace and its size (None: the tensor's).
+  void* workspace(int i, int64_t* bytes) {
+    if (none(i)) {
+      *bytes = none(i + 1) ? 0 : integer(i + 1, INT64_MAX);
+      return nullptr;
+    }
+    const at::Tensor* t = tensor(i);
+    *bytes = t && none(i + 1) ? static_cast<int64_t>(t->nbytes()) : integer(i + 1, INT64_MAX);
+    return array<void>(i, *bytes, c10::nullopt);
   }
   int64_t fail() {
     ok = false;
@@ -262,28 +277,76 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t longest = r.integer(12);
   const int32_t* seq_ids = r.array<int32_t>(13, 4 * rows, at::kInt);
   int64_t bytes = 0;
-  void* workspace = nullptr;
-  if (!r.none(14)) {
-    const at::Tensor* w = r.tensor(14);
-    bytes = w && r.none(15) ? static_cast<int64_t>(w->nbytes()) : r.integer(15, INT64_MAX);
-    workspace = r.array<void>(14, bytes, c10::nullopt);
-  } else if (!r.none(15)) {
-    bytes = r.integer(15, INT64_MAX);
-  }
+  void* workspace = r.workspace(14, &bytes);
   return make(r, [&] {
     return library.attn_paged(cache, table, layer, rows, heads, seq_ids, q_format, q, stride, f32 ? PESTI_FMT_F32 : PESTI_FMT_F16, out,
                               scale, longest, workspace, bytes, r.stream);
   });
 }
 
+// cache_extend(cache, table, their devices, refs held, n, seq_ids, counts, status)
+PyObject* cache_extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 9 || !library.cache_extend) Py_RETURN_NONE;
+  Reader r(a);
+  const pesti_kv_cache* cache;
+  const pesti_kv_table* table;
+  if (!structs(r, &cache, &table)) Py_RETURN_NONE;
+  const int64_t count = r.integer(5);
+  const int32_t* seq_ids = r.array<int32_t>(6, 4 * count, at::kInt);
+  const int32_t* counts = r.array<int32_t>(7, 4 * count, at::kInt);
+  int32_t* status = r.array<int32_t>(8, 4, at::kInt);
+  return make(r, [&] { return library.cache_extend(cache, table, count, seq_ids, counts, status, r.stream); });
+}
+
+// cache_free(cache, table, their devices, refs held, n, seq_ids)
+PyObject* cache_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 7 || !library.cache_free) Py_RETURN_NONE;
+  Reader r(a);
+  const pesti_kv_cache* cache;
+  const pesti_kv_table* table;
+  if (!structs(r, &cache, &table)) Py_RETURN_NONE;
+  const int64_t count = r.integer(5);
+  const int32_t* seq_ids = r.array<int32_t>(6, 4 * count, at::kInt);
+  return make(r, [&] { return library.cache_free(cache, table, count, seq_ids, r.stream); });
+}
+
+// cache_fork(cache, table, their devices, refs held, n, parents, children, status, workspace, workspace_bytes)
+PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 11 || !library.cache_fork) Py_RETURN_NONE;
+  Reader r(a);
+  const pesti_kv_cache* cache;
+  const pesti_kv_table* table;
+  if (!structs(r, &cache, &table)) Py_RETURN_NONE;
+  const int64_t count = r.integer(5);
+  const int32_t* parents = r.array<int32_t>(6, 4 * count, at::kInt);
+  const int32_t* children = r.array<int32_t>(7, 4 * count, at::kInt);
+  int32_t* status = r.array<int32_t>(8, 4, at::kInt);
+  int64_t bytes = 0;
+  void* workspace = r.workspace(9, &bytes);
+  return make(r, [&] { return library.cache_fork(cache, table, count, parents, children, status, workspace, bytes, r.stream); });
+}
+
+// cache_compact(cache, table, their devices, refs held, live, workspace, workspace_bytes)
+PyObject* cache_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 8 || !library.cache_compact) Py_RETURN_NONE;
+  Reader r(a);
+  const pesti_kv_cache* cache;
+  const pesti_kv_table* table;
+  if (!structs(r, &cache, &table)) Py_RETURN_NONE;
+  int32_t* live = r.array<int32_t>(5, 4, at::kInt);
+  int64_t bytes = 0;
+  void* workspace = r.workspace(6, &bytes);
+  return make(r, [&] { return library.cache_compact(cache, table, live, workspace, bytes, r.stream); });
+}
+
 // link(addresses of the library's functions, in Library's order)
 PyObject* link(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* f[4];
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "link takes four addresses");
+  void* f[kCalls];
+  if (n != kCalls) {
+    PyErr_SetString(PyExc_TypeError, "link takes eight addresses");
     return nullptr;
   }
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kCalls; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -291,6 +354,10 @@ PyObject* link(PyObject*, PyObject* const* a, Py_ssize_t n) {
   library.gemv_i4group_swiglu = reinterpret_cast<decltype(library.gemv_i4group_swiglu)>(f[1]);
   library.cache_append = reinterpret_cast<decltype(library.cache_append)>(f[2]);
   library.attn_paged = reinterpret_cast<decltype(library.attn_paged)>(f[3]);
+  library.cache_extend = reinterpret_cast<decltype(library.cache_extend)>(f[4]);
+  library.cache_free = reinterpret_cast<decltype(library.cache_free)>(f[5]);
+  library.cache_fork = reinterpret_cast<decltype(library.cache_fork)>(f[6]);
+  library.cache_compact = reinterpret_cast<decltype(library.cache_compact)>(f[7]);
   Py_RETURN_NONE;
 }
 
@@ -315,6 +382,10 @@ PyMethodDef methods[] = {
     {"gemv_i4group_swiglu", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemv_i4group_swiglu)), METH_FASTCALL, nullptr},
     {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
     {"attn_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn_paged)), METH_FASTCALL, nullptr},
+    {"cache_extend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_extend)), METH_FASTCALL, nullptr},
+    {"cache_free", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_free)), METH_FASTCALL, nullptr},
+    {"cache_fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_fork)), METH_FASTCALL, nullptr},
+    {"cache_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_compact)), METH_FASTCALL, nullptr},
     {"link", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(link)), METH_FASTCALL, nullptr},
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

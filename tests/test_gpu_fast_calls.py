@@ -28,7 +28,14 @@ def fixture():
     out = torch.zeros(3, 14, 64, device="cuda")
     ws = workspace_of(g.cache, 3, 14, 320)
     ints = torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda")
+    status = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    upkeep = torch.empty(dmv.pesti_cache_workspace_bytes(g.cache, g.table), dtype=torch.uint8, device="cuda")
     return {
+        "pesti_cache_extend": (status, dict(cache=g.cache, table=g.table, n=3, seq_ids=ints, counts=ints * 0 - 1, status=status)),
+        "pesti_cache_free": (g.arrays["table"], dict(cache=g.cache, table=g.table, n=3, seq_ids=ints - 9)),
+        "pesti_cache_fork": (status, dict(cache=g.cache, table=g.table, n=3, parents=ints, children=ints, status=status,
+                                          workspace=upkeep)),
+        "pesti_cache_compact": (status, dict(cache=g.cache, table=g.table, live=status, workspace=upkeep)),
         "pesti_gemv_i4group": (y, dict(out_features=96, in_features=256, group=64, packed=m[0], scales=m[1], zeros=m[2], x=x, y=y,
                                        bias=bias, batch=2)),
         "pesti_gemv_i4group_swiglu": (y, dict(out_features=96, in_features=256, group=64, gate_packed=m[0], gate_scales=m[1],
@@ -41,6 +48,9 @@ def fixture():
 
 
 NAMES = ["pesti_gemv_i4group", "pesti_gemv_i4group_swiglu", "pesti_cache_append", "pesti_attn_paged"]
+# (as the fixture has them these change nothing: no more tokens, no such sequence, children that are not empty; and pages
+# that lie in front already once they have been moved there)
+UPKEEP = ["pesti_cache_extend", "pesti_cache_free", "pesti_cache_fork", "pesti_cache_compact"]
 
 
 @pytest.mark.parametrize("name", NAMES)
@@ -87,7 +97,24 @@ def bad(value):
         yield "no number", "5"
 
 
-@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("name", UPKEEP)
+def test_upkeep_is_made(name, monkeypatch):
+    announce(f"fast {name}")
+    import torch
+    _, args = fixture()[name]
+    made = []
+    fast = "_call_" + name[len("pesti_"):]
+    inner = getattr(_lib, fast)
+    monkeypatch.setattr(_lib, fast, lambda *a: made.append(inner(*a)) or made[-1])
+    arrays = [t for t in (*args["table"].tensors, *args["cache"].tensors, args.get("status", args.get("live"))) if t is not None]
+    after = []
+    for stream in (None, torch.cuda.current_stream()):
+        assert getattr(dmv, name)(**args, stream=stream) == 0
+        after.append([t.clone() for t in arrays])
+    assert made == [0] and all(torch.equal(a, b) for a, b in zip(*after))
+
+
+@pytest.mark.parametrize("name", NAMES + UPKEEP)
 def test_the_same_refusals(name):
     announce(f"fast {name} refusals")
     import torch
@@ -96,7 +123,7 @@ def test_the_same_refusals(name):
     seen = 0
     for key, value in args.items():
         for what, wrong in bad(value):
-            if key in ("rows", "batch", "stride", "max_length") and what == "too large":
+            if key in ("rows", "batch", "stride", "max_length", "n") and what == "too large":
                 continue   # sizes of memory that no test has
             answers = []
             for given in (None, stream):
@@ -106,7 +133,7 @@ def test_the_same_refusals(name):
                     answers.append((type(e), str(e)))
             assert answers[0] == answers[1], (key, what)
             seen += answers[0][0] != "status"
-    assert seen > 20
+    assert seen >= (6 if name in UPKEEP else 20)
     torch.cuda.synchronize()
 
 
