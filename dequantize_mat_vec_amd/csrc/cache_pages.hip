@@ -122,24 +122,30 @@ __global__ __launch_bounds__(kPlanThreads) void take_kernel(TakeArgs t) {
   __syncthreads();
   auto seq = [&](int i) { return t.list ? t.list[i] : i; };
   auto named = [&](int32_t s) { return static_cast<uint32_t>(s) < static_cast<uint32_t>(a.seqs); };
-  for (int i = tid; i < t.n; i += kPlanThreads) {
-    const int32_t s = seq(i);
-    if (!named(s)) continue;
+  constexpr int kEntries = PESTI_MAX_SEQS / kPlanThreads;
+  int32_t mine[kEntries];   // the sequences of the thread's entries (a load behind the stores at the end would wait for them)
+#pragma unroll
+  for (int j = 0; j < kEntries; ++j) {
+    const int i = j * kPlanThreads + tid;
+    mine[j] = -1;
+    if (i >= t.n) continue;
+    mine[j] = seq(i);
+    if (!named(mine[j])) continue;
     if (FORK && !named(t.second[i])) continue;
-    atomicMin(&claim[s], i);
+    atomicMin(&claim[mine[j]], i);
   }
   __syncthreads();
   int64_t total = 0;
   bool outgrown = false;
-  int32_t info[PESTI_MAX_SEQS / kPlanThreads];   // of the thread's entries, until the claims have been read
+  int32_t info[kEntries];   // of the thread's entries, until the claims have been read
 #pragma unroll
-  for (int j = 0; j < PESTI_MAX_SEQS / kPlanThreads; ++j) {
+  for (int j = 0; j < kEntries; ++j) {
     const int i = j * kPlanThreads + tid;
     info[j] = 0;
     if (j * kPlanThreads >= t.n) continue;
     int64_t need = 0;
     if (i < t.n) {
-      const int32_t s = seq(i);
+      const int32_t s = mine[j];
       int64_t len = -1;
       if (named(s) && claim[s] == i) {
         const int32_t old = kv_length(a, s);
@@ -170,7 +176,7 @@ __global__ __launch_bounds__(kPlanThreads) void take_kernel(TakeArgs t) {
   }
   int64_t missing = __syncthreads_or(outgrown) ? -1 : 0;
 #pragma unroll
-  for (int j = 0; j < PESTI_MAX_SEQS / kPlanThreads; ++j)
+  for (int j = 0; j < kEntries; ++j)
     if (j * kPlanThreads + tid < t.n) claim[j * kPlanThreads + tid] = info[j];
   constexpr int32_t kRound = kPlanThreads * kRun;
   int64_t found = 0, sum = 0, before = 0;
@@ -221,8 +227,11 @@ __global__ __launch_bounds__(kPlanThreads) void take_kernel(TakeArgs t) {
     found += sum;
     __syncthreads();   // the round's runs have been read
   }
-  for (int i = tid; i < t.n; i += kPlanThreads) {
-    if (after[i] >= 0) a.lengths[seq(i)] = after[i];
+#pragma unroll
+  for (int j = 0; j < kEntries; ++j) {
+    const int i = j * kPlanThreads + tid;
+    if (i >= t.n) continue;
+    if (after[i] >= 0) a.lengths[mine[j]] = after[i];
     if constexpr (FORK)   // (pairs whose last page is copied have theirs)
       if (after[i] < 0 || (after[i] & (page - 1)) == 0)
         t.plan[i] = make_int4(-1, -1, after[i] < 0 ? 0 : after[i] >> a.page_shift, after[i] >= 0);
