@@ -233,9 +233,11 @@ __device__ __forceinline__ constexpr int k_dim(int s, int steps, int g) {
 
 // Wavefronts per SIMD that the registers are to leave room for.  Stated, since
 // the compiler left to itself adds accumulator registers up to two wavefronts'
-// share where three fit (8 bits, D 128: 113 -> 107 us).
+// share where three fit (8 bits, D 128: 113 -> 107 us), or one's where two do (32
+// rows up to 3000 of 4 heads of 256 in 8 bits 62 -> 41; in binary16 those have 76
+// registers too many for two, which takes 90 instead of 76).
 constexpr int attn_waves(bool i8, int d, int nt, bool small) {
-  return d * nt <= 64 ? 4 : (d * nt <= (i8 || !small ? 128 : 96) ? 3 : (d * nt <= 192 ? 2 : 1));
+  return d * nt <= 64 ? 4 : (d * nt <= (i8 || !small ? 128 : 96) ? 3 : (i8 || d * nt <= 192 ? 2 : 1));
 }
 
 // One workgroup: the NT * 8 query heads of block blockIdx.x of a KV head, a part
