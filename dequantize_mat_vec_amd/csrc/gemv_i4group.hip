@@ -451,6 +451,20 @@ void gemv_i4group_kernel(I4Args p) {
         wz[r] = u32x2{static_cast<uint32_t>(z), static_cast<uint32_t>(z >> 32)};
       }
     }
+    // Groups of a row's last chunk may lie past its end.  Their sums are 0 (x is zero
+    // there), but the places hold the next row's scales, perhaps infinities or NaN.
+    const int left = o.groups - g0 - 8 * g;   // groups of the row from the lane's first on
+    if ((o.groups & (GS - 1)) != 0 && left < 8) {
+      const int lo = left < 0 ? 0 : (left < 4 ? left : 4), hi = left < 4 ? 0 : left - 4;
+      const uint64_t lo_mask = lo == 4 ? ~uint64_t{0} : (uint64_t{1} << 16 * lo) - 1, hi_mask = (uint64_t{1} << 16 * hi) - 1;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        ws[r].x &= static_cast<uint32_t>(lo_mask);
+        ws[r].y &= static_cast<uint32_t>(lo_mask >> 32);
+        ws[r].z &= static_cast<uint32_t>(hi_mask);
+        ws[r].w &= static_cast<uint32_t>(hi_mask >> 32);
+      }
+    }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int r = 0; r < R; ++r) {
