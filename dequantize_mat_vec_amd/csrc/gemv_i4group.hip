@@ -117,6 +117,12 @@ __device__ __forceinline__ uint32_t i4_magic() {
   asm volatile("" : "+v"(v));
   return v;
 }
+
+// The sum of both parts' products.  An infinity of the first stands: an infinite
+// scale makes infinities of any sign, or NaN, of the second's sums.
+__device__ __forceinline__ float both_parts(float hi, float lo) {
+  return __builtin_fabsf(hi) == INFINITY ? hi : fmaf(lo, 0x1p-11f, hi);
+}
 #endif
 
 // ---------------------------------------------------------------------------
@@ -180,6 +186,22 @@ __global__ __launch_bounds__(256) void gemv_i4group_few_kernel(I4Args p) {
         }
       }
   };
+  // One dword's sum of a row and column, and its scale, from memory.
+  auto scale_of = [&](int64_t slab, int r, int d) {
+    const I4Matrix& m = PAIR && r ? o.b : o.a;
+    return i4_scale(m, row_of(slab, r), o.groups, d >> shift);
+  };
+  auto dot = [&](int64_t slab, int r, int b, int d) {
+    const I4Matrix& m = PAIR && r ? o.b : o.a;
+    const int64_t row = row_of(slab, r);
+    const uint32_t q = load_u32(m.packed + row * (o.in / 2) + 4 * d);
+    const int z = i4_zero(m, row, o.groups, d >> shift);
+    const float* src = o.x + static_cast<int64_t>(col0 + (b < cols ? b : 0)) * o.in + 8 * d;
+    float s = 0.f;
+#pragma nounroll
+    for (int e = 0; e < 8; ++e) s = fmaf(static_cast<float>(static_cast<int>(q >> (4 * e) & 15) - z), src[e], s);
+    return s;
+  };
   int64_t slab = blockIdx.x;
   load(slab, 0);
   if (passes == 1) load_x(0);
@@ -219,6 +241,24 @@ __global__ __launch_bounds__(256) void gemv_i4group_few_kernel(I4Args p) {
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int b = 0; b < B; ++b) acc[r][b] = row_sum<L>(acc[r][b]);
+    bool none = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int b = 0; b < B; ++b) none |= acc[r][b] != acc[r][b];
+    if (__any(none)) {   // a NaN, perhaps of a stand-in's zeros times an infinite scale: without those
+#pragma nounroll
+      for (int i = 0; i < R * B; ++i) {
+        const int r = i / B, b = i % B;
+        float v = 0.f;
+#pragma nounroll
+        for (int d = sub; d < dwords; d += L) v = fmaf(dot(slab, r, b, d), scale_of(slab, r, d), v);
+        v = row_sum<L>(v);
+#pragma unroll
+        for (int k = 0; k < R * B; ++k)
+          if (k == i) acc[k / B][k % B] = acc[k / B][k % B] != acc[k / B][k % B] ? v : acc[k / B][k % B];
+      }
+    }
     if (sub == 0) {
       if constexpr (PAIR) {
         const int64_t row = slab * kRows + mine;
@@ -541,8 +581,8 @@ void gemv_i4group_kernel(I4Args p) {
       for (int i = 0; i < 4; ++i) {
         const uint32_t v = __builtin_bit_cast(uint32_t, total[r][i]);
         const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-        y[r][i] = fmaf(__builtin_bit_cast(float, static_cast<uint32_t>(h[1])), 0x1p-11f,
-                       __builtin_bit_cast(float, static_cast<uint32_t>(h[0])));
+        y[r][i] = both_parts(__builtin_bit_cast(float, static_cast<uint32_t>(h[0])),
+                             __builtin_bit_cast(float, static_cast<uint32_t>(h[1])));
       }
     const int64_t row = static_cast<int64_t>(t) * 16 + n;
     if (g >= 2 || row >= out) return;
@@ -578,7 +618,7 @@ void gemv_i4group_kernel(I4Args p) {
         hi += j < waves ? a : 0.f;
         lo += j < waves ? b : 0.f;
       }
-      y[r] = fmaf(lo, 0x1p-11f, hi);
+      y[r] = both_parts(hi, lo);
     }
     o.y[eb * out + row] = PAIR ? y[0] / (1.f + expf(-y[0])) * y[R - 1] : (o.bias ? y[0] + bias : y[0]);
   };

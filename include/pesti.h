@@ -453,7 +453,8 @@ int pesti_gemm_experts_swiglu(int32_t format, int64_t rows, int64_t experts,
  * is scaled by a power of two that brings its largest finite |x| to [2^14,
  * 2^15), and what the first part leaves is held 2^11 times as large in the
  * second, which adds at most 2^-22 |x_i| + 2^-50 max|x| (of the run) per element
- * to the float32 error.  Group sums are float32 and take their scale once.
+ * to the float32 error.  Group sums are float32 and take their scale once; an
+ * infinite or NaN scale makes infinities or NaN of its own row alone.
  *
  * pesti_gemv_group_i4group: up to PESTI_MAX_GROUP such mat-vecs of one group
  * size and batch in one launch, as pesti_gemv_group; every op's y has the bits

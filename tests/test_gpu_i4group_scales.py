@@ -71,3 +71,42 @@ def test_a_scale_reaches_its_own_row_alone_in_swiglu(batch, out, inf, group, whi
         bad, rows = spoiled(gate if which == "gate" else up, value)
         h = swiglu(bad, up) if which == "gate" else swiglu(gate, bad)
         assert np.array_equal(h[:, ~rows], want[:, ~rows]), value
+
+
+OWN = ENDS + [(1, 40, 896, 128), (2, 33, 96, 32), (5, 3101, 928, 32), (8, 4115, 4096, 64), (8, 1045, 8192, 128)]
+
+
+@pytest.mark.parametrize("batch,out,inf,group", OWN)
+def test_an_infinite_scale_gives_infinities(batch, out, inf, group):
+    """Weights of one sign times positive x: an infinite scale of any one group is an infinite sum, of its sign."""
+    announce(f"i4group infinite scale {batch}x{out}x{inf} group {group}")
+    rng = rng_of(3, out, inf)
+    packed, scales, zeros = i4_matrix(rng, out, inf, group)
+    zeros[:] = 20   # every q - z is negative
+    rows = np.arange(0, out, 3)
+    at = rng.integers(0, scales.shape[1], len(rows))
+    at[: len(rows) // 2] = 0
+    sign = np.where(rng.random(len(rows)) < 0.5, -1.0, 1.0)
+    scales[rows, at] = sign * np.inf
+    for x in (rng.random((batch, inf)) + 0.1, np.ones((batch, inf))):   # (ones: nothing is left for a second part)
+        y = run((packed, scales, zeros), out, inf, group, x.astype(np.float32))
+        assert np.array_equal(y[:, rows], np.broadcast_to(-sign * np.inf, (batch, len(rows))))
+        assert np.isfinite(np.delete(y, rows, 1)).all()
+
+
+def test_an_infinite_scale_in_swiglu():
+    announce("i4group infinite scale in swiglu")
+    import torch
+    for batch, out, inf, group in ((1, 33, 928, 32), (4, 9003, 800, 32), (5, 2500, 928, 64), (8, 1045, 8224, 32)):
+        rng = rng_of(4, out, inf)
+        gate, up = (i4_matrix(rng, out, inf, group) for _ in range(2))
+        gate[0][:] |= 0x11
+        gate[2][:], up[2][:] = 0, 20   # weights of gate are positive, those of up negative
+        up[1][0::3, 0], gate[1][1::3, -1] = np.inf, np.inf
+        x = to_dev((rng.random((batch, inf)) + 0.1).astype(np.float32))
+        buf, h = guarded_y(batch * out)
+        dmv.pesti_gemv_i4group_swiglu(out, inf, group, *put(gate), *put(up), x, h, batch)
+        torch.cuda.synchronize()
+        assert guards_intact(buf, batch * out)
+        h = h.cpu().numpy().reshape(batch, out)
+        assert np.all(h[:, 0::3] == -np.inf) and np.all(h[:, 1::3] == -np.inf) and np.isfinite(h[:, 2::3]).all()
