@@ -48,7 +48,7 @@ struct AttnArgs {
   int64_t q_stride;
   void* y;
   float* parts;            // [rows][heads][splits][head_dim], unnormalised
-  float* stats;            // [rows][heads][splits][2]: maximum (base 2), sum
+  float* stats;            // [rows][heads][splits][2]: maximum (base 2), sum (kNoPart: nothing else is written)
   float scale;             // scale * log2(e)
   int32_t heads;
   int32_t group;           // query heads per KV head
@@ -62,6 +62,7 @@ struct AttnArgs {
 // Wavefronts of a workgroup: four, or eight where a sequence is one part.
 constexpr int attn_most_waves(int d, int nt) { return d * nt <= 128 ? 8 : 4; }
 constexpr int kTile = 32;            // tokens of one step of a wavefront
+constexpr float kNoPart = -1.f;      // the sum of a part without tokens
 
 // Tiles per part, and parts, of a sequence of `length` tokens.  Parts of all
 // sequences have one size, so that workgroups of a batch of uneven lengths
@@ -311,7 +312,7 @@ void attn_kernel(AttnArgs p) {
     if (tid < heads_here) {
       float* stats = p.stats + 2 * ((row * p.heads + first_head + tid) * p.splits + part);
       stats[0] = -INFINITY;
-      stats[1] = 0.f;
+      stats[1] = kNoPart;
     }
     return;
   }

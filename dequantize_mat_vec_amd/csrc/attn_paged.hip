@@ -10,9 +10,13 @@ constexpr int kFewParts = 8;
 constexpr int kManyRows = 32;
 
 // y of one row and head from its parts: part i counts 2^(max_i - max) times, one
-// without tokens (maximum -infinity, sum 0) not at all.  The parts are added in
-// an order that the launch fixes.
-//
+// whose every score is -infinity 0 times.  Zero times an infinity or NaN of its
+// values is NaN, as in one part; a part without tokens, whose values are not
+// written, is left out.  The parts are added in an order that the launch fixes.
+__device__ __forceinline__ float part_weight(float m, float l, float top) {
+  return m == -INFINITY ? (l == l ? 0.f : 1.f) : exp2f(m - top);   // a NaN without a maximum stays
+}
+
 // Few parts: a thread takes four dimensions of all of them.
 __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs p, int64_t threads) {
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -35,10 +39,11 @@ __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs p, int64_t 
 #pragma unroll
   for (int i = 0; i < kFewParts; ++i) {
     if (i >= parts) break;
-    const float w = m[i] == -INFINITY ? (l[i] == l[i] ? 0.f : 1.f) : exp2f(m[i] - top);   // a NaN without a maximum stays
+    const float w = part_weight(m[i], l[i], top);
+    const bool none = l[i] == kNoPart;
     total = fmaf(w, l[i], total);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = w == 0.f ? y[j] : fmaf(w, v[i][j], y[j]);   // (a part without tokens wrote nothing)
+    for (int j = 0; j < 4; ++j) y[j] = none ? y[j] : fmaf(w, v[i][j], y[j]);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) y[j] = total == 0.f ? 0.f : y[j] / total;
@@ -52,7 +57,7 @@ __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs p, int64_t 
 template <int LANES>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
   constexpr int kGroups = 256 / LANES, kAhead = 8;
-  __shared__ float weight[kMaxParts], sums[4], tops[4];
+  __shared__ float weight[kMaxParts], sums[4], tops[4];   // (a weight of -1: no part)
   __shared__ f32x4 joint[kGroups][LANES];
   const int tid = threadIdx.x, d = p.kv.head_dim, parts = p.splits;
   const int64_t row = blockIdx.z, head = row * p.heads + blockIdx.y, slot0 = head * parts;
@@ -69,7 +74,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
   }
   if (tid >= parts) {
     m = -INFINITY;
-    l = 0.f;
+    l = kNoPart;
   }
   float top = m;
 #pragma unroll
@@ -77,8 +82,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
   if ((tid & 63) == 0) tops[tid >> 6] = top;
   __syncthreads();
   top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-  const float w = m == -INFINITY ? (l == l ? 0.f : 1.f) : exp2f(m - top);   // a NaN without a maximum stays
-  weight[tid] = w;
+  const float w = part_weight(m, l, top);
+  weight[tid] = l == kNoPart ? -1.f : w;
   float total = w * l;
 #pragma unroll
   for (int o = 1; o < 64; o *= 2) total += __shfl_xor(total, o, 64);
@@ -88,9 +93,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
   f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
-    const float f = weight[first + k * kGroups];   // (0 past the last part)
+    const float f = weight[first + k * kGroups];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = f == 0.f ? y[j] : fmaf(f, v[k][j], y[j]);   // (a part without tokens wrote nothing)
+    for (int j = 0; j < 4; ++j) y[j] = f < 0.f ? y[j] : fmaf(f, v[k][j], y[j]);
   }
   joint[first][e] = y;
   __syncthreads();
