@@ -71,12 +71,8 @@ PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // place() -> (current device, its current stream's handle), None where there is no GPU
 PyObject* place(PyObject*, PyObject* const*, Py_ssize_t) {
-  try {
-    const auto dev = c10::hip::current_device();
-    return Py_BuildValue("(iN)", static_cast<int>(dev), PyLong_FromVoidPtr(c10::hip::getCurrentHIPStream(dev).stream()));
-  } catch (...) {
-    Py_RETURN_NONE;
-  }
+  const auto dev = c10::hip::current_device();   // (throws)
+  return Py_BuildValue("(iN)", static_cast<int>(dev), PyLong_FromVoidPtr(c10::hip::getCurrentHIPStream(dev).stream()));
 }
 
 struct Library {
@@ -100,12 +96,8 @@ struct Reader {
   void* stream = nullptr;
 
   explicit Reader(PyObject* const* args) : a(args) {
-    try {
-      dev = c10::hip::current_device();
-      stream = c10::hip::getCurrentHIPStream(static_cast<c10::DeviceIndex>(dev)).stream();
-    } catch (...) {
-      ok = false;
-    }
+    dev = c10::hip::current_device();
+    stream = c10::hip::getCurrentHIPStream(static_cast<c10::DeviceIndex>(dev)).stream();
   }
   bool none(int i) const { return a[i] == Py_None; }
   // An integer of 0 .. most.
@@ -374,20 +366,48 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// A tensor's methods throw where it has no strides or no memory of its own (sparse ones, those of a
+// torch.vmap), and an exception that left these functions would end the process: such a call is
+// left to the function in _lib.py, which raises the error.
+typedef PyObject* Method(PyObject*, PyObject* const*, Py_ssize_t);
+template <Method* CALL>
+PyObject* or_none(PyObject* self, PyObject* const* a, Py_ssize_t n) noexcept {
+  try {
+    return CALL(self, a, n);
+  } catch (...) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+}
+template <Method* CALL, PyObject** SLOW>
+PyObject* or_slow(PyObject* self, PyObject* const* a, Py_ssize_t n) noexcept {
+  try {
+    return CALL(self, a, n);
+  } catch (...) {
+    PyErr_Clear();
+    return PyObject_Vectorcall(*SLOW, a, n, nullptr);
+  }
+}
+
+// A method of the module.
+PyMethodDef entry(const char* name, Method* call) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call)), METH_FASTCALL, nullptr};
+}
+
 PyMethodDef methods[] = {
-    {"sized", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(sized)), METH_FASTCALL, nullptr},
-    {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rows)), METH_FASTCALL, nullptr},
-    {"place", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(place)), METH_FASTCALL, nullptr},
-    {"gemv_i4group", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemv_i4group)), METH_FASTCALL, nullptr},
-    {"gemv_i4group_swiglu", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemv_i4group_swiglu)), METH_FASTCALL, nullptr},
-    {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
-    {"attn_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn_paged)), METH_FASTCALL, nullptr},
-    {"cache_extend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_extend)), METH_FASTCALL, nullptr},
-    {"cache_free", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_free)), METH_FASTCALL, nullptr},
-    {"cache_fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_fork)), METH_FASTCALL, nullptr},
-    {"cache_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_compact)), METH_FASTCALL, nullptr},
-    {"link", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(link)), METH_FASTCALL, nullptr},
-    {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
+    entry("sized", or_slow<sized, &slow_sized>),
+    entry("rows", or_slow<rows, &slow_rows>),
+    entry("place", or_none<place>),
+    entry("gemv_i4group", or_none<gemv_i4group>),
+    entry("gemv_i4group_swiglu", or_none<gemv_i4group_swiglu>),
+    entry("cache_append", or_none<cache_append>),
+    entry("attn_paged", or_none<attn_paged>),
+    entry("cache_extend", or_none<cache_extend>),
+    entry("cache_free", or_none<cache_free>),
+    entry("cache_fork", or_none<cache_fork>),
+    entry("cache_compact", or_none<cache_compact>),
+    entry("link", link),
+    entry("bind", bind),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
