@@ -167,14 +167,14 @@ def load(path: os.PathLike | None = None) -> ctypes.CDLL:
 def _bind_fast_args():
     """Put the compiled argument checks (csrc/tensor_args.cpp) before the ones below: the same answers and errors,
     a fifth of the time.  Without them (built for another torch, say) those below do alone."""
-    global _sized, _rows, _current
+    global _sized, _rows, _current, _permit
     try:
         from . import _tensor_args
     except ImportError:
         return
     if _sized is not _tensor_args.sized:
         _tensor_args.bind(_sized, _rows)
-        _sized, _rows, _current = _tensor_args.sized, _tensor_args.rows, _tensor_args.place
+        _sized, _rows, _current, _permit = _tensor_args.sized, _tensor_args.rows, _tensor_args.place, _tensor_args.permit
 
 
 def _not_made(*args):
@@ -397,8 +397,19 @@ def _sized(dev, obj, nbytes, what, dtype=None):
 
 
 def _current():
-    """(current device, its current stream's handle); the compiled one gives None where there is no GPU."""
+    """(current device, its current stream's handle); the compiled one gives None until torch has been asked once."""
     return None
+
+
+def _permit():
+    """torch has named the device in this process: the compiled _current() may."""
+
+
+def _device(torch):
+    """The current device.  torch sets itself up on the first call, or refuses it: in a child forked after that."""
+    dev = torch.cuda.current_device()
+    _permit()
+    return dev
 
 
 def _place(stream):
@@ -411,9 +422,9 @@ def _place(stream):
         at = _current()
         if at is not None:
             return torch, at[0], at[1]
-        dev = torch.cuda.current_device()
+        dev = _device(torch)
         return torch, dev, _raw_stream(torch, dev)
-    return torch, torch.cuda.current_device() if torch.cuda.is_available() else 0, _stream(stream)
+    return torch, _device(torch) if torch.cuda.is_available() else 0, _stream(stream)
 
 
 _TYPE_FORMATS = {"torch.float32": 17, "torch.float16": 16}   # by str(dtype)

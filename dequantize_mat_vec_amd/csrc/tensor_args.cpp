@@ -10,6 +10,7 @@
 // argument is of another kind: the function in _lib.py then looks at it (a 4-bit
 // mat-vec 4.2 -> 3.3 us of the host, 3.1 of them the launch, attention 5.0 -> 3.4).
 #include <Python.h>
+#include <pthread.h>
 
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -69,8 +70,19 @@ PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return PyObject_Vectorcall(slow_rows, a, n, nullptr);
 }
 
-// place() -> (current device, its current stream's handle), None where there is no GPU
+// Has torch been asked for the device in this process?  It sets itself up then, or refuses a child
+// forked behind its back; the device is not asked for here before that.
+bool permitted = false;
+
+// permit(): torch has named the device
+PyObject* permit(PyObject*, PyObject* const*, Py_ssize_t) {
+  permitted = true;
+  Py_RETURN_NONE;
+}
+
+// place() -> (current device, its current stream's handle), None where torch is to be asked
 PyObject* place(PyObject*, PyObject* const*, Py_ssize_t) {
+  if (!permitted) Py_RETURN_NONE;
   const auto dev = c10::hip::current_device();   // (throws)
   return Py_BuildValue("(iN)", static_cast<int>(dev), PyLong_FromVoidPtr(c10::hip::getCurrentHIPStream(dev).stream()));
 }
@@ -91,11 +103,12 @@ constexpr int kCalls = 8;
 // does not pass.
 struct Reader {
   PyObject* const* a;
-  bool ok = true;
+  bool ok;
   int dev = -1;
   void* stream = nullptr;
 
-  explicit Reader(PyObject* const* args) : a(args) {
+  explicit Reader(PyObject* const* args) : a(args), ok(permitted) {
+    if (!ok) return;
     dev = c10::hip::current_device();
     stream = c10::hip::getCurrentHIPStream(static_cast<c10::DeviceIndex>(dev)).stream();
   }
@@ -397,6 +410,7 @@ PyMethodDef entry(const char* name, Method* call) {
 PyMethodDef methods[] = {
     entry("sized", or_slow<sized, &slow_sized>),
     entry("rows", or_slow<rows, &slow_rows>),
+    entry("permit", permit),
     entry("place", or_none<place>),
     entry("gemv_i4group", or_none<gemv_i4group>),
     entry("gemv_i4group_swiglu", or_none<gemv_i4group_swiglu>),
@@ -413,4 +427,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_args", nullptr, -1, method
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject* PyInit__tensor_args() { return PyModule_Create(&module); }
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit__tensor_args() {
+  if (pthread_atfork(nullptr, nullptr, [] { permitted = false; }) != 0) return PyErr_NoMemory();
+  return PyModule_Create(&module);
+}
