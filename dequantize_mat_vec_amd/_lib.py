@@ -164,17 +164,24 @@ def load(path: os.PathLike | None = None) -> ctypes.CDLL:
     return lib
 
 
-def _bind_fast_args():
-    """Put the compiled argument checks (csrc/tensor_args.cpp) before the ones below: the same answers and errors,
-    a fifth of the time.  Without them (built for another torch, say) those below do alone."""
-    global _sized, _rows, _current, _permit
+def _compiled():
+    """The compiled argument checks (csrc/tensor_args.cpp); None where there are none, or those of another torch."""
+    import torch
     try:
         from . import _tensor_args
     except ImportError:
-        return
-    if _sized is not _tensor_args.sized:
-        _tensor_args.bind(_sized, _rows)
-        _sized, _rows, _current, _permit = _tensor_args.sized, _tensor_args.rows, _tensor_args.place, _tensor_args.permit
+        return None
+    return _tensor_args if _tensor_args.torch == torch.__version__ else None
+
+
+def _bind_fast_args():
+    """Put the compiled argument checks before the ones below: the same answers and errors, a fifth of the time.
+    Without them those below do alone."""
+    global _sized, _rows, _current, _permit
+    fast = _compiled()
+    if fast is not None and _sized is not fast.sized:
+        fast.bind(_sized, _rows)
+        _sized, _rows, _current, _permit = fast.sized, fast.rows, fast.place, fast.permit
 
 
 def _not_made(*args):
@@ -190,9 +197,8 @@ def _link_fast_calls(lib):
     """A decode step's calls on the current stream, made by the compiled checks as a whole."""
     global _call_gemv_i4group, _call_gemv_i4group_swiglu, _call_cache_append, _call_attn_paged
     global _call_cache_extend, _call_cache_free, _call_cache_fork, _call_cache_compact
-    try:
-        from . import _tensor_args as fast
-    except ImportError:
+    fast = _compiled()
+    if fast is None:
         return
     fast.link(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.pesti_gemv_i4group, lib.pesti_gemv_i4group_swiglu, lib.pesti_cache_append, lib.pesti_attn_paged,

@@ -429,5 +429,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_args", nullptr, -1, method
 
 extern "C" __attribute__((visibility("default"))) PyObject* PyInit__tensor_args() {
   if (pthread_atfork(nullptr, nullptr, [] { permitted = false; }) != 0) return PyErr_NoMemory();
-  return PyModule_Create(&module);
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch", PESTI_TORCH) != 0) {   // the one whose tensors these functions know
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
 }
