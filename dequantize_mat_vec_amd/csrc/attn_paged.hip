@@ -165,6 +165,23 @@ int64_t workspace_of(const pesti_kv_cache* cache, int64_t rows, int64_t heads, i
   return splits <= 1 ? 0 : rows * heads * splits * (cache->head_dim + 2) * 4;
 }
 
+// The most that calls of up to so many rows and so long a bound need, so that a
+// buffer of a program's largest call serves it as sequences finish: fewer rows have
+// more parts each, and a bound just past the longest in parts of four tiles has half
+// as many as that.
+int64_t most_workspace(const pesti_kv_cache* cache, int64_t rows, int64_t heads, int64_t max_length) {
+  int64_t most = 0;
+  for (int64_t r = 1; r <= rows; ++r) {
+    const int64_t four = 256 / (r * cache->kv_heads * head_blocks(cache, heads)) * 4 * pesti::kTile;   // longest in parts of four
+    for (const int64_t bound : {four < max_length ? four : max_length, max_length}) {
+      if (bound < 1) continue;
+      const int64_t bytes = workspace_of(cache, r, heads, split_of(cache, r, heads, bound).parts);
+      most = bytes > most ? bytes : most;
+    }
+  }
+  return most;
+}
+
 int join(const pesti::AttnArgs& p, int64_t rows, hipStream_t st) {
   pesti::AttnArgs args = p;
   int64_t threads = rows * p.heads * (p.kv.head_dim / 4);
@@ -187,7 +204,7 @@ extern "C" {
 
 int64_t pesti_attn_paged_workspace_bytes(const pesti_kv_cache* cache, int64_t rows, int64_t heads, int64_t max_length) {
   const int st = check(cache, rows, heads, max_length);
-  return st != PESTI_OK ? st : workspace_of(cache, rows, heads, split_of(cache, rows, heads, max_length).parts);
+  return st != PESTI_OK ? st : most_workspace(cache, rows, heads, max_length);
 }
 
 int pesti_attn_paged(const pesti_kv_cache* cache, const pesti_kv_table* table, int64_t layer, int64_t rows, int64_t heads,

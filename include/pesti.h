@@ -596,9 +596,11 @@ int pesti_cache_append(const pesti_kv_cache* cache, const pesti_kv_table* table,
  * 2^30, is the caller's bound of the rows' lengths, which chooses the split; a
  * longer sequence is attended whole all the same.  workspace: device memory of
  * pesti_attn_paged_workspace_bytes(cache, rows, heads, max_length) bytes (0:
- * none needed), 16-byte aligned, for one call at a time; PESTI_ERR_WORKSPACE if
- * NULL or smaller.  Nothing in it needs to start at zero.  The function is
- * host-only and gives a negative PESTI_ERR_* for bad arguments. */
+ * none needed), 16-byte aligned, for one call at a time.  It serves every call
+ * on that cache with as many rows and as long a bound or fewer: the size of the
+ * largest call is enough for a program's others.  PESTI_ERR_WORKSPACE if NULL or
+ * smaller than the call's own parts.  Nothing in it needs to start at zero.  The
+ * function is host-only and gives a negative PESTI_ERR_* for bad arguments. */
 int64_t pesti_attn_paged_workspace_bytes(const pesti_kv_cache* cache, int64_t rows, int64_t heads,
                                          int64_t max_length);
 int pesti_attn_paged(const pesti_kv_cache* cache, const pesti_kv_table* table, int64_t layer,
