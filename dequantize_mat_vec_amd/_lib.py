@@ -669,8 +669,9 @@ def _rows(dev, obj, rows, width, stride, size, what, dtype):
         inner *= n
     if stride is None:
         stride = strides[0] if len(shape) > 1 and shape[0] > 1 else width
-    # values from the first row to the last one's end, within the tensor's memory
-    if rows > 0 and (rows - 1) * stride + width > obj.untyped_storage().nbytes() // size - obj.storage_offset():
+    # values from the first row to the last one's end, within the tensor (whose memory may go on behind them)
+    held = 1 + sum((n - 1) * s for n, s in zip(shape, strides)) if min(shape, default=1) > 0 else 0
+    if rows > 0 and (rows - 1) * stride + width > min(held, obj.untyped_storage().nbytes() // size - obj.storage_offset()):
         raise ValueError(f"{what}: {rows} rows of {width} values, {stride} apart, do not fit in its memory")
     return obj.data_ptr(), stride
 

@@ -49,6 +49,14 @@ PyObject* sized(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return PyObject_Vectorcall(slow_sized, a, n, nullptr);
 }
 
+// Values of a two-dimensional tensor from its first to its last, within its memory.
+int64_t values_held(const at::Tensor& t, int64_t size) {
+  if (t.size(0) == 0 || t.size(1) == 0) return 0;
+  const int64_t own = (t.size(0) - 1) * t.stride(0) + (t.size(1) - 1) * t.stride(1) + 1;
+  const int64_t memory = static_cast<int64_t>(t.storage().nbytes()) / size - t.storage_offset();
+  return own < memory ? own : memory;
+}
+
 // rows(dev, obj, rows, width, stride, size, what, dtype) -> (pointer, stride)
 PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n == 8 && PyLong_CheckExact(a[0]) && PyLong_CheckExact(a[2]) && PyLong_CheckExact(a[3]) &&
@@ -60,8 +68,7 @@ PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const long long most = 1LL << 40;
       if (!PyErr_Occurred() && size > 0 && count >= 0 && count < most && stride >= 0 && stride < most && width >= 0 &&
           width < most && count * (stride / 1024 + 1) < most) {
-        const long long held = static_cast<long long>(t->storage().nbytes()) / size - t->storage_offset();
-        if (count == 0 || (count - 1) * stride + width <= held)
+        if (count == 0 || (count - 1) * stride + width <= values_held(*t, size))
           return Py_BuildValue("(NL)", PyLong_FromVoidPtr(t->data_ptr()), stride);
       }
       PyErr_Clear();
@@ -162,8 +169,7 @@ struct Reader {
     if (!f32 && t->scalar_type() != at::kHalf) fail();
     *format = f32 ? PESTI_FMT_F32 : PESTI_FMT_F16;
     if (*stride < 0) *stride = t->size(0) > 1 ? t->stride(0) : width;
-    const int64_t held = static_cast<int64_t>(t->storage().nbytes()) / (f32 ? 4 : 2) - t->storage_offset();
-    if (*stride < 0 || *stride > int64_t{1} << 31 || (count > 0 && (count - 1) * *stride + width > held)) fail();
+    if (*stride < 0 || *stride > int64_t{1} << 31 || (count > 0 && (count - 1) * *stride + width > values_held(*t, f32 ? 4 : 2))) fail();
     return t->data_ptr();
   }
   // A workspace and its size (None: the tensor's).
