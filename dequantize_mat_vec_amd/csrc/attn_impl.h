@@ -528,14 +528,22 @@ void attn_kernel(AttnArgs p) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = mine >> j & 1 ? x[j] : -INFINITY;
         }
-        const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-        now = fmaxf(most[n], column_max(top));
-        const float base = now == -INFINITY ? 0.f : now - kLift;
+        const float here = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        now = fmaxf(most[n], column_max(here));
+        const float top = now == -INFINITY ? 0.f : now, base = top - kLift;
         add = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           e[j] = __builtin_amdgcn_exp2f(x[j] - base);
           add += e[j];
+        }
+        if (!I8 && __any(__builtin_fabsf(base) >= 0x1p24f)) {   // no number may lie kLift below the maximum
+          add = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            e[j] = __builtin_amdgcn_exp2f(x[j] - top) * 0x1p14f;
+            add += e[j];
+          }
         }
       };
       weigh();
