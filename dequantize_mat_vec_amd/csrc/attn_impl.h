@@ -709,7 +709,9 @@ namespace pesti_attn {
 // Head tiles of 8 that a workgroup takes: two where a KV head has more than 8
 // query heads and the registers leave three wavefronts on a SIMD (16 rows up to
 // 2000, 16 query heads to a KV head of 128, where they leave one: 22.6 us with
-// one tile, 24.7 with two).
+// one tile, 24.7 with two).  Blocks of more heads read K and V each for themselves:
+// 131071 tokens of 8 KV heads of 128 with 8, 16 and 32 query heads to each 102, 153
+// and 299 us (538, 1075 and 2149 MB from memory).
 inline int head_tiles(int64_t group, int64_t head_dim) { return group > 8 && head_dim <= 64 ? 2 : 1; }
 
 template <bool I8, int D, int NT, bool SMALL>
