@@ -27,8 +27,8 @@
 // tiles of its part of the sequence in turn.  Parts are joined by a second
 // kernel (attn_paged.hip) where a sequence has more than one.  Measured, with that:
 // 131071 tokens of 8 KV heads of 128 98 us in binary16 (5.5 TB/s), 57 in 8 bits; 97
-// tokens of 2 heads of 64 5.3, of which the launch is 2.0 and the rest the way from
-// one load to the next and some 800 instructions of a wavefront alone on its SIMD.
+// tokens of 2 heads of 64 5.2, of which the launch is 2.0 and the rest the way from
+// one load to the next and some 700 vector instructions of a wavefront alone on its SIMD.
 #pragma once
 
 #include <type_traits>

@@ -9,7 +9,7 @@
 // sequence, length and page: the values are asked for with the row's place, the page
 // with the length, and into 8 bits the exact rounding's cases are looked at only
 // where a residual says so (that call 7.1 us, 8.6 with them always; one row of each
-// of 64 sequences 2.9).  Counted over that call, the vector ALUs are busy for 61% of
+// of 64 sequences 2.9).  Counted over that call, the vector ALUs are busy for 60% of
 // the time in which a compute unit has wavefronts, and those wait for 64% of theirs.
 #include "i8_round.h"
 #include "kv_cache.h"
