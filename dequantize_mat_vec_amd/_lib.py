@@ -171,7 +171,7 @@ def _compiled():
         from . import _tensor_args
     except ImportError:
         return None
-    return _tensor_args if _tensor_args.torch == torch.__version__ else None
+    return _tensor_args if getattr(_tensor_args, "torch", None) == torch.__version__ else None   # (an earlier build's has none)
 
 
 def _bind_fast_args():
