@@ -561,7 +561,7 @@ def gemv_i4group_ops(ops, group, batch=1):
                                _sized(dev, x, 4 * batch * inf, f"op {i}: x", torch.float32),
                                _sized(dev, y, 4 * batch * out, f"op {i}: y", torch.float32),
                                _sized(dev, bias, 4 * out, f"op {i}: bias", torch.float32))
-    arr.made_for = (len(ops), group, batch)
+    arr.made_for, arr.device = (len(ops), group, batch), dev
     return arr
 
 
@@ -572,8 +572,11 @@ def pesti_gemv_group_i4group(ops, group, batch=1, stream=None):
     n, made_group, made_batch = getattr(arr, "made_for", (len(arr), group, batch))
     if made_group != group or made_batch < batch:
         raise ValueError(f"the ops were built for groups of {made_group} and batch {made_batch}, not {group} and {batch}")
+    _, dev, st = _place(stream)
+    if getattr(arr, "device", dev) != dev:
+        raise ValueError(f"the ops' tensors are on device {arr.device}, the current one is {dev}")
     return _check("pesti_gemv_group_i4group", load().pesti_gemv_group_i4group(
-        n, ctypes.cast(arr, ctypes.c_void_p), group, batch, _stream(stream)))
+        n, ctypes.cast(arr, ctypes.c_void_p), group, batch, st))
 
 
 def pesti_gemv_i4group_swiglu(out_features, in_features, group, gate_packed, gate_scales, gate_zeros, up_packed, up_scales,
