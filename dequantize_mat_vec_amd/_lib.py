@@ -550,7 +550,7 @@ def pesti_gemv_i4group(out_features, in_features, group, packed, scales, zeros, 
 
 def gemv_i4group_ops(ops, group, batch=1):
     """ctypes array of pesti_gemv_i4group_op from (out, in, packed, scales, zeros, x, y, bias) tuples whose pointer
-    fields are tensors, ints or None."""
+    fields are tensors, ints or None.  The array keeps the tensors alive."""
     torch, dev, _ = _place(0)
     arr = (GemvI4GroupOp * max(len(ops), 1))()
     for i, (out, inf, packed, scales, zeros, x, y, bias) in enumerate(ops):
@@ -561,7 +561,7 @@ def gemv_i4group_ops(ops, group, batch=1):
                                _sized(dev, x, 4 * batch * inf, f"op {i}: x", torch.float32),
                                _sized(dev, y, 4 * batch * out, f"op {i}: y", torch.float32),
                                _sized(dev, bias, 4 * out, f"op {i}: bias", torch.float32))
-    arr.made_for, arr.device = (len(ops), group, batch), dev
+    arr.made_for, arr.device, arr.tensors = (len(ops), group, batch), dev, [op[2:] for op in ops]
     return arr
 
 
