@@ -584,9 +584,11 @@ int pesti_cache_append(const pesti_kv_cache* cache, const pesti_kv_table* table,
  * [rows][heads][head_dim] in y_format (PESTI_FMT_F32 or PESTI_FMT_F16); q and
  * y 16-byte aligned, q_stride >= heads * head_dim and its bytes a multiple of
  * 16.  A row without tokens (length 0, or no valid page) is zeros, as is one
- * whose every score is -infinity; a NaN of q or K makes NaN of the heads that
- * it enters, a NaN or infinity of V NaN or infinities of its dimension (in 8
- * bits, where a row's scale holds it, of all), whatever its token weighs.
+ * whose every score is -infinity.  An infinity of K makes a score infinite (NaN
+ * where q's value is 0, or 2^-39 of the head's largest and less), a NaN of q or K
+ * makes NaN of the heads that it enters, a NaN or infinity of V NaN or infinities
+ * of its dimension (in 8 bits, where a row's scale holds it, of all), whatever its
+ * token weighs.
  *
  * Scores, maximum, sum and result are float32.  q times scale and the softmax's
  * weights enter the matrix cores in two binary16 parts each (22 bits), K and V
